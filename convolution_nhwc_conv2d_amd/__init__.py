@@ -9,6 +9,9 @@ this import fails, and every library error raises :class:`CnhwcError`.
     conv3d(x, w, stride, padding, dilation, *, algo, inner_algo, ws_limit, ...)
     plan2d(...) / plan3d(...) -> Plan      (algorithm selection only; no GPU needed)
 
+The sequence operators (layer norm, the short causal convolution, the selective
+state space scan, forward and backward) are in ``sequence.py`` and re-exported here.
+
 Layouts: x [N,H,W,C] / [N,D,H,W,C]; w [O,KH,KW,C] / [O,KD,KH,KW,C];
 y [N,OH,OW,O] / [N,OD,OH,OW,O]; dtype float32, float16 or bfloat16 (x, w, y
 share it).
@@ -469,3 +472,10 @@ def direct_flops(x_shape, w_shape, plan):
     for v in w_shape[1:]:
         k *= v
     return 2 * x_shape[0] * plan.out_d * plan.out_h * plan.out_w * o * k
+
+
+from .sequence import (  # noqa: E402,F401  (uses the loaded library and the helpers above)
+    SEQ_EXPORTED, ConvGrads, ScanGrads, causal_conv1d, causal_conv1d_backward,
+    causal_conv1d_backward_workspace_bytes, causal_conv1d_step, layer_norm, layer_norm_backward,
+    layer_norm_backward_workspace_bytes, selective_scan, selective_scan_backward, selective_scan_step,
+    selective_scan_workspace_bytes)

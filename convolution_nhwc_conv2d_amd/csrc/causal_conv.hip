@@ -1,0 +1,549 @@
+// Short causal (depthwise) convolution, forward, backward and single tokens,
+// for gfx950.
+//
+// With X = K-1 rows of state followed by the valid rows of x:
+//   pre[t,c] = bias[c] + sum_k w[c,k] X[t+k,c],  y = act(pre)
+// and backward, with dpre = dy act'(pre) (0 outside the valid positions):
+//   dX[j,c] = sum_k w[c,k] dpre[j-k,c],  dw[c,k] = sum_t dpre[t,c] X[t+k,c],
+//   dbias[c] = sum_t dpre[t,c];
+// the first K-1 rows of dX are the state's gradient, the others x's, and the
+// gradient of the state that the forward pass left is added to the last K-1.
+//
+// A few operations per element, so memory is the bound: a thread owns 16 bytes
+// of channels over a run of positions and slides a register window along it,
+// so each row is loaded once per run (plus the K-1 rows before it, which the
+// neighbouring run has just brought into the cache).  The weights stay in
+// registers.  The backward pass recomputes pre from x instead of reading a
+// saved copy, sums dw and dbias in registers over the run, adds the runs of a
+// workgroup through LDS, and leaves one row of partial sums per workgroup to a
+// second kernel, which adds them in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+
+#include "internal.hpp"
+#include "seq_common.hpp"
+#include "seq_host.hpp"
+
+namespace cnhwc {
+namespace seq {
+namespace {
+
+struct ConvGeo {
+  int32_t l, c, act;
+  int32_t vecs;      // channel vectors
+  int32_t run;       // positions per thread, a multiple of kBatch
+  int64_t runs;      // runs per sequence (forward), workgroups per sequence (backward)
+  int64_t xs[2], dys[2];
+};
+
+constexpr int kBatch = 4;  // rows loaded together
+
+// w[c0..c0+V)[K] and bias as floats.
+template <int DT, int V, int K>
+struct Taps {
+  float w[V][K], b[V];
+  __device__ __forceinline__ void load(const Elem<DT>* __restrict__ wp, const Elem<DT>* __restrict__ bp, int64_t c0) {
+    if constexpr (V == 1) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) w[0][k] = to_f<DT>(wp[c0 * K + k]);
+      b[0] = bp ? to_f<DT>(bp[c0]) : 0.0f;
+    } else {
+      Pack<DT, V> p[K];  // K vectors hold the V * K weights
+#pragma unroll
+      for (int i = 0; i < K; ++i) p[i] = load_pack<DT, V>(wp + c0 * K + i * V);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[v][k] = to_f<DT>(p[(v * K + k) / V].e[(v * K + k) % V]);
+      const Pack<DT, V> pb = bp ? load_pack<DT, V>(bp + c0) : Pack<DT, V>{};
+#pragma unroll
+      for (int v = 0; v < V; ++v) b[v] = to_f<DT>(pb.e[v]);
+    }
+  }
+};
+
+// Row r of a sequence: x for 0 <= r < len, the state before it, zeros elsewhere.
+template <int DT, int V, int K>
+__device__ __forceinline__ Pack<DT, V> load_row(const Elem<DT>* __restrict__ x, const Elem<DT>* __restrict__ state,
+                                                int64_t xs1, int32_t c, int64_t r, int32_t len) {
+  if (r >= 0 && r < len) return load_pack<DT, V>(x + r * xs1);
+  if (r < 0 && r >= -(K - 1) && state) return load_pack<DT, V>(state + (r + K - 1) * int64_t(c));
+  return Pack<DT, V>{};
+}
+
+template <int DT, int V, int K>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(
+    const Elem<DT>* __restrict__ x, const Elem<DT>* __restrict__ wp, const Elem<DT>* __restrict__ bp,
+    const Elem<DT>* __restrict__ state, const int32_t* __restrict__ lengths, Elem<DT>* __restrict__ y,
+    Elem<DT>* __restrict__ state_out, ConvGeo g, int64_t total) {
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+    const int64_t run_id = id / g.vecs;
+    const int64_t c0 = (id - run_id * g.vecs) * V;
+    const int64_t n = run_id / g.runs;
+    const int32_t t0 = int32_t((run_id - n * g.runs) * g.run);
+    const int32_t len = valid_len(lengths, n, g.l);
+    const Elem<DT>* xn = x + n * g.xs[0] + c0;
+    const Elem<DT>* sn = state ? state + n * (K - 1) * int64_t(g.c) + c0 : nullptr;
+    Elem<DT>* yn = y + n * g.l * int64_t(g.c) + c0;
+    Taps<DT, V, K> tap;
+    tap.load(wp, bp, c0);
+    float win[K][V];  // the K newest rows, win[K-1] the newest
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+      const Pack<DT, V> p = load_row<DT, V, K>(xn, sn, g.xs[1], g.c, int64_t(t0) - (K - 1) + k, len);
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[k + 1][v] = to_f<DT>(p.e[v]);
+    }
+    const int32_t end = t0 + g.run < g.l ? t0 + g.run : g.l;
+    for (int32_t tb = t0; tb < end; tb += kBatch) {
+      Pack<DT, V> p[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) p[i] = load_row<DT, V, K>(xn, sn, g.xs[1], g.c, tb + i, len);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int32_t t = tb + i;
+#pragma unroll
+        for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+          for (int v = 0; v < V; ++v) win[k][v] = win[k + 1][v];
+#pragma unroll
+        for (int v = 0; v < V; ++v) win[K - 1][v] = to_f<DT>(p[i].e[v]);
+        if (t >= end) continue;
+        Pack<DT, V> o;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float a = tap.b[v];
+#pragma unroll
+          for (int k = 0; k < K; ++k) a = __builtin_fmaf(tap.w[v][k], win[k][v], a);
+          if (g.act == CNHWC_ACT_SILU) a *= sigmoid(a);
+          o.e[v] = t < len ? from_f<DT>(a) : Elem<DT>(0);
+        }
+        store_pack<DT, V>(yn + t * int64_t(g.c), o);
+      }
+    }
+    if (K > 1 && state_out && t0 == 0) {
+      Elem<DT>* so = state_out + n * (K - 1) * int64_t(g.c) + c0;
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        const int64_t r = int64_t(len) + j - (K - 1);
+        store_pack<DT, V>(so + j * int64_t(g.c), load_row<DT, V, K>(xn, sn, g.xs[1], g.c, r, len));
+      }
+    }
+  }
+}
+
+// One token per sequence; state_out may be state.
+template <int DT, int V, int K>
+__global__ __launch_bounds__(256) void conv_step_kernel(
+    const Elem<DT>* __restrict__ x, const Elem<DT>* state, const Elem<DT>* __restrict__ wp,
+    const Elem<DT>* __restrict__ bp, Elem<DT>* __restrict__ y, Elem<DT>* state_out, ConvGeo g, int64_t total) {
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+    const int64_t n = id / g.vecs;
+    const int64_t c0 = (id - n * g.vecs) * V;
+    const int64_t so = n * (K - 1) * int64_t(g.c) + c0;
+    Taps<DT, V, K> tap;
+    tap.load(wp, bp, c0);
+    Pack<DT, V> row[K];
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) row[k] = load_pack<DT, V>(state + so + k * int64_t(g.c));
+    row[K - 1] = load_pack<DT, V>(x + n * g.xs[0] + c0);
+    Pack<DT, V> o;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float a = tap.b[v];
+#pragma unroll
+      for (int k = 0; k < K; ++k) a = __builtin_fmaf(tap.w[v][k], to_f<DT>(row[k].e[v]), a);
+      if (g.act == CNHWC_ACT_SILU) a *= sigmoid(a);
+      o.e[v] = from_f<DT>(a);
+    }
+    store_pack<DT, V>(y + n * int64_t(g.c) + c0, o);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) store_pack<DT, V>(state_out + so + k * int64_t(g.c), row[k + 1]);
+  }
+}
+
+// A workgroup: 32 channel vectors by 8 runs of positions of one sequence, over
+// the L + K - 1 rows j of dX.  part: per workgroup column of 32 vectors and per
+// (sequence, workgroup along it) one row [C*K | C] of dw and dbias sums.
+constexpr int kLanes = 32, kRunsPerBlock = 8;
+
+template <int DT, int V, int K>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(
+    const Elem<DT>* __restrict__ dy, const Elem<DT>* __restrict__ dfin, const Elem<DT>* __restrict__ x,
+    const Elem<DT>* __restrict__ wp, const Elem<DT>* __restrict__ bp, const Elem<DT>* __restrict__ state,
+    const int32_t* __restrict__ lengths, Elem<DT>* __restrict__ dx, Elem<DT>* __restrict__ dstate,
+    float* __restrict__ part, ConvGeo g, int64_t col_blocks) {
+  const int64_t row_id = blockIdx.x / col_blocks;
+  const int32_t vec = int32_t(blockIdx.x - row_id * col_blocks) * kLanes + int32_t(threadIdx.x & (kLanes - 1));
+  const int64_t n = row_id / g.runs;
+  const int64_t j0 = ((row_id - n * g.runs) * kRunsPerBlock + threadIdx.x / kLanes) * g.run;
+  const int64_t rows = int64_t(g.l) + K - 1;
+  const int32_t len = valid_len(lengths, n, g.l);
+  const bool live = vec < g.vecs && j0 < rows;
+  const int64_t c0 = int64_t(vec < g.vecs ? vec : 0) * V;
+  float dw[V][K], db[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    db[v] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) dw[v][k] = 0.0f;
+  }
+  if (live) {
+    const Elem<DT>* xn = x + n * g.xs[0] + c0;
+    const Elem<DT>* gn = dy + n * g.dys[0] + c0;
+    const int64_t so = n * (K - 1) * int64_t(g.c) + c0;
+    const Elem<DT>* sn = state ? state + so : nullptr;
+    Elem<DT>* dxn = dx + n * g.l * int64_t(g.c) + c0;
+    Taps<DT, V, K> tap;
+    tap.load(wp, bp, c0);
+    float win[K][V], dpre[K][V];  // X rows t..t+K-1 and dpre of t-K+1..t
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v) dpre[k][v] = win[k][v] = 0.0f;
+    // rows before the first position whose dpre this run needs, t = j0 - (K-1)
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) {
+      const Pack<DT, V> p = load_row<DT, V, K>(xn, sn, g.xs[1], g.c, j0 - 2 * (K - 1) + k, len);
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[k + 1][v] = to_f<DT>(p.e[v]);
+    }
+    const int64_t end = j0 + g.run < rows ? j0 + g.run : rows;
+    for (int64_t tb = j0 - (K - 1); tb < end; tb += kBatch) {
+      Pack<DT, V> px[kBatch], pg[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t t = tb + i;
+        px[i] = load_row<DT, V, K>(xn, sn, g.xs[1], g.c, t, len);
+        pg[i] = t >= 0 && t < len ? load_pack<DT, V>(gn + t * g.dys[1]) : Pack<DT, V>{};
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t t = tb + i;
+        if (t >= end) break;
+        const bool valid = t >= 0 && t < len, own = t >= j0;
+        const int64_t fin = t - len;  // row of dfin that belongs to dX row t
+        Pack<DT, V> pf{};
+        if (own && dfin && fin >= 0 && fin < K - 1) pf = load_pack<DT, V>(dfin + so + fin * int64_t(g.c));
+        Pack<DT, V> o;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) {
+            win[k][v] = win[k + 1][v];
+            dpre[k][v] = dpre[k + 1][v];
+          }
+          win[K - 1][v] = to_f<DT>(px[i].e[v]);
+          float d = to_f<DT>(pg[i].e[v]);
+          if (g.act == CNHWC_ACT_SILU) {
+            float a = tap.b[v];
+#pragma unroll
+            for (int k = 0; k < K; ++k) a = __builtin_fmaf(tap.w[v][k], win[k][v], a);
+            const float s = sigmoid(a);
+            d *= s * __builtin_fmaf(a, 1.0f - s, 1.0f);
+          }
+          dpre[K - 1][v] = d = valid ? d : 0.0f;
+          if (own) {
+            db[v] += d;
+            float r = to_f<DT>(pf.e[v]);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              // past the valid rows X may hold anything: d is 0 there and so is the term
+              dw[v][k] = valid ? __builtin_fmaf(d, win[k][v], dw[v][k]) : dw[v][k];
+              r = __builtin_fmaf(tap.w[v][k], dpre[K - 1 - k][v], r);
+            }
+            o.e[v] = from_f<DT>(r);
+          }
+        }
+        if (!own) continue;
+        if (t < K - 1) {
+          if (dstate) store_pack<DT, V>(dstate + so + t * int64_t(g.c), o);
+        } else {
+          store_pack<DT, V>(dxn + (t - (K - 1)) * int64_t(g.c), o);
+        }
+      }
+    }
+  }
+  // the two runs of a wavefront, then the wavefronts through LDS in order
+  __shared__ float sum[4][kLanes * V * (K + 1)];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float r = add_halves(dw[v][k]);
+      if (lane < kLanes) sum[wave][(lane * V + v) * K + k] = r;
+    }
+    const float r = add_halves(db[v]);
+    if (lane < kLanes) sum[wave][kLanes * V * K + lane * V + v] = r;
+  }
+  __syncthreads();
+  float* pr = part + row_id * (int64_t(g.c) * (K + 1));
+  const int64_t cb = int64_t(blockIdx.x - row_id * col_blocks) * kLanes * V;
+  for (int i = threadIdx.x; i < kLanes * V * (K + 1); i += 256) {
+    const float r = sum[0][i] + sum[1][i] + sum[2][i] + sum[3][i];
+    if (i < kLanes * V * K) {
+      if (cb * K + i < int64_t(g.c) * K) pr[cb * K + i] = r;
+    } else if (cb + (i - kLanes * V * K) < g.c) {
+      pr[int64_t(g.c) * K + cb + (i - kLanes * V * K)] = r;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+ConvGeo geo_of(const cnhwc_causal_conv_desc_t& d, int ve) {
+  ConvGeo g{};
+  g.l = int32_t(d.l);
+  g.c = int32_t(d.c);
+  g.act = d.activation;
+  g.vecs = int32_t(d.c / ve);
+  for (int i = 0; i < 2; ++i) {
+    g.xs[i] = d.x_stride[i];
+    g.dys[i] = d.dy_stride[i];
+  }
+  return g;
+}
+
+// 16-byte vectors of rows at these strides.
+bool vectors(const cnhwc_causal_conv_desc_t& d, const int64_t (&s)[2], const void* p) {
+  const int64_t v = 16 / int64_t(dtype_size(d.dtype));
+  return aligned(p, 16) && d.c % v == 0 && (d.n == 1 || s[0] % v == 0) && (d.l == 1 || s[1] % v == 0);
+}
+
+// Positions per thread: long runs load fewer rows twice, short ones fill the
+// device (about 512 threads for each of the 256 compute units).
+int32_t pick_run(int64_t work, int32_t most) {
+  int64_t run = work / (256 * 512);
+  run = run < kBatch ? kBatch : (run > most ? most : run);
+  return int32_t(ceil_div(run, kBatch) * kBatch);
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <typename F>
+void with_taps(int32_t k, F&& f) {
+  switch (k) {
+    case 1: f(Int<1>{}); break;
+    case 2: f(Int<2>{}); break;
+    case 3: f(Int<3>{}); break;
+    case 4: f(Int<4>{}); break;
+    case 5: f(Int<5>{}); break;
+    case 6: f(Int<6>{}); break;
+    case 7: f(Int<7>{}); break;
+    default: f(Int<8>{}); break;
+  }
+}
+
+template <int DT, int V>
+hipError_t conv_fwd_t(const cnhwc_causal_conv_desc_t& d, const void* x, const void* w, const void* b,
+                      const void* state, const int32_t* lengths, void* y, void* state_out, hipStream_t st) {
+  using E = Elem<DT>;
+  ConvGeo g = geo_of(d, V);
+  g.run = pick_run(d.n * d.l * g.vecs, 32);
+  g.runs = ceil_div(d.l, g.run);
+  const int64_t total = d.n * g.runs * g.vecs;
+  with_taps(d.k, [&](auto k) {
+    hipLaunchKernelGGL((conv_fwd_kernel<DT, V, decltype(k)::value>), grid_of(ceil_div(total, 256)), dim3(256),
+                       0, st, static_cast<const E*>(x), static_cast<const E*>(w), static_cast<const E*>(b),
+                       static_cast<const E*>(state), lengths, static_cast<E*>(y), static_cast<E*>(state_out), g,
+                       total);
+  });
+  return hipGetLastError();
+}
+
+template <int DT, int V>
+hipError_t conv_step_t(const cnhwc_causal_conv_desc_t& d, const void* x, const void* state, const void* w,
+                       const void* b, void* y, void* state_out, hipStream_t st) {
+  using E = Elem<DT>;
+  const ConvGeo g = geo_of(d, V);
+  const int64_t total = d.n * g.vecs;
+  with_taps(d.k, [&](auto k) {
+    hipLaunchKernelGGL((conv_step_kernel<DT, V, decltype(k)::value>), grid_of(ceil_div(total, 256)), dim3(256),
+                       0, st, static_cast<const E*>(x), static_cast<const E*>(state), static_cast<const E*>(w),
+                       static_cast<const E*>(b), static_cast<E*>(y), static_cast<E*>(state_out), g, total);
+  });
+  return hipGetLastError();
+}
+
+// Run length and workgroups per sequence of the backward pass, from the shape only.
+void bwd_runs(const cnhwc_causal_conv_desc_t& d, int64_t ve, int32_t* run, int64_t* blocks) {
+  const int64_t rows = d.l + d.k - 1;
+  *run = pick_run(d.n * rows * ceil_div(d.c, ve), 64);
+  *blocks = ceil_div(rows, int64_t(*run) * kRunsPerBlock);
+}
+
+template <int DT, int V>
+hipError_t conv_bwd_t(const cnhwc_causal_conv_desc_t& d, const void* dy, const void* dfin, const void* x,
+                      const void* w, const void* b, const void* state, const int32_t* lengths, void* dx, void* dw,
+                      void* db, void* dstate, float* part, hipStream_t st) {
+  using E = Elem<DT>;
+  ConvGeo g = geo_of(d, V);
+  bwd_runs(d, V, &g.run, &g.runs);
+  const int64_t cols = ceil_div(g.vecs, kLanes), parts = d.n * g.runs;
+  with_taps(d.k, [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    if constexpr (V == 1 || K <= 4)  // more taps than four hold too many registers with vectors
+      hipLaunchKernelGGL((conv_bwd_kernel<DT, V, K>), dim3(unsigned(cols * parts)), dim3(256), 0, st,
+                         static_cast<const E*>(dy), static_cast<const E*>(dfin), static_cast<const E*>(x),
+                         static_cast<const E*>(w), static_cast<const E*>(b), static_cast<const E*>(state), lengths,
+                         static_cast<E*>(dx), static_cast<E*>(dstate), part, g, cols);
+  });
+  sum_parts<DT>(part, parts, SumOut{{dw, db, nullptr}, {d.c * d.k, d.c, 0}}, false, st);
+  return hipGetLastError();
+}
+
+cnhwc_status_t check_desc(const cnhwc_causal_conv_desc_t* d, bool bwd) {
+  if (!d || !dtype_ok(d->dtype) || d->reserved != 0) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (d->activation != CNHWC_ACT_NONE && d->activation != CNHWC_ACT_SILU) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (!extent_ok(d->n) || !extent_ok(d->l) || !extent_ok(d->c) || d->k < 1) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (!strides_ok(d->n, d->l, d->c, d->x_stride)) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (bwd && !strides_ok(d->n, d->l, d->c, d->dy_stride)) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (d->k > CNHWC_CAUSAL_CONV_MAX_K) return CNHWC_ERR_UNSUPPORTED;
+  // positions fit 32 bits with the run's overhang; the grids of the backward
+  // pass (at least 16384 elements a workgroup) and of its reduction stay in range
+  if (d->l > INT_MAX - 1024 || d->c > (1ll << 23) || !dense_ok(d->n, d->l + d->k, d->c) ||
+      d->n * (d->l + d->k) * d->c > (1ll << 37))
+    return CNHWC_ERR_UNSUPPORTED;
+  return CNHWC_OK;
+}
+
+// The K-1 state rows of every sequence, in bytes.
+uint64_t state_bytes(const cnhwc_causal_conv_desc_t& d) {
+  return uint64_t(d.n) * (d.k - 1) * d.c * dtype_size(d.dtype);
+}
+
+}  // namespace
+}  // namespace seq
+}  // namespace cnhwc
+
+using namespace cnhwc;
+using namespace cnhwc::seq;
+
+// With one tap there is no state: its pointers are not looked at.
+extern "C" cnhwc_status_t cnhwc_causal_conv_fwd(const cnhwc_causal_conv_desc_t* desc, const void* x, const void* w,
+                                                const void* bias, const void* state, const int32_t* lengths,
+                                                void* y, void* state_out, void* hip_stream) {
+  const cnhwc_status_t st = check_desc(desc, false);
+  if (st != CNHWC_OK) return st;
+  const cnhwc_causal_conv_desc_t& d = *desc;
+  if (d.k == 1) state = nullptr, state_out = nullptr;
+  const uint64_t es = dtype_size(d.dtype);
+  Buffers bf;
+  bf.in(x, span(d.n, d.l, d.c, d.x_stride) * es, es, true);
+  bf.in(w, uint64_t(d.c) * d.k * es, es, true);
+  bf.in(bias, d.c * es, es, false);
+  bf.in(state, state_bytes(d), es, false);
+  bf.in(lengths, d.n * 4, 4, false);
+  bf.out(y, uint64_t(d.n) * d.l * d.c * es, es, true);
+  bf.out(state_out, state_bytes(d), es, false);
+  if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
+  const bool vec = vectors(d, d.x_stride, x) && aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) &&
+                   aligned(y, 16) && aligned(state_out, 16);
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  hipError_t e;
+  if (d.dtype == CNHWC_F32)
+    e = vec ? conv_fwd_t<CNHWC_F32, 4>(d, x, w, bias, state, lengths, y, state_out, s)
+            : conv_fwd_t<CNHWC_F32, 1>(d, x, w, bias, state, lengths, y, state_out, s);
+  else if (d.dtype == CNHWC_F16)
+    e = vec ? conv_fwd_t<CNHWC_F16, 8>(d, x, w, bias, state, lengths, y, state_out, s)
+            : conv_fwd_t<CNHWC_F16, 1>(d, x, w, bias, state, lengths, y, state_out, s);
+  else
+    e = vec ? conv_fwd_t<CNHWC_BF16, 8>(d, x, w, bias, state, lengths, y, state_out, s)
+            : conv_fwd_t<CNHWC_BF16, 1>(d, x, w, bias, state, lengths, y, state_out, s);
+  return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
+}
+
+extern "C" cnhwc_status_t cnhwc_causal_conv_bwd_workspace(const cnhwc_causal_conv_desc_t* desc, uint64_t* bytes) {
+  const cnhwc_status_t st = check_desc(desc, true);
+  if (st != CNHWC_OK) return st;
+  if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
+  // the vector and the element form alike: which one runs also depends on the pointers
+  uint64_t most = 0;
+  for (int64_t ve : {int64_t(1), 16 / int64_t(dtype_size(desc->dtype))}) {
+    int32_t run;
+    int64_t blocks;
+    bwd_runs(*desc, ve, &run, &blocks);
+    const uint64_t b = uint64_t(desc->n) * blocks * (uint64_t(desc->c) * (desc->k + 1)) * 4;
+    most = b > most ? b : most;
+  }
+  *bytes = most;
+  return CNHWC_OK;
+}
+
+extern "C" cnhwc_status_t cnhwc_causal_conv_bwd(const cnhwc_causal_conv_desc_t* desc, const void* dy,
+                                                const void* dstate_out, const void* x, const void* w,
+                                                const void* bias, const void* state, const int32_t* lengths,
+                                                void* dx, void* dw, void* dbias, void* dstate, void* workspace,
+                                                uint64_t workspace_bytes, void* hip_stream) {
+  uint64_t need = 0;
+  const cnhwc_status_t st = cnhwc_causal_conv_bwd_workspace(desc, &need);
+  if (st != CNHWC_OK) return st;
+  const cnhwc_causal_conv_desc_t& d = *desc;
+  if (d.k == 1) state = nullptr, dstate_out = nullptr, dstate = nullptr;
+  if ((bias == nullptr) != (dbias == nullptr)) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < need) return CNHWC_ERR_WORKSPACE_TOO_SMALL;
+  const uint64_t es = dtype_size(d.dtype);
+  Buffers bf;
+  bf.in(dy, span(d.n, d.l, d.c, d.dy_stride) * es, es, true);
+  bf.in(dstate_out, state_bytes(d), es, false);
+  bf.in(x, span(d.n, d.l, d.c, d.x_stride) * es, es, true);
+  bf.in(w, uint64_t(d.c) * d.k * es, es, true);
+  bf.in(bias, d.c * es, es, false);
+  bf.in(state, state_bytes(d), es, false);
+  bf.in(lengths, d.n * 4, 4, false);
+  bf.out(dx, uint64_t(d.n) * d.l * d.c * es, es, true);
+  bf.out(dw, uint64_t(d.c) * d.k * es, es, true);
+  bf.out(dbias, d.c * es, es, false);
+  bf.out(dstate, state_bytes(d), es, false);
+  bf.out(workspace, need, 16, true);
+  if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
+  const bool vec = d.k <= 4 && vectors(d, d.x_stride, x) && vectors(d, d.dy_stride, dy) && aligned(dstate_out, 16) &&
+                   aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) && aligned(dx, 16) && aligned(dstate, 16);
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  float* part = static_cast<float*>(workspace);
+  hipError_t e;
+  auto run = [&](auto dt, auto v) {
+    return conv_bwd_t<decltype(dt)::value, decltype(v)::value>(d, dy, dstate_out, x, w, bias, state, lengths, dx, dw,
+                                                               dbias, dstate, part, s);
+  };
+  if (d.dtype == CNHWC_F32) e = vec ? run(Int<CNHWC_F32>{}, Int<4>{}) : run(Int<CNHWC_F32>{}, Int<1>{});
+  else if (d.dtype == CNHWC_F16) e = vec ? run(Int<CNHWC_F16>{}, Int<8>{}) : run(Int<CNHWC_F16>{}, Int<1>{});
+  else e = vec ? run(Int<CNHWC_BF16>{}, Int<8>{}) : run(Int<CNHWC_BF16>{}, Int<1>{});
+  return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
+}
+
+extern "C" cnhwc_status_t cnhwc_causal_conv_step(const cnhwc_causal_conv_desc_t* desc, const void* x,
+                                                 const void* state, const void* w, const void* bias, void* y,
+                                                 void* state_out, void* hip_stream) {
+  const cnhwc_status_t st = check_desc(desc, false);
+  if (st != CNHWC_OK) return st;
+  const cnhwc_causal_conv_desc_t& d = *desc;
+  if (d.l != 1) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (d.k == 1) state = nullptr, state_out = nullptr;
+  const uint64_t es = dtype_size(d.dtype);
+  Buffers bf;
+  bf.in(x, span(d.n, d.l, d.c, d.x_stride) * es, es, true);
+  if (state != state_out) bf.in(state, state_bytes(d), es, true);
+  bf.in(w, uint64_t(d.c) * d.k * es, es, true);
+  bf.in(bias, d.c * es, es, false);
+  bf.out(y, uint64_t(d.n) * d.c * es, es, true);
+  bf.out(state_out, state_bytes(d), es, d.k > 1);
+  if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
+  const bool vec = vectors(d, d.x_stride, x) && aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) &&
+                   aligned(y, 16) && aligned(state_out, 16);
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  hipError_t e;
+  if (d.dtype == CNHWC_F32)
+    e = vec ? conv_step_t<CNHWC_F32, 4>(d, x, state, w, bias, y, state_out, s)
+            : conv_step_t<CNHWC_F32, 1>(d, x, state, w, bias, y, state_out, s);
+  else if (d.dtype == CNHWC_F16)
+    e = vec ? conv_step_t<CNHWC_F16, 8>(d, x, state, w, bias, y, state_out, s)
+            : conv_step_t<CNHWC_F16, 1>(d, x, state, w, bias, y, state_out, s);
+  else
+    e = vec ? conv_step_t<CNHWC_BF16, 8>(d, x, state, w, bias, y, state_out, s)
+            : conv_step_t<CNHWC_BF16, 1>(d, x, state, w, bias, y, state_out, s);
+  return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
+}

@@ -1,0 +1,1032 @@
+// Selective state space scan, forward, backward and single tokens, for gfx950.
+//
+//   D[t,d] = softplus(delta[t,d] + delta_bias[d])
+//   h[t,d,s] = e[t,d,s] h[t-1,d,s] + D[t,d] u[t,d] b[t,s],  e = exp(D[t,d] a[d,s])
+//   y[t,d] = (sum_s c[t,s] h[t,d,s] + skip[d] u[t,d]) silu(gate[t,d])
+//
+// Every channel and state has its own decay, so no product over t or s has the
+// form of a matrix product: the work is vector instructions, and of those the
+// exponential (a quarter-rate instruction) costs as much as the other four.
+//
+// A wavefront holds 64 / SL groups of SL lanes; a group holds four channels and
+// SL * SPL states, each lane SPL states of all four channels.  So per position a
+// lane reads b and c for its own states once for four channels, the sum over
+// the states is log2(SL) lane permutations for every SPL terms, and what
+// belongs to a channel alone (softplus, gate, loads and stores) is done once
+// by the four lanes of a quad, one channel each, and handed round by quad
+// permutations.  b and c come through LDS, converted once per workgroup.
+//
+// Long sequences are cut into chunks.  One kernel runs each chunk from a zero
+// state and leaves the chunk's end state and sum of D; a second one, along the
+// chunks, turns these into the state that enters every chunk (a chunk scales
+// what enters it by exp(a sum D)); the last runs each chunk from there.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+
+#include "internal.hpp"
+#include "seq_common.hpp"
+#include "seq_host.hpp"
+
+namespace cnhwc {
+namespace seq {
+namespace {
+
+constexpr int kTile = 8;    // positions whose loads are issued together
+constexpr int kWaves = 4;   // most wavefronts of a workgroup
+constexpr float kLog2e = 1.44269504f;
+constexpr float kLn2 = 0.693147181f;
+
+struct ScanGeo {
+  int32_t l, d, s, softplus;
+  int32_t chunk;         // positions per chunk, a multiple of kTile
+  int32_t chunks;        // per sequence
+  int32_t col_blocks;    // workgroups along the channels
+  int64_t us[2], ds[2], bs[2], cs[2], gs[2], ys[2];
+};
+
+template <int DT>
+struct ScanIn {
+  const Elem<DT>* u;
+  const Elem<DT>* delta;
+  const float* a;
+  const Elem<DT>* b;
+  const Elem<DT>* c;
+  const float* skip;
+  const Elem<DT>* gate;
+  const float* delta_bias;
+  const float* state;
+  const int32_t* lengths;
+};
+
+// Where a thread stands: its group's four channels, its own channel of them,
+// its states.
+template <int SL, int SPL>
+struct Place {
+  static constexpr int kChannels = 64 / SL * 4;  // per wavefront
+  static constexpr int kStates = SL * SPL;       // per group; states past S are zero
+  int32_t dq, d, s0;
+  bool live;   // the own channel exists
+  bool first;  // this lane stores for its channel
+  __device__ __forceinline__ Place(int32_t wave_d0, int32_t d_all) {
+    const int lane = threadIdx.x & 63;
+    dq = wave_d0 + lane / SL * 4;
+    d = dq + (lane & 3);
+    s0 = lane % SL * SPL;
+    live = d < d_all;
+    first = lane % SL < 4 && live;
+  }
+};
+
+// The [D,S] values of a thread's four channels by SPL states; zero outside.
+template <int SL, int SPL>
+__device__ __forceinline__ void load_states(float (&h)[4][SPL], const float* __restrict__ p, const Place<SL, SPL>& at,
+                                            const ScanGeo& g) {
+  const bool whole = SPL == 4 && g.s == SL * SPL && aligned16(p);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t base = int64_t(at.dq + j) * g.s + at.s0;
+    if (whole) {
+      float4 v = make_float4(0, 0, 0, 0);
+      if (at.dq + j < g.d) v = *reinterpret_cast<const float4*>(p + base);
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < SPL; ++i) h[j][i] = f[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < SPL; ++i) h[j][i] = at.dq + j < g.d && at.s0 + i < g.s ? p[base + i] : 0.0f;
+    }
+  }
+}
+
+template <int SL, int SPL>
+__device__ __forceinline__ void store_states(const float (&h)[4][SPL], float* __restrict__ p, const Place<SL, SPL>& at,
+                                             const ScanGeo& g) {
+  const bool whole = SPL == 4 && g.s == SL * SPL && aligned16(p);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t base = int64_t(at.dq + j) * g.s + at.s0;
+    if (at.dq + j >= g.d) continue;
+    if (whole) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = h[j][i < SPL ? i : 0];
+      *reinterpret_cast<float4*>(p + base) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < SPL; ++i)
+        if (at.s0 + i < g.s) p[base + i] = h[j][i];
+    }
+  }
+}
+
+// One float of each lane of the quad, in all four.
+__device__ __forceinline__ void quad_all(float v, float (&out)[4]) {
+  out[0] = dpp<0 * kQuadBcast>(v);
+  out[1] = dpp<1 * kQuadBcast>(v);
+  out[2] = dpp<2 * kQuadBcast>(v);
+  out[3] = dpp<3 * kQuadBcast>(v);
+}
+
+// Of the four channels' sums over the group's lanes, the own channel's.
+template <int SL>
+__device__ __forceinline__ float own_sum(const float (&v)[4]) {
+  const int j = threadIdx.x & 3;
+  const float s0 = group_sum<SL>(v[0]), s1 = group_sum<SL>(v[1]);
+  const float s2 = group_sum<SL>(v[2]), s3 = group_sum<SL>(v[3]);
+  return j < 2 ? (j == 0 ? s0 : s1) : (j == 2 ? s2 : s3);
+}
+
+// b and c of a tile of positions in LDS as floats, zero past the valid
+// positions and past S.  stage() issues the loads, put() writes them.
+template <int DT, int NS>
+struct StagedBC {
+  static constexpr int kAll = kTile * 2 * NS;
+  static constexpr int kPer = kAll / 64;  // for a workgroup of one wavefront
+  Elem<DT> v[kPer];
+  __device__ __forceinline__ void stage(const Elem<DT>* __restrict__ b, const Elem<DT>* __restrict__ c,
+                                        const ScanGeo& g, int32_t t0, int32_t end) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = threadIdx.x + k * blockDim.x;
+      const int s = i % NS, which = i / NS % 2, t = t0 + i / (2 * NS);
+      v[k] = Elem<DT>(0);
+      if (i < kAll && s < g.s && t < end) v[k] = which ? c[t * g.cs[1] + s] : b[t * g.bs[1] + s];
+    }
+  }
+  __device__ __forceinline__ void put(float* lds) const {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = threadIdx.x + k * blockDim.x;
+      if (i < kAll) lds[i] = to_f<DT>(v[k]);
+    }
+  }
+};
+
+template <int SPL>
+__device__ __forceinline__ void lds_states(const float* p, float (&f)[SPL]) {
+  if constexpr (SPL == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) f[i] = p[i];
+  }
+}
+
+// Workgroup -> sequence, chunk, first channel of this wavefront.
+template <int SL, int SPL>
+__device__ __forceinline__ void locate(const ScanGeo& g, int64_t& n, int32_t& chunk, int32_t& wave_d0) {
+  const int64_t row = blockIdx.x / g.col_blocks;
+  const int32_t col = int32_t(blockIdx.x - row * g.col_blocks);
+  n = row / g.chunks;
+  chunk = int32_t(row - n * g.chunks);
+  wave_d0 = (col * int32_t(blockDim.x / 64) + int32_t(threadIdx.x >> 6)) * Place<SL, SPL>::kChannels;
+}
+
+// ---------------------------------------------------------------- forward
+
+// LOCAL: the chunk from a zero state; ends [n,chunk,D,S] and sums [n,chunk,D].
+// Otherwise the outputs, from the entering states `starts` ([n,chunk,D,S], or
+// the initial state where there is one chunk) and, with one chunk, state_out.
+template <int DT, int SL, int SPL, bool LOCAL>
+__global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g, Elem<DT>* __restrict__ y,
+                                                       float* __restrict__ states, float* __restrict__ sums,
+                                                       float* __restrict__ state_out) {
+  constexpr int NS = SL * SPL;
+  __shared__ __attribute__((aligned(16))) float bc[2][kTile * 2 * NS];
+  int64_t n;
+  int32_t chunk, wave_d0;
+  locate<SL, SPL>(g, n, chunk, wave_d0);
+  const Place<SL, SPL> at(wave_d0, g.d);
+  const int32_t len = valid_len(in.lengths, n, g.l);
+  const int32_t t_begin = chunk * g.chunk;
+  const int32_t t_end = t_begin + g.chunk < g.l ? t_begin + g.chunk : g.l;
+  const int32_t t_valid = t_end < len ? t_end : len;
+
+  float a2[4][SPL], h[4][SPL];
+  load_states<SL, SPL>(a2, in.a, at, g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, h[j][i] = 0.0f;
+  const int64_t ds = int64_t(g.d) * g.s;
+  if constexpr (!LOCAL) {
+    if (g.chunks > 1) load_states<SL, SPL>(h, states + (n * g.chunks + chunk) * ds, at, g);
+    else if (in.state) load_states<SL, SPL>(h, in.state + n * ds, at, g);
+  }
+  const float bias = in.delta_bias && at.live ? in.delta_bias[at.d] : 0.0f;
+  const float skip = !LOCAL && in.skip && at.live ? in.skip[at.d] : 0.0f;
+  const Elem<DT>* un = in.u + n * g.us[0] + at.d;
+  const Elem<DT>* dn = in.delta + n * g.ds[0] + at.d;
+  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] + at.d : nullptr;
+  const Elem<DT>* bn = in.b + n * g.bs[0];
+  const Elem<DT>* cn = in.c + n * g.cs[0];
+  Elem<DT>* yn = LOCAL ? nullptr : y + n * g.l * int64_t(g.d) + at.d;
+
+  Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile];
+  StagedBC<DT, NS> st;
+  auto fetch = [&](int32_t t0) {
+    st.stage(bn, cn, g, t0, t_valid);
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const bool ok = at.live && t0 + i < t_valid;
+      u_t[i] = ok ? un[(t0 + i) * g.us[1]] : Elem<DT>(0);
+      d_t[i] = ok ? dn[(t0 + i) * g.ds[1]] : Elem<DT>(0);
+      if (!LOCAL) g_t[i] = ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
+    }
+  };
+  float sum = 0.0f;
+  fetch(t_begin);
+  st.put(bc[0]);
+  __syncthreads();
+  int buf = 0;
+  for (int32_t t0 = t_begin; t0 < t_end; t0 += kTile, buf ^= 1) {
+    float uf[kTile], df[kTile], gf[kTile];
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      uf[i] = to_f<DT>(u_t[i]);
+      df[i] = to_f<DT>(d_t[i]);
+      if (!LOCAL) gf[i] = to_f<DT>(g_t[i]);
+    }
+    if (t0 + kTile < t_end) fetch(t0 + kTile);
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const bool valid = t0 + i < t_valid;
+      float dl = df[i] + bias;
+      if (g.softplus) dl = softplus(dl);
+      dl = valid && at.live ? dl : 0.0f;
+      float dq[4], xq[4];
+      quad_all(dl, dq);
+      quad_all(dl * uf[i], xq);
+      if (LOCAL) sum += dl;
+      float bf[SPL], cf[SPL], yq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      lds_states<SPL>(&bc[buf][i * 2 * NS + at.s0], bf);
+      if (!LOCAL) lds_states<SPL>(&bc[buf][i * 2 * NS + NS + at.s0], cf);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < SPL; ++k) {
+          const float e = __builtin_amdgcn_exp2f(dq[j] * a2[j][k]);
+          h[j][k] = __builtin_fmaf(e, h[j][k], xq[j] * bf[k]);
+          if (!LOCAL) yq[j] = __builtin_fmaf(h[j][k], cf[k], yq[j]);
+        }
+      if constexpr (!LOCAL) {
+        float v = __builtin_fmaf(skip, uf[i], own_sum<SL>(yq));
+        if (in.gate) v *= gf[i] * sigmoid(gf[i]);
+        if (at.first && t0 + i < t_end) yn[(t0 + i) * int64_t(g.d)] = from_f<DT>(valid ? v : 0.0f);
+      }
+    }
+    if (t0 + kTile < t_end) st.put(bc[buf ^ 1]);
+    __syncthreads();
+  }
+  if constexpr (LOCAL) {
+    store_states<SL, SPL>(h, states + (n * g.chunks + chunk) * ds, at, g);
+    if (at.first) sums[(n * g.chunks + chunk) * int64_t(g.d) + at.d] = sum;
+  } else {
+    if (state_out) store_states<SL, SPL>(h, state_out + n * ds, at, g);
+  }
+}
+
+// Along the chunks of one (sequence, channel, state): ends -> entering states,
+// in place, and the final state.
+__global__ __launch_bounds__(256) void scan_join_kernel(float* __restrict__ states, const float* __restrict__ sums,
+                                                        const float* __restrict__ a, const float* __restrict__ state,
+                                                        float* __restrict__ state_out, ScanGeo g, int64_t total) {
+  const int64_t ds = int64_t(g.d) * g.s;
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+    const int64_t n = id / ds, at = id - n * ds, d = at / g.s;
+    const float a2 = a[at] * kLog2e;
+    float h = state ? state[id] : 0.0f;
+    for (int32_t k = 0; k < g.chunks; ++k) {
+      const int64_t c = n * g.chunks + k;
+      const float end = states[c * ds + at];
+      states[c * ds + at] = h;
+      h = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * sums[c * g.d + d]), h, end);
+    }
+    if (state_out) state_out[id] = h;
+  }
+}
+
+// One token: groups of SL lanes by SPL states of one channel each.  The same
+// operations in the same order as a prompt in one chunk: a prompt fed token by
+// token leaves the same bits.
+template <int DT, int SL, int SPL>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanIn<DT> in, ScanGeo g, Elem<DT>* __restrict__ y,
+                                                        float* state_out, int64_t total) {
+  const int s0 = int(threadIdx.x) % SL * SPL;
+  // whole groups of SL lanes: total is counted in channels
+  for (int64_t id = (int64_t(blockIdx.x) * 256 + threadIdx.x) / SL; id < total;
+       id += int64_t(gridDim.x) * (256 / SL)) {
+    const int64_t n = id / g.d, d = id - n * g.d;
+    const float u = to_f<DT>(in.u[n * g.us[0] + d]);
+    float dl = to_f<DT>(in.delta[n * g.ds[0] + d]) + (in.delta_bias ? in.delta_bias[d] : 0.0f);
+    if (g.softplus) dl = softplus(dl);
+    float h[SPL], a[SPL], v = 0.0f;
+    const int64_t hs = id * g.s + s0, as = d * g.s + s0;
+    const bool whole = SPL == 4 && g.s == SL * SPL && aligned16(in.state) && aligned16(state_out) && aligned16(in.a);
+    if (whole) {
+      lds_states<SPL>(in.state + hs, h);
+      lds_states<SPL>(in.a + as, a);
+    } else {
+#pragma unroll
+      for (int k = 0; k < SPL; ++k) {
+        h[k] = s0 + k < g.s ? in.state[hs + k] : 0.0f;
+        a[k] = s0 + k < g.s ? in.a[as + k] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < SPL; ++k) {
+      const bool ok = s0 + k < g.s;
+      const float b = ok ? to_f<DT>(in.b[n * g.bs[0] + s0 + k]) : 0.0f;
+      const float c = ok ? to_f<DT>(in.c[n * g.cs[0] + s0 + k]) : 0.0f;
+      h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(dl * (a[k] * kLog2e)), h[k], dl * u * b);
+      v = __builtin_fmaf(h[k], c, v);
+    }
+    if (whole) {
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = h[k < SPL ? k : 0];
+      *reinterpret_cast<float4*>(state_out + hs) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < SPL; ++k)
+        if (s0 + k < g.s) state_out[hs + k] = h[k];
+    }
+    v = group_sum<SL>(v);
+    if (s0 == 0) {
+      if (in.skip) v = __builtin_fmaf(in.skip[d], u, v);
+      if (in.gate) {
+        const float z = to_f<DT>(in.gate[n * g.gs[0] + d]);
+        v *= z * sigmoid(z);
+      }
+      y[id] = from_f<DT>(v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+//
+// With gy = dy silu(gate) and g[t] the gradient of h[t], along t from the end:
+//   g[t] = c[t] gy[t] + e[t+1] g[t+1]
+//   db[t,s] = sum_d g D u,  dc[t,s] = sum_d gy h,  da[d,s] = sum_t g e h[t-1] D,
+//   du = D sum_s g b + skip gy,  dD = sum_s g e h[t-1] a + u sum_s g b,
+//   dgate = dy y silu'(gate),  dskip = sum_t gy u.
+// Nothing is saved by the forward pass.  The chunk kernel runs along t from a
+// zero state and, beside the end state, sums what the chunk's outputs pass to
+// the state that entered it, sum_t (e[begin] ... e[t]) c[t] gy[t]: the same
+// exponentials serve both.  The join kernel then knows the state that enters
+// every chunk and the gradient that comes back into its end.
+
+template <int DT>
+struct ScanOut {
+  Elem<DT>* u;
+  Elem<DT>* delta;
+  Elem<DT>* gate;
+  float* bc_part;   // [col_blocks][N*L][2][S] sums of db and dc
+  float* param_part;  // [N*chunks][D*S | D | D] sums of da, dskip, ddelta_bias
+};
+
+template <int DT, int SL, int SPL>
+__global__ __launch_bounds__(256) void scan_bwd_local_kernel(ScanIn<DT> in, ScanGeo g,
+                                                             const Elem<DT>* __restrict__ dy,
+                                                             float* __restrict__ states, float* __restrict__ backs,
+                                                             float* __restrict__ sums) {
+  constexpr int NS = SL * SPL;
+  __shared__ __attribute__((aligned(16))) float bc[2][kTile * 2 * NS];
+  int64_t n;
+  int32_t chunk, wave_d0;
+  locate<SL, SPL>(g, n, chunk, wave_d0);
+  const Place<SL, SPL> at(wave_d0, g.d);
+  const int32_t len = valid_len(in.lengths, n, g.l);
+  const int32_t t_begin = chunk * g.chunk;
+  const int32_t t_end = t_begin + g.chunk < g.l ? t_begin + g.chunk : g.l;
+  const int32_t t_valid = t_end < len ? t_end : len;
+
+  float a2[4][SPL], h[4][SPL], p[4][SPL], r[4][SPL];
+  load_states<SL, SPL>(a2, in.a, at, g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, h[j][i] = 0.0f, p[j][i] = 1.0f, r[j][i] = 0.0f;
+  const float bias = in.delta_bias && at.live ? in.delta_bias[at.d] : 0.0f;
+  const Elem<DT>* un = in.u + n * g.us[0] + at.d;
+  const Elem<DT>* dn = in.delta + n * g.ds[0] + at.d;
+  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] + at.d : nullptr;
+  const Elem<DT>* yn = dy + n * g.ys[0] + at.d;
+  const Elem<DT>* bn = in.b + n * g.bs[0];
+  const Elem<DT>* cn = in.c + n * g.cs[0];
+
+  Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile], y_t[kTile];
+  StagedBC<DT, NS> st;
+  auto fetch = [&](int32_t t0) {
+    st.stage(bn, cn, g, t0, t_valid);
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      const bool ok = at.live && t0 + i < t_valid;
+      u_t[i] = ok ? un[(t0 + i) * g.us[1]] : Elem<DT>(0);
+      d_t[i] = ok ? dn[(t0 + i) * g.ds[1]] : Elem<DT>(0);
+      g_t[i] = ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
+      y_t[i] = ok ? yn[(t0 + i) * g.ys[1]] : Elem<DT>(0);
+    }
+  };
+  float sum = 0.0f;
+  fetch(t_begin);
+  st.put(bc[0]);
+  __syncthreads();
+  int buf = 0;
+  for (int32_t t0 = t_begin; t0 < t_valid; t0 += kTile, buf ^= 1) {
+    float uf[kTile], df[kTile], gf[kTile], yf[kTile];
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      uf[i] = to_f<DT>(u_t[i]);
+      df[i] = to_f<DT>(d_t[i]);
+      gf[i] = to_f<DT>(g_t[i]);
+      yf[i] = to_f<DT>(y_t[i]);
+    }
+    if (t0 + kTile < t_valid) fetch(t0 + kTile);
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) {
+      float dl = df[i] + bias;
+      if (g.softplus) dl = softplus(dl);
+      dl = t0 + i < t_valid && at.live ? dl : 0.0f;
+      const float gy = in.gate ? yf[i] * gf[i] * sigmoid(gf[i]) : yf[i];
+      float dq[4], xq[4], gq[4];
+      quad_all(dl, dq);
+      quad_all(dl * uf[i], xq);
+      quad_all(gy, gq);
+      sum += dl;
+      float bf[SPL], cf[SPL];
+      lds_states<SPL>(&bc[buf][i * 2 * NS + at.s0], bf);
+      lds_states<SPL>(&bc[buf][i * 2 * NS + NS + at.s0], cf);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < SPL; ++k) {
+          const float e = __builtin_amdgcn_exp2f(dq[j] * a2[j][k]);
+          h[j][k] = __builtin_fmaf(e, h[j][k], xq[j] * bf[k]);
+          p[j][k] *= e;
+          r[j][k] = __builtin_fmaf(p[j][k], cf[k] * gq[j], r[j][k]);
+        }
+    }
+    if (t0 + kTile < t_valid) st.put(bc[buf ^ 1]);
+    __syncthreads();
+  }
+  const int64_t c = n * g.chunks + chunk, ds = int64_t(g.d) * g.s;
+  store_states<SL, SPL>(h, states + c * ds, at, g);
+  store_states<SL, SPL>(r, backs + c * ds, at, g);
+  if (at.first) sums[c * int64_t(g.d) + at.d] = sum;
+}
+
+// In place: ends -> entering states; what each chunk passes back -> the
+// gradient that enters at its end.  dstate: the initial state's gradient.
+__global__ __launch_bounds__(256) void scan_bwd_join_kernel(float* __restrict__ states, float* __restrict__ backs,
+                                                            const float* __restrict__ sums,
+                                                            const float* __restrict__ a,
+                                                            const float* __restrict__ state,
+                                                            const float* __restrict__ dstate_out,
+                                                            float* __restrict__ dstate, ScanGeo g, int64_t total) {
+  const int64_t ds = int64_t(g.d) * g.s;
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+    const int64_t n = id / ds, at = id - n * ds, d = at / g.s;
+    const float a2 = a[at] * kLog2e;
+    float h = state ? state[id] : 0.0f;
+    for (int32_t k = 0; k < g.chunks; ++k) {
+      const int64_t c = n * g.chunks + k;
+      const float end = states[c * ds + at];
+      states[c * ds + at] = h;
+      h = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * sums[c * g.d + d]), h, end);
+    }
+    float r = dstate_out ? dstate_out[id] : 0.0f;
+    for (int32_t k = g.chunks - 1; k >= 0; --k) {
+      const int64_t c = n * g.chunks + k;
+      const float back = backs[c * ds + at];
+      backs[c * ds + at] = r;
+      r = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * sums[c * g.d + d]), r, back);
+    }
+    if (dstate) dstate[id] = r;
+  }
+}
+
+// Sums over the wavefront's groups (lanes of equal state index): a db and a dc
+// value change places between the halves of the wavefront, so one register
+// holds both from there on.
+__device__ __forceinline__ float swap_halves_add(float x, float y) {  // x's sum in the lower half, y's in the upper
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y),
+                                                  false, false);
+  return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+}
+
+template <int SL>
+__device__ __forceinline__ float row_groups_sum(float v) {  // over the groups of a row of 16 lanes
+  if constexpr (SL <= 8) v += dpp<kRor8>(v);
+  if constexpr (SL <= 4) v += dpp<kRor4>(v);
+  return v;
+}
+
+constexpr int kSub = 8;        // positions whose states are in registers together
+constexpr int kSubs = 8;       // sub-chunks of a chunk at most: kSub * kSubs positions
+
+// Sub-chunk after sub-chunk from the end of the chunk: the states that enter
+// each are in LDS (from one sweep along the chunk), its kSub states are run
+// again into registers, then the gradient comes back through them.
+template <int DT, int SL, int SPL>
+__global__ __launch_bounds__(256) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo g, const Elem<DT>* __restrict__ dy,
+                                                       const float* __restrict__ states,
+                                                       const float* __restrict__ backs, ScanOut<DT> out) {
+  constexpr int NS = SL * SPL;
+  static_assert(kSub == kTile, "b and c are staged by sub-chunk");
+  __shared__ __attribute__((aligned(16))) float bc[kTile * 2 * NS];
+  __shared__ float part[2][kWaves][kSub][2 * NS];
+  __shared__ float kept[kWaves][kSubs - 1][4 * SPL][64];
+  int64_t n;
+  int32_t chunk, wave_d0;
+  locate<SL, SPL>(g, n, chunk, wave_d0);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const Place<SL, SPL> at(wave_d0, g.d);
+  const int32_t len = valid_len(in.lengths, n, g.l);
+  const int32_t t_begin = chunk * g.chunk;
+  const int32_t t_end = t_begin + g.chunk < g.l ? t_begin + g.chunk : g.l;
+  const int32_t t_valid = t_end < len ? t_end : len;
+  const int32_t subs = (t_end - t_begin + kSub - 1) / kSub;
+  const int64_t c_id = n * g.chunks + chunk, ds = int64_t(g.d) * g.s;
+
+  float a2[4][SPL], h[4][SPL], carry[4][SPL], da[4][SPL];
+  load_states<SL, SPL>(a2, in.a, at, g);
+  load_states<SL, SPL>(h, states + c_id * ds, at, g);
+  load_states<SL, SPL>(carry, backs + c_id * ds, at, g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, da[j][i] = 0.0f;
+  const float bias = in.delta_bias && at.live ? in.delta_bias[at.d] : 0.0f;
+  const float skip = in.skip && at.live ? in.skip[at.d] : 0.0f;
+  const Elem<DT>* un = in.u + n * g.us[0] + at.d;
+  const Elem<DT>* dn = in.delta + n * g.ds[0] + at.d;
+  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] + at.d : nullptr;
+  const Elem<DT>* yn = dy + n * g.ys[0] + at.d;
+  const Elem<DT>* bn = in.b + n * g.bs[0];
+  const Elem<DT>* cn = in.c + n * g.cs[0];
+  const int64_t o_n = n * g.l * int64_t(g.d) + at.d;
+
+  StagedBC<DT, NS> st;
+  // D and u of a sub-chunk's positions, 0 past the valid ones
+  auto steps = [&](int32_t t0, float (&df)[kSub], float (&uf)[kSub], float (&sg)[kSub]) {
+    Elem<DT> u_t[kSub], d_t[kSub];
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      const bool ok = at.live && t0 + i < t_valid;
+      u_t[i] = ok ? un[(t0 + i) * g.us[1]] : Elem<DT>(0);
+      d_t[i] = ok ? dn[(t0 + i) * g.ds[1]] : Elem<DT>(0);
+    }
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      uf[i] = to_f<DT>(u_t[i]);
+      float dl = to_f<DT>(d_t[i]) + bias;
+      sg[i] = 1.0f;
+      if (g.softplus) dl = softplus(dl, sg[i]);
+      df[i] = t0 + i < t_valid && at.live ? dl : 0.0f;
+    }
+  };
+  float df[kSub], uf[kSub], sg[kSub];
+  for (int32_t k = 0; k < subs - 1; ++k) {
+    const int32_t t0 = t_begin + k * kSub;
+    st.stage(bn, cn, g, t0, t_valid);
+    steps(t0, df, uf, sg);
+    __syncthreads();
+    st.put(bc);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      float dq[4], xq[4], bf[SPL];
+      quad_all(df[i], dq);
+      quad_all(df[i] * uf[i], xq);
+      lds_states<SPL>(&bc[i * 2 * NS + at.s0], bf);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < SPL; ++s)
+          h[j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq[j] * a2[j][s]), h[j][s], xq[j] * bf[s]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) kept[wave][k][j * SPL + s][lane] = h[j][s];
+  }
+
+  float dskip = 0.0f, dbias = 0.0f;
+  const int64_t rows = (int64_t(gridDim.x) / (int64_t(g.col_blocks) * g.chunks)) * g.l;  // N * L
+  const int64_t col = blockIdx.x % g.col_blocks;
+  for (int32_t k = subs - 1; k >= 0; --k) {
+    const int32_t t0 = t_begin + k * kSub;
+    st.stage(bn, cn, g, t0, t_valid);
+    steps(t0, df, uf, sg);
+    float yf[kSub], zf[kSub];
+    {
+      Elem<DT> y_t[kSub], g_t[kSub];
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) {
+        const bool ok = at.live && t0 + i < t_valid;
+        y_t[i] = ok ? yn[(t0 + i) * g.ys[1]] : Elem<DT>(0);
+        g_t[i] = ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
+      }
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) yf[i] = to_f<DT>(y_t[i]), zf[i] = to_f<DT>(g_t[i]);
+    }
+    __syncthreads();
+    st.put(bc);
+    __syncthreads();
+    float hs[kSub + 1][4][SPL];
+    if (k > 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) hs[0][j][s] = kept[wave][k - 1][j * SPL + s][lane];
+    } else {
+      load_states<SL, SPL>(hs[0], states + c_id * ds, at, g);
+    }
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      float dq[4], xq[4], bf[SPL];
+      quad_all(df[i], dq);
+      quad_all(df[i] * uf[i], xq);
+      lds_states<SPL>(&bc[i * 2 * NS + at.s0], bf);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < SPL; ++s)
+          hs[i + 1][j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq[j] * a2[j][s]), hs[i][j][s], xq[j] * bf[s]);
+    }
+    float (&pt)[kSub][2 * NS] = part[k & 1][wave];
+#pragma unroll
+    for (int i = kSub - 1; i >= 0; --i) {
+      const float z = zf[i];
+      const float sz = in.gate ? sigmoid(z) : 0.0f;
+      const float gy = in.gate ? yf[i] * z * sz : yf[i];
+      float dq[4], xq[4], gq[4], bf[SPL], cf[SPL], db[SPL], dc[SPL];
+      quad_all(df[i], dq);
+      quad_all(df[i] * uf[i], xq);
+      quad_all(gy, gq);
+      lds_states<SPL>(&bc[i * 2 * NS + at.s0], bf);
+      lds_states<SPL>(&bc[i * 2 * NS + NS + at.s0], cf);
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) db[s] = dc[s] = 0.0f;
+      float yq[4], bq[4], eq[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        yq[j] = bq[j] = eq[j] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+          const float e = __builtin_amdgcn_exp2f(dq[j] * a2[j][s]);
+          const float gr = __builtin_fmaf(cf[s], gq[j], carry[j][s]);
+          const float w = gr * (e * hs[i][j][s]);
+          yq[j] = __builtin_fmaf(hs[i + 1][j][s], cf[s], yq[j]);
+          bq[j] = __builtin_fmaf(gr, bf[s], bq[j]);
+          eq[j] = __builtin_fmaf(w, a2[j][s], eq[j]);
+          da[j][s] = __builtin_fmaf(w, dq[j], da[j][s]);
+          db[s] = __builtin_fmaf(gr, xq[j], db[s]);
+          dc[s] = __builtin_fmaf(hs[i + 1][j][s], gq[j], dc[s]);
+          carry[j][s] = e * gr;
+        }
+      }
+      const float yo = own_sum<SL>(yq), bo = own_sum<SL>(bq), eo = own_sum<SL>(eq);
+      const bool valid = t0 + i < t_valid && at.live;
+      const float dd = valid ? (eo * kLn2 + uf[i] * bo) * sg[i] : 0.0f;
+      dbias += dd;
+      dskip = __builtin_fmaf(gy, uf[i], dskip);
+      if (at.first && t0 + i < t_end) {
+        const int64_t o = o_n + (t0 + i) * int64_t(g.d);
+        out.u[o] = from_f<DT>(valid ? __builtin_fmaf(df[i], bo, skip * gy) : 0.0f);
+        out.delta[o] = from_f<DT>(dd);
+        if (in.gate) {
+          const float dz = yf[i] * __builtin_fmaf(skip, uf[i], yo) * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
+          out.gate[o] = from_f<DT>(valid ? dz : 0.0f);
+        }
+      }
+      // over the wavefront's channels
+#pragma unroll
+      for (int s = 0; s < SPL; ++s) {
+        const float v = row_groups_sum<SL>(add_row_pairs(swap_halves_add(db[s], dc[s])));
+        if ((lane & 31) < SL) pt[i][(lane >> 5) * NS + at.s0 + s] = v;
+      }
+    }
+    __syncthreads();
+    // the workgroup's channels; the buffer is used again two sub-chunks later
+    for (int i = threadIdx.x; i < kSub * 2 * NS; i += blockDim.x) {
+      const int t = i / (2 * NS), q = i % (2 * NS), which = q / NS, s = q % NS;
+      if (t0 + t >= t_valid || s >= g.s) continue;
+      float v = part[k & 1][0][t][q];
+      for (int w = 1; w < waves; ++w) v += part[k & 1][w][t][q];
+      out.bc_part[((col * rows + n * g.l + t0 + t) * 2 + which) * g.s + s] = v;
+    }
+  }
+  float* pp = out.param_part + c_id * (ds + 2 * int64_t(g.d));
+  store_states<SL, SPL>(da, pp, at, g);
+  if (at.first) {
+    pp[ds + at.d] = dskip;
+    pp[ds + g.d + at.d] = dbias;
+  }
+}
+
+// db, dc = the sums over the workgroups along the channels; 0 past the valid positions.
+template <int DT>
+__global__ __launch_bounds__(256) void scan_bwd_bc_kernel(const float* __restrict__ part,
+                                                          const int32_t* __restrict__ lengths, ScanGeo g,
+                                                          Elem<DT>* __restrict__ db, Elem<DT>* __restrict__ dc,
+                                                          int64_t total) {
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+    const int64_t row = id / (2 * g.s);
+    const int32_t q = int32_t(id - row * 2 * g.s);
+    const int64_t n = row / g.l;
+    float v = 0.0f;
+    if (row - n * g.l < valid_len(lengths, n, g.l)) {
+#pragma unroll 4
+      for (int32_t k = 0; k < g.col_blocks; ++k) v += part[k * total + id];
+    }
+    if (q < g.s) db[row * g.s + q] = from_f<DT>(v);
+    else dc[row * g.s + q - g.s] = from_f<DT>(v);
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+ScanGeo geo_of(const cnhwc_scan_desc_t& d) {
+  ScanGeo g{};
+  g.l = int32_t(d.l);
+  g.d = int32_t(d.d);
+  g.s = d.s;
+  g.softplus = d.softplus;
+  for (int i = 0; i < 2; ++i) {
+    g.us[i] = d.u_stride[i];
+    g.ds[i] = d.delta_stride[i];
+    g.bs[i] = d.b_stride[i];
+    g.cs[i] = d.c_stride[i];
+    g.gs[i] = d.gate_stride[i];
+    g.ys[i] = d.dy_stride[i];
+  }
+  return g;
+}
+
+template <int DT>
+ScanIn<DT> inputs_of(const cnhwc_scan_inputs_t& in) {
+  using E = Elem<DT>;
+  return {static_cast<const E*>(in.u), static_cast<const E*>(in.delta), in.a, static_cast<const E*>(in.b),
+          static_cast<const E*>(in.c), in.skip, static_cast<const E*>(in.gate), in.delta_bias, in.state, in.lengths};
+}
+
+template <int SL, int SPL>
+struct Shape {
+  static constexpr int sl = SL, spl = SPL;
+};
+// Lanes per group and states per lane for S states.
+template <typename F>
+auto with_shape(int32_t s, F&& f) {
+  if (s <= 4) return f(Shape<4, 1>{});
+  if (s <= 8) return f(Shape<4, 2>{});
+  if (s <= 16) return f(Shape<4, 4>{});
+  if (s <= 32) return f(Shape<8, 4>{});
+  return f(Shape<16, 4>{});
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <typename F>
+auto with_dtype(int32_t dt, F&& f) {
+  if (dt == CNHWC_F32) return f(Int<CNHWC_F32>{});
+  if (dt == CNHWC_F16) return f(Int<CNHWC_F16>{});
+  return f(Int<CNHWC_BF16>{});
+}
+
+int32_t channels_per_wave(int32_t s) { return s <= 16 ? 64 : (s <= 32 ? 32 : 16); }
+
+// Wavefronts of a workgroup and workgroups along the channels.
+void columns(const cnhwc_scan_desc_t& d, int32_t* waves, int32_t* col_blocks) {
+  const int64_t w = ceil_div(d.d, channels_per_wave(d.s));
+  *waves = int32_t(w < kWaves ? w : kWaves);
+  *col_blocks = int32_t(ceil_div(w, *waves));
+}
+
+// Positions per chunk of the forward pass.
+int32_t fwd_chunk(const cnhwc_scan_desc_t& d) {
+  return int32_t(ceil_div(d.l, kTile) * kTile);
+}
+
+constexpr int32_t kBwdChunk = kSub * kSubs;
+
+uint64_t fwd_bytes(const cnhwc_scan_desc_t& d) {
+  const int64_t chunks = ceil_div(d.l, fwd_chunk(d));
+  return chunks > 1 ? align_up(uint64_t(d.n) * chunks * d.d * (d.s + 1) * 4, 256) : 0;
+}
+
+struct BwdLayout {
+  uint64_t states, backs, sums, bc, params, total;
+};
+BwdLayout bwd_layout(const cnhwc_scan_desc_t& d) {
+  int32_t waves, cols;
+  columns(d, &waves, &cols);
+  const uint64_t nc = uint64_t(d.n) * ceil_div(d.l, kBwdChunk), ds = uint64_t(d.d) * d.s;
+  BwdLayout L;
+  uint64_t at = 0;
+  auto take = [&](uint64_t floats) {
+    const uint64_t o = at;
+    at = align_up(at + floats * 4, 256);
+    return o;
+  };
+  L.states = take(nc * ds);
+  L.backs = take(nc * ds);
+  L.sums = take(nc * d.d);
+  L.bc = take(uint64_t(cols) * d.n * d.l * 2 * d.s);
+  L.params = take(nc * (ds + 2 * uint64_t(d.d)));
+  L.total = at;
+  return L;
+}
+
+cnhwc_status_t check_desc(const cnhwc_scan_desc_t* d, bool bwd) {
+  if (!d || !dtype_ok(d->dtype) || d->reserved != 0 || (d->softplus != 0 && d->softplus != 1))
+    return CNHWC_ERR_INVALID_ARGUMENT;
+  if (!extent_ok(d->n) || !extent_ok(d->l) || !extent_ok(d->d) || d->s < 1) return CNHWC_ERR_INVALID_ARGUMENT;
+  if (!strides_ok(d->n, d->l, d->d, d->u_stride) || !strides_ok(d->n, d->l, d->d, d->delta_stride) ||
+      !strides_ok(d->n, d->l, d->s, d->b_stride) || !strides_ok(d->n, d->l, d->s, d->c_stride) ||
+      !strides_ok(d->n, d->l, d->d, d->gate_stride) || (bwd && !strides_ok(d->n, d->l, d->d, d->dy_stride)))
+    return CNHWC_ERR_INVALID_ARGUMENT;
+  if (d->s > CNHWC_SCAN_MAX_STATE) return CNHWC_ERR_UNSUPPORTED;
+  // positions fit 32 bits with a chunk's overhang; grids and offsets stay in range
+  if (d->l > INT_MAX - 1024 || d->d > (1ll << 23) || !dense_ok(d->n, d->l, d->d * d->s) ||
+      d->n * ceil_div(d->l, kBwdChunk) * ceil_div(d->d, 16) > (1ll << 24))
+    return CNHWC_ERR_UNSUPPORTED;
+  return CNHWC_OK;
+}
+
+void add_inputs(Buffers& bf, const cnhwc_scan_desc_t& d, const cnhwc_scan_inputs_t& in, bool state) {
+  const uint64_t es = dtype_size(d.dtype);
+  bf.in(in.u, span(d.n, d.l, d.d, d.u_stride) * es, es, true);
+  bf.in(in.delta, span(d.n, d.l, d.d, d.delta_stride) * es, es, true);
+  bf.in(in.a, uint64_t(d.d) * d.s * 4, 4, true);
+  bf.in(in.b, span(d.n, d.l, d.s, d.b_stride) * es, es, true);
+  bf.in(in.c, span(d.n, d.l, d.s, d.c_stride) * es, es, true);
+  bf.in(in.skip, d.d * 4, 4, false);
+  bf.in(in.gate, span(d.n, d.l, d.d, d.gate_stride) * es, es, false);
+  bf.in(in.delta_bias, d.d * 4, 4, false);
+  if (state) bf.in(in.state, uint64_t(d.n) * d.d * d.s * 4, 4, false);
+  bf.in(in.lengths, d.n * 4, 4, false);
+}
+
+}  // namespace
+}  // namespace seq
+}  // namespace cnhwc
+
+using namespace cnhwc;
+using namespace cnhwc::seq;
+
+extern "C" cnhwc_status_t cnhwc_scan_fwd_workspace(const cnhwc_scan_desc_t* desc, uint64_t* bytes) {
+  const cnhwc_status_t st = check_desc(desc, false);
+  if (st != CNHWC_OK) return st;
+  if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
+  *bytes = fwd_bytes(*desc);
+  return CNHWC_OK;
+}
+
+extern "C" cnhwc_status_t cnhwc_scan_fwd(const cnhwc_scan_desc_t* desc, const cnhwc_scan_inputs_t* in, void* y,
+                                         float* state_out, void* workspace, uint64_t workspace_bytes,
+                                         void* hip_stream) {
+  const cnhwc_status_t st = check_desc(desc, false);
+  if (st != CNHWC_OK) return st;
+  if (!in) return CNHWC_ERR_INVALID_ARGUMENT;
+  const cnhwc_scan_desc_t& d = *desc;
+  const uint64_t need = fwd_bytes(d);
+  if (workspace_bytes < need) return CNHWC_ERR_WORKSPACE_TOO_SMALL;
+  const uint64_t es = dtype_size(d.dtype);
+  Buffers bf;
+  add_inputs(bf, d, *in, true);
+  bf.out(y, uint64_t(d.n) * d.l * d.d * es, es, true);
+  bf.out(state_out, uint64_t(d.n) * d.d * d.s * 4, 4, false);
+  if (need) bf.out(workspace, need, 16, true);
+  if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  ScanGeo g = geo_of(d);
+  int32_t waves;
+  columns(d, &waves, &g.col_blocks);
+  g.chunk = fwd_chunk(d);
+  g.chunks = int32_t(ceil_div(d.l, g.chunk));
+  const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(waves * 64);
+  float* states = static_cast<float*>(workspace);
+  float* sums = states + d.n * g.chunks * d.d * d.s;
+  return with_dtype(d.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const ScanIn<DT> si = inputs_of<DT>(*in);
+    Elem<DT>* yo = static_cast<Elem<DT>*>(y);
+    return with_shape(d.s, [&](auto sh) {
+      constexpr int SL = decltype(sh)::sl, SPL = decltype(sh)::spl;
+      if (g.chunks > 1) {
+        hipLaunchKernelGGL((scan_fwd_kernel<DT, SL, SPL, true>), grid, block, 0, s, si, g, yo, states, sums, nullptr);
+        const int64_t total = d.n * d.d * d.s;
+        hipLaunchKernelGGL(scan_join_kernel, grid_of(ceil_div(total, 256)), dim3(256), 0, s, states, sums, in->a,
+                           in->state, state_out, g, total);
+      }
+      hipLaunchKernelGGL((scan_fwd_kernel<DT, SL, SPL, false>), grid, block, 0, s, si, g, yo, states, sums,
+                         g.chunks > 1 ? nullptr : state_out);
+      return hipGetLastError() == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
+    });
+  });
+}
+
+extern "C" cnhwc_status_t cnhwc_scan_bwd_workspace(const cnhwc_scan_desc_t* desc, uint64_t* bytes) {
+  const cnhwc_status_t st = check_desc(desc, true);
+  if (st != CNHWC_OK) return st;
+  if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
+  *bytes = bwd_layout(*desc).total;
+  return CNHWC_OK;
+}
+
+extern "C" cnhwc_status_t cnhwc_scan_bwd(const cnhwc_scan_desc_t* desc, const cnhwc_scan_inputs_t* in,
+                                         const void* dy, const float* dstate_out, const cnhwc_scan_grads_t* grads,
+                                         void* workspace, uint64_t workspace_bytes, void* hip_stream) {
+  const cnhwc_status_t st = check_desc(desc, true);
+  if (st != CNHWC_OK) return st;
+  if (!in || !grads) return CNHWC_ERR_INVALID_ARGUMENT;
+  const cnhwc_scan_desc_t& d = *desc;
+  if ((in->skip == nullptr) != (grads->skip == nullptr) || (in->gate == nullptr) != (grads->gate == nullptr) ||
+      (in->delta_bias == nullptr) != (grads->delta_bias == nullptr))
+    return CNHWC_ERR_INVALID_ARGUMENT;
+  const BwdLayout L = bwd_layout(d);
+  if (workspace_bytes < L.total) return CNHWC_ERR_WORKSPACE_TOO_SMALL;
+  const uint64_t es = dtype_size(d.dtype), act = uint64_t(d.n) * d.l * d.d * es, nls = uint64_t(d.n) * d.l * d.s * es;
+  const uint64_t state_bytes = uint64_t(d.n) * d.d * d.s * 4;
+  Buffers bf;
+  add_inputs(bf, d, *in, true);
+  bf.in(dy, span(d.n, d.l, d.d, d.dy_stride) * es, es, true);
+  bf.in(dstate_out, state_bytes, 4, false);
+  bf.out(grads->u, act, es, true);
+  bf.out(grads->delta, act, es, true);
+  bf.out(grads->a, uint64_t(d.d) * d.s * 4, 4, true);
+  bf.out(grads->b, nls, es, true);
+  bf.out(grads->c, nls, es, true);
+  bf.out(grads->skip, d.d * 4, 4, false);
+  bf.out(grads->gate, act, es, false);
+  bf.out(grads->delta_bias, d.d * 4, 4, false);
+  bf.out(grads->state, state_bytes, 4, false);
+  bf.out(workspace, L.total, 16, true);
+  if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  ScanGeo g = geo_of(d);
+  int32_t waves;
+  columns(d, &waves, &g.col_blocks);
+  g.chunk = kBwdChunk;
+  g.chunks = int32_t(ceil_div(d.l, g.chunk));
+  const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(waves * 64);
+  char* ws = static_cast<char*>(workspace);
+  float* states = reinterpret_cast<float*>(ws + L.states);
+  float* backs = reinterpret_cast<float*>(ws + L.backs);
+  float* sums = reinterpret_cast<float*>(ws + L.sums);
+  float* bc = reinterpret_cast<float*>(ws + L.bc);
+  float* params = reinterpret_cast<float*>(ws + L.params);
+  return with_dtype(d.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    using E = Elem<DT>;
+    const ScanIn<DT> si = inputs_of<DT>(*in);
+    const E* gy = static_cast<const E*>(dy);
+    const ScanOut<DT> so{static_cast<E*>(grads->u), static_cast<E*>(grads->delta), static_cast<E*>(grads->gate), bc,
+                         params};
+    with_shape(d.s, [&](auto sh) {
+      constexpr int SL = decltype(sh)::sl, SPL = decltype(sh)::spl;
+      hipLaunchKernelGGL((scan_bwd_local_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, sums);
+      const int64_t total = d.n * d.d * d.s;
+      hipLaunchKernelGGL(scan_bwd_join_kernel, grid_of(ceil_div(total, 256)), dim3(256), 0, s, states, backs, sums,
+                         in->a, in->state, dstate_out, grads->state, g, total);
+      hipLaunchKernelGGL((scan_bwd_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, so);
+    });
+    const int64_t bc_total = d.n * d.l * 2 * d.s;
+    hipLaunchKernelGGL((scan_bwd_bc_kernel<DT>), grid_of(ceil_div(bc_total, 256)), dim3(256), 0, s, bc, in->lengths,
+                       g, static_cast<E*>(grads->b), static_cast<E*>(grads->c), bc_total);
+    sum_parts<CNHWC_F32>(params, d.n * g.chunks,
+                         SumOut{{grads->a, grads->skip, grads->delta_bias}, {d.d * d.s, d.d, d.d}}, true, s);
+    return hipGetLastError() == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
+  });
+}
+
+extern "C" cnhwc_status_t cnhwc_scan_step(const cnhwc_scan_desc_t* desc, const cnhwc_scan_inputs_t* in, void* y,
+                                          float* state_out, void* hip_stream) {
+  const cnhwc_status_t st = check_desc(desc, false);
+  if (st != CNHWC_OK) return st;
+  if (!in || desc->l != 1 || !in->state || in->lengths) return CNHWC_ERR_INVALID_ARGUMENT;
+  const cnhwc_scan_desc_t& d = *desc;
+  const uint64_t es = dtype_size(d.dtype);
+  Buffers bf;
+  add_inputs(bf, d, *in, in->state != state_out);
+  bf.out(y, uint64_t(d.n) * d.d * es, es, true);
+  bf.out(state_out, uint64_t(d.n) * d.d * d.s * 4, 4, true);
+  if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
+  hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
+  const ScanGeo g = geo_of(d);
+  const int64_t total = d.n * d.d;
+  return with_dtype(d.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const ScanIn<DT> si = inputs_of<DT>(*in);
+    return with_shape(d.s, [&](auto sh) {
+      constexpr int SL = decltype(sh)::sl, SPL = decltype(sh)::spl;
+      hipLaunchKernelGGL((scan_step_kernel<DT, SL, SPL>), grid_of(ceil_div(total, 256 / SL)), dim3(256), 0, s, si, g,
+                         static_cast<Elem<DT>*>(y), state_out, total);
+      return hipGetLastError() == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
+    });
+  });
+}

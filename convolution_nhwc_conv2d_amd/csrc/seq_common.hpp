@@ -1,0 +1,215 @@
+// Device helpers shared by the sequence kernels (layer norm, causal
+// convolution, selective scan): element types, vector loads and stores, sums
+// across lanes, and the scalar functions.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <cstdint>
+#include <type_traits>
+
+#include "cnhwc_seq.h"
+
+namespace cnhwc {
+namespace seq {
+
+template <int DT> struct ElemOf { using T = uint16_t; };
+template <> struct ElemOf<CNHWC_F32> { using T = float; };
+template <int DT> using Elem = typename ElemOf<DT>::T;
+
+template <int DT>
+__device__ __forceinline__ float to_f(Elem<DT> v) {
+  if constexpr (DT == CNHWC_F32) return v;
+  else if constexpr (DT == CNHWC_BF16) return __builtin_bit_cast(float, uint32_t(v) << 16);
+  else return static_cast<float>(__builtin_bit_cast(_Float16, v));
+}
+
+// Round to nearest even; the 16-bit forms are single conversion instructions.
+template <int DT>
+__device__ __forceinline__ Elem<DT> from_f(float v) {
+  if constexpr (DT == CNHWC_F32) return v;
+  else if constexpr (DT == CNHWC_BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+
+// V consecutive elements; V * sizeof(element) is 16 bytes (aligned) or V is 1.
+template <int DT, int V>
+struct Pack { Elem<DT> e[V]; };
+
+template <int DT, int V>
+__device__ __forceinline__ Pack<DT, V> load_pack(const Elem<DT>* p) {
+  Pack<DT, V> r;
+  if constexpr (V == 1) {
+    r.e[0] = *p;
+  } else {
+    static_assert(V * sizeof(Elem<DT>) == 16, "16-byte vectors");
+    r = __builtin_bit_cast(Pack<DT, V>, *reinterpret_cast<const uint4*>(p));
+  }
+  return r;
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void store_pack(Elem<DT>* p, const Pack<DT, V>& v) {
+  if constexpr (V == 1) {
+    *p = v.e[0];
+  } else {
+    static_assert(V * sizeof(Elem<DT>) == 16, "16-byte vectors");
+    *reinterpret_cast<uint4*>(p) = __builtin_bit_cast(uint4, v);
+  }
+}
+
+// A parameter of dtype DT or fp32 (the choice is uniform over the launch).
+template <int DT>
+__device__ __forceinline__ float load_param(const void* p, int64_t i, bool f32) {
+  if constexpr (DT == CNHWC_F32) return static_cast<const float*>(p)[i];
+  else return f32 ? static_cast<const float*>(p)[i] : to_f<DT>(static_cast<const uint16_t*>(p)[i]);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_param(void* p, int64_t i, bool f32, float v) {
+  if constexpr (DT == CNHWC_F32) {
+    static_cast<float*>(p)[i] = v;
+  } else {
+    if (f32) static_cast<float*>(p)[i] = v;
+    else static_cast<uint16_t*>(p)[i] = from_f<DT>(v);
+  }
+}
+
+__device__ __forceinline__ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// ---------------------------------------------------------------- lanes
+
+// v moved by a row-local lane permutation (every lane of the pattern is live).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;         // lanes 1032, 2301 of a quad
+constexpr int kHalfMirror = 0x141, kRowMirror = 0x140;    // reversed 8 or 16 lanes
+constexpr int kRor8 = 0x128, kRor4 = 0x124;               // rows of 16 rotated
+constexpr int kQuadBcast = 0x55;                          // times j: lane j of each quad
+
+__device__ __forceinline__ float add_row_pairs(float v) {  // rows 0+1 and 2+3, in every lane
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+}
+__device__ __forceinline__ float add_halves(float v) {  // lower and upper 32 lanes, in every lane
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+}
+
+// Sum over groups of G consecutive lanes, the same bits in each of them.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  if constexpr (G >= 2) v += dpp<kQuadXor1>(v);
+  if constexpr (G >= 4) v += dpp<kQuadXor2>(v);
+  if constexpr (G >= 8) v += dpp<kHalfMirror>(v);
+  if constexpr (G >= 16) v += dpp<kRowMirror>(v);
+  if constexpr (G >= 32) v = add_row_pairs(v);
+  if constexpr (G >= 64) v = add_halves(v);
+  return v;
+}
+
+// ---------------------------------------------------------------- functions
+
+// e^x for x up to 88; the product with log2(e) is carried in two terms, so the
+// relative error stays near one unit of the last place instead of growing with
+// |x|.  NaN stays NaN; below -110 (minus infinity too) the result is 0.
+__device__ __forceinline__ float exp_full(float x) {
+  constexpr float hi = 1.44269502f, lo = 1.92596299e-8f;  // log2(e) = hi + lo
+  x = x < -110.0f ? -110.0f : x;
+  const float t = x * hi;
+  const float r = __builtin_fmaf(x, hi, -t) + x * lo;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * 0.693147181f, e);
+}
+
+// 1 / v for ordinary v: the hardware's estimate and one Newton step.
+__device__ __forceinline__ float rcp_full(float v) {
+  const float r = __builtin_amdgcn_rcpf(v);
+  return __builtin_fmaf(r, __builtin_fmaf(-v, r, 1.0f), r);
+}
+
+// 1 / (1 + e^-x); the exponent is held at 80, where the result is 1.8e-35.
+__device__ __forceinline__ float sigmoid(float x) {
+  const float n = -x > 80.0f ? 80.0f : -x;
+  return rcp_full(1.0f + exp_full(n));
+}
+
+// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  With
+// q = e / (2 + e) <= 1/3, log(1 + e) = 2 atanh(q) = 2 q (1 + q^2/3 + q^4/5 + ...):
+// nine terms leave 2^-29 of the value.  Also s = 1 / (1 + e^-x), its derivative.
+__device__ __forceinline__ float softplus(float x, float& s) {
+  const float e = exp_full(-__builtin_fabsf(x));
+  const float q = e * rcp_full(2.0f + e);
+  const float q2 = q * q;
+  float p = 1.0f / 17.0f;
+  p = __builtin_fmaf(p, q2, 1.0f / 15.0f);
+  p = __builtin_fmaf(p, q2, 1.0f / 13.0f);
+  p = __builtin_fmaf(p, q2, 1.0f / 11.0f);
+  p = __builtin_fmaf(p, q2, 1.0f / 9.0f);
+  p = __builtin_fmaf(p, q2, 1.0f / 7.0f);
+  p = __builtin_fmaf(p, q2, 1.0f / 5.0f);
+  p = __builtin_fmaf(p, q2, 1.0f / 3.0f);
+  p = __builtin_fmaf(p, q2, 1.0f);
+  const float inv = rcp_full(1.0f + e);
+  s = x < 0.0f ? e * inv : inv;
+  return (x > 0.0f ? x : 0.0f) + 2.0f * q * p;
+}
+__device__ __forceinline__ float softplus(float x) {
+  float s;
+  return softplus(x, s);
+}
+
+// Valid positions of sequence n.
+__device__ __forceinline__ int32_t valid_len(const int32_t* lengths, int64_t n, int32_t l) {
+  if (!lengths) return l;
+  const int32_t v = lengths[n];
+  return v < 0 ? 0 : (v > l ? l : v);
+}
+
+// ---------------------------------------------------------------- partial sums
+
+// Up to three outputs side by side in the rows of partial sums; those with a
+// NULL pointer are skipped.
+struct SumOut {
+  void* p[3];
+  int64_t n[3];
+};
+
+// part: `parts` rows of n[0] + n[1] + n[2] fp32 partial sums.  The outputs = the
+// sums over the rows, in a fixed order, rounded once: 16 columns by 16 row
+// groups to a workgroup, so a few thousand columns fill the device.
+template <int DT>
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ part, int64_t parts, SumOut out,
+                                                        bool f32) {
+  __shared__ float sum[16][17];
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int64_t c = int64_t(blockIdx.x) * 16 + col, width = out.n[0] + out.n[1] + out.n[2];
+  float v = 0.0f;
+  if (c < width) {
+#pragma unroll 8
+    for (int64_t r = grp; r < parts; r += 16) v += part[r * width + c];
+  }
+  sum[grp][col] = v;
+  __syncthreads();
+  if (grp != 0 || c >= width) return;
+#pragma unroll
+  for (int k = 1; k < 16; ++k) v += sum[k][col];
+  int64_t at = c;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (at >= 0 && at < out.n[i] && out.p[i]) store_param<DT>(out.p[i], at, f32, v);
+    at -= out.n[i];
+  }
+}
+
+template <int DT>
+void sum_parts(const float* part, int64_t parts, const SumOut& out, bool f32, hipStream_t st) {
+  const int64_t width = out.n[0] + out.n[1] + out.n[2];
+  hipLaunchKernelGGL((sum_parts_kernel<DT>), dim3(unsigned((width + 15) / 16)), dim3(256), 0, st, part, parts, out,
+                     f32);
+}
+
+}  // namespace seq
+}  // namespace cnhwc
