@@ -184,13 +184,16 @@ __device__ __forceinline__ void locate(const ScanGeo& g, int64_t& n, int32_t& ch
   wave_d0 = (col * int32_t(blockDim.x / 64) + int32_t(threadIdx.x >> 6)) * Place<SL, SPL>::kChannels;
 }
 
+#ifndef SCAN_OCC
+#define SCAN_OCC 1
+#endif
 // ---------------------------------------------------------------- forward
 
 // LOCAL: the chunk from a zero state; ends [n,chunk,D,S] and sums [n,chunk,D].
 // Otherwise the outputs, from the entering states `starts` ([n,chunk,D,S], or
 // the initial state where there is one chunk) and, with one chunk, state_out.
 template <int DT, int SL, int SPL, bool LOCAL>
-__global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g, Elem<DT>* __restrict__ y,
+__global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g, Elem<DT>* __restrict__ y,
                                                        float* __restrict__ states, float* __restrict__ sums,
                                                        float* __restrict__ state_out) {
   constexpr int NS = SL * SPL;
@@ -233,7 +236,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g,
       const bool ok = at.live && t0 + i < t_valid;
       u_t[i] = ok ? un[(t0 + i) * g.us[1]] : Elem<DT>(0);
       d_t[i] = ok ? dn[(t0 + i) * g.ds[1]] : Elem<DT>(0);
-      if (!LOCAL) g_t[i] = ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
+      g_t[i] = !LOCAL && ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
     }
   };
   float sum = 0.0f;
@@ -242,20 +245,27 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g,
   __syncthreads();
   int buf = 0;
   for (int32_t t0 = t_begin; t0 < t_end; t0 += kTile, buf ^= 1) {
+    // what belongs to a channel alone, for the whole tile: D, u, and the gate's factor
     float uf[kTile], df[kTile], gf[kTile];
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
       uf[i] = to_f<DT>(u_t[i]);
-      df[i] = to_f<DT>(d_t[i]);
-      if (!LOCAL) gf[i] = to_f<DT>(g_t[i]);
+      df[i] = to_f<DT>(d_t[i]) + bias;
+      gf[i] = to_f<DT>(g_t[i]);
     }
     if (t0 + kTile < t_end) fetch(t0 + kTile);
+    if (g.softplus) {
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) df[i] = softplus(df[i]);
+    }
+    if (!LOCAL && in.gate) {
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) gf[i] *= sigmoid(gf[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
       const bool valid = t0 + i < t_valid;
-      float dl = df[i] + bias;
-      if (g.softplus) dl = softplus(dl);
-      dl = valid && at.live ? dl : 0.0f;
+      const float dl = valid && at.live ? df[i] : 0.0f;
       float dq[4], xq[4];
       quad_all(dl, dq);
       quad_all(dl * uf[i], xq);
@@ -273,7 +283,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g,
         }
       if constexpr (!LOCAL) {
         float v = __builtin_fmaf(skip, uf[i], own_sum<SL>(yq));
-        if (in.gate) v *= gf[i] * sigmoid(gf[i]);
+        if (in.gate) v *= gf[i];
         if (at.first && t0 + i < t_end) yn[(t0 + i) * int64_t(g.d)] = from_f<DT>(valid ? v : 0.0f);
       }
     }
@@ -288,8 +298,31 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g,
   }
 }
 
-// Along the chunks of one (sequence, channel, state): ends -> entering states,
-// in place, and the final state.
+// Ends -> entering states of one (sequence, channel, state), in place; returns
+// the final state.  The chunks' values are loaded kJoin at a time: what they
+// are is known beforehand, only the sum along them is serial.
+constexpr int kJoin = 16;
+__device__ __forceinline__ float join_forward(float* state, const float* sum, float a2, float h, const ScanGeo& g) {
+  const int64_t ds = int64_t(g.d) * g.s;
+  for (int32_t k0 = 0; k0 < g.chunks; k0 += kJoin) {
+    float p[kJoin], e[kJoin];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      const bool ok = k0 + i < g.chunks;
+      p[i] = ok ? state[(k0 + i) * ds] : 0.0f;
+      e[i] = ok ? sum[(k0 + i) * int64_t(g.d)] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      if (k0 + i >= g.chunks) break;
+      state[(k0 + i) * ds] = h;
+      h = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * e[i]), h, p[i]);
+    }
+  }
+  return h;
+}
+
+// Along the chunks: ends -> entering states, in place, and the final state.
 __global__ __launch_bounds__(256) void scan_join_kernel(float* __restrict__ states, const float* __restrict__ sums,
                                                         const float* __restrict__ a, const float* __restrict__ state,
                                                         float* __restrict__ state_out, ScanGeo g, int64_t total) {
@@ -298,12 +331,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(float* __restrict__ stat
     const int64_t n = id / ds, at = id - n * ds, d = at / g.s;
     const float a2 = a[at] * kLog2e;
     float h = state ? state[id] : 0.0f;
-    for (int32_t k = 0; k < g.chunks; ++k) {
-      const int64_t c = n * g.chunks + k;
-      const float end = states[c * ds + at];
-      states[c * ds + at] = h;
-      h = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * sums[c * g.d + d]), h, end);
-    }
+    h = join_forward(states + n * g.chunks * ds + at, sums + n * g.chunks * int64_t(g.d) + d, a2, h, g);
     if (state_out) state_out[id] = h;
   }
 }
@@ -491,18 +519,24 @@ __global__ __launch_bounds__(256) void scan_bwd_join_kernel(float* __restrict__ 
     const int64_t n = id / ds, at = id - n * ds, d = at / g.s;
     const float a2 = a[at] * kLog2e;
     float h = state ? state[id] : 0.0f;
-    for (int32_t k = 0; k < g.chunks; ++k) {
-      const int64_t c = n * g.chunks + k;
-      const float end = states[c * ds + at];
-      states[c * ds + at] = h;
-      h = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * sums[c * g.d + d]), h, end);
-    }
+    float* back = backs + n * g.chunks * ds + at;
+    const float* sum = sums + n * g.chunks * int64_t(g.d) + d;
+    join_forward(states + n * g.chunks * ds + at, sum, a2, h, g);
     float r = dstate_out ? dstate_out[id] : 0.0f;
-    for (int32_t k = g.chunks - 1; k >= 0; --k) {
-      const int64_t c = n * g.chunks + k;
-      const float back = backs[c * ds + at];
-      backs[c * ds + at] = r;
-      r = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * sums[c * g.d + d]), r, back);
+    for (int32_t k0 = g.chunks - 1; k0 >= 0; k0 -= kJoin) {
+      float p[kJoin], e[kJoin];
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) {
+        const bool ok = k0 - i >= 0;
+        p[i] = ok ? back[(k0 - i) * ds] : 0.0f;
+        e[i] = ok ? sum[(k0 - i) * int64_t(g.d)] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) {
+        if (k0 - i < 0) break;
+        back[(k0 - i) * ds] = r;
+        r = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * e[i]), r, p[i]);
+      }
     }
     if (dstate) dstate[id] = r;
   }
@@ -807,8 +841,25 @@ void columns(const cnhwc_scan_desc_t& d, int32_t* waves, int32_t* col_blocks) {
 }
 
 // Positions per chunk of the forward pass.
+#ifndef SCAN_WAVES
+#define SCAN_WAVES 4096
+#endif
+#ifndef SCAN_ONE
+#define SCAN_ONE 1024
+#endif
+#ifndef SCAN_MIN
+#define SCAN_MIN 32
+#endif
 int32_t fwd_chunk(const cnhwc_scan_desc_t& d) {
-  return int32_t(ceil_div(d.l, kTile) * kTile);
+  int32_t waves, cols;
+  columns(d, &waves, &cols);
+  const int64_t one = d.n * cols * waves;
+  int64_t chunk = d.l;
+  if (one < SCAN_ONE) {
+    chunk = ceil_div(d.l * one, SCAN_WAVES);
+    chunk = chunk < SCAN_MIN ? SCAN_MIN : chunk;
+  }
+  return int32_t(ceil_div(chunk, kTile) * kTile);
 }
 
 constexpr int32_t kBwdChunk = kSub * kSubs;
