@@ -33,7 +33,7 @@ namespace seq {
 namespace {
 
 constexpr int kTile = 8;    // positions whose loads are issued together
-constexpr int kWaves = 4;   // most wavefronts of a workgroup
+constexpr int kWaves = 4;   // wavefronts of a workgroup
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
 
@@ -64,10 +64,10 @@ struct ScanIn {
 template <int SL, int SPL>
 struct Place {
   static constexpr int kChannels = 64 / SL * 4;  // per wavefront
-  static constexpr int kStates = SL * SPL;       // per group; states past S are zero
   int32_t dq, d, s0;
-  bool live;   // the own channel exists
-  bool first;  // this lane stores for its channel
+  uint32_t at;  // the own channel to load from: the last one where it does not exist
+  bool live;    // the own channel exists
+  bool first;   // this lane stores for its channel
   __device__ __forceinline__ Place(int32_t wave_d0, int32_t d_all) {
     const int lane = threadIdx.x & 63;
     dq = wave_d0 + lane / SL * 4;
@@ -75,8 +75,23 @@ struct Place {
     s0 = lane % SL * SPL;
     live = d < d_all;
     first = lane % SL < 4 && live;
+    at = live ? d : d_all - 1;
   }
 };
+
+// The own channel's elements of a tile of positions (0 past the valid ones);
+// row: the sequence's first position, uniform over the wavefront.
+template <int DT>
+__device__ __forceinline__ void load_tile(Elem<DT> (&v)[kTile], const Elem<DT>* __restrict__ row, int64_t stride,
+                                          uint32_t d, int32_t t0, int32_t t_valid) {
+  if (t0 + kTile <= t_valid) {
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) v[i] = (row + (t0 + i) * stride)[d];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) v[i] = t0 + i < t_valid ? (row + (t0 + i) * stride)[d] : Elem<DT>(0);
+  }
+}
 
 // The [D,S] values of a thread's four channels by SPL states; zero outside.
 template <int SL, int SPL>
@@ -120,21 +135,36 @@ __device__ __forceinline__ void store_states(const float (&h)[4][SPL], float* __
   }
 }
 
+// The values are computed here and not later: without this the compiler moves
+// a tile's whole arithmetic behind the next tile's staging and holds the
+// operands of all its positions in registers meanwhile.
+template <int SPL>
+__device__ __forceinline__ void settle(float (&h)[4][SPL]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) asm volatile("" : "+v"(h[j][i]));
+}
+
 // One float of each lane of the quad, in all four.
 __device__ __forceinline__ void quad_all(float v, float (&out)[4]) {
-  out[0] = dpp<0 * kQuadBcast>(v);
+  out[0] = dpp<0>(v);
   out[1] = dpp<1 * kQuadBcast>(v);
   out[2] = dpp<2 * kQuadBcast>(v);
   out[3] = dpp<3 * kQuadBcast>(v);
 }
 
-// Of the four channels' sums over the group's lanes, the own channel's.
+// Of the four channels' sums over the group's lanes, the own channel's: lanes
+// trade the channels that are not theirs, so the four sums take three additions.
 template <int SL>
 __device__ __forceinline__ float own_sum(const float (&v)[4]) {
-  const int j = threadIdx.x & 3;
-  const float s0 = group_sum<SL>(v[0]), s1 = group_sum<SL>(v[1]);
-  const float s2 = group_sum<SL>(v[2]), s3 = group_sum<SL>(v[3]);
-  return j < 2 ? (j == 0 ? s0 : s1) : (j == 2 ? s2 : s3);
+  const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+  const float p = (odd ? v[1] : v[0]) + dpp<kQuadXor1>(odd ? v[0] : v[1]);
+  const float q = (odd ? v[3] : v[2]) + dpp<kQuadXor1>(odd ? v[2] : v[3]);
+  float r = (upper ? q : p) + dpp<kQuadXor2>(upper ? p : q);
+  if constexpr (SL >= 8) r += dpp<kHalfMirror>(dpp<kQuadReverse>(r));  // lane ^ 4
+  if constexpr (SL >= 16) r += dpp<kRor8>(r);
+  return r;
 }
 
 // b and c of a tile of positions in LDS as floats, zero past the valid
@@ -142,13 +172,13 @@ __device__ __forceinline__ float own_sum(const float (&v)[4]) {
 template <int DT, int NS>
 struct StagedBC {
   static constexpr int kAll = kTile * 2 * NS;
-  static constexpr int kPer = kAll / 64;  // for a workgroup of one wavefront
+  static constexpr int kPer = (kAll + 255) / 256;
   Elem<DT> v[kPer];
   __device__ __forceinline__ void stage(const Elem<DT>* __restrict__ b, const Elem<DT>* __restrict__ c,
                                         const ScanGeo& g, int32_t t0, int32_t end) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
+      const int i = threadIdx.x + k * 256;
       const int s = i % NS, which = i / NS % 2, t = t0 + i / (2 * NS);
       v[k] = Elem<DT>(0);
       if (i < kAll && s < g.s && t < end) v[k] = which ? c[t * g.cs[1] + s] : b[t * g.bs[1] + s];
@@ -157,7 +187,7 @@ struct StagedBC {
   __device__ __forceinline__ void put(float* lds) const {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
+      const int i = threadIdx.x + k * 256;
       if (i < kAll) lds[i] = to_f<DT>(v[k]);
     }
   }
@@ -181,9 +211,15 @@ __device__ __forceinline__ void locate(const ScanGeo& g, int64_t& n, int32_t& ch
   const int32_t col = int32_t(blockIdx.x - row * g.col_blocks);
   n = row / g.chunks;
   chunk = int32_t(row - n * g.chunks);
-  wave_d0 = (col * int32_t(blockDim.x / 64) + int32_t(threadIdx.x >> 6)) * Place<SL, SPL>::kChannels;
+  wave_d0 = __builtin_amdgcn_readfirstlane((col * kWaves + int32_t(threadIdx.x >> 6)) * Place<SL, SPL>::kChannels);
 }
 
+#ifndef SCAN_OCCL
+#define SCAN_OCCL 2
+#endif
+#ifndef SCAN_OCCB
+#define SCAN_OCCB 2
+#endif
 #ifndef SCAN_OCC
 #define SCAN_OCC 1
 #endif
@@ -218,26 +254,22 @@ __global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, 
     if (g.chunks > 1) load_states<SL, SPL>(h, states + (n * g.chunks + chunk) * ds, at, g);
     else if (in.state) load_states<SL, SPL>(h, in.state + n * ds, at, g);
   }
-  const float bias = in.delta_bias && at.live ? in.delta_bias[at.d] : 0.0f;
-  const float skip = !LOCAL && in.skip && at.live ? in.skip[at.d] : 0.0f;
-  const Elem<DT>* un = in.u + n * g.us[0] + at.d;
-  const Elem<DT>* dn = in.delta + n * g.ds[0] + at.d;
-  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] + at.d : nullptr;
+  const float bias = in.delta_bias ? in.delta_bias[at.at] : 0.0f;
+  const float skip = !LOCAL && in.skip ? in.skip[at.at] : 0.0f;
+  const Elem<DT>* un = in.u + n * g.us[0];
+  const Elem<DT>* dn = in.delta + n * g.ds[0];
+  const Elem<DT>* gn = !LOCAL && in.gate ? in.gate + n * g.gs[0] : nullptr;
   const Elem<DT>* bn = in.b + n * g.bs[0];
   const Elem<DT>* cn = in.c + n * g.cs[0];
-  Elem<DT>* yn = LOCAL ? nullptr : y + n * g.l * int64_t(g.d) + at.d;
+  Elem<DT>* yn = LOCAL ? nullptr : y + n * g.l * int64_t(g.d);
 
-  Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile];
+  Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile] = {};
   StagedBC<DT, NS> st;
   auto fetch = [&](int32_t t0) {
     st.stage(bn, cn, g, t0, t_valid);
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      const bool ok = at.live && t0 + i < t_valid;
-      u_t[i] = ok ? un[(t0 + i) * g.us[1]] : Elem<DT>(0);
-      d_t[i] = ok ? dn[(t0 + i) * g.ds[1]] : Elem<DT>(0);
-      g_t[i] = !LOCAL && ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
-    }
+    load_tile<DT>(u_t, un, g.us[1], at.at, t0, t_valid);
+    load_tile<DT>(d_t, dn, g.ds[1], at.at, t0, t_valid);
+    if (gn) load_tile<DT>(g_t, gn, g.gs[1], at.at, t0, t_valid);
   };
   float sum = 0.0f;
   fetch(t_begin);
@@ -281,10 +313,11 @@ __global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, 
           h[j][k] = __builtin_fmaf(e, h[j][k], xq[j] * bf[k]);
           if (!LOCAL) yq[j] = __builtin_fmaf(h[j][k], cf[k], yq[j]);
         }
+      settle(h);
       if constexpr (!LOCAL) {
         float v = __builtin_fmaf(skip, uf[i], own_sum<SL>(yq));
         if (in.gate) v *= gf[i];
-        if (at.first && t0 + i < t_end) yn[(t0 + i) * int64_t(g.d)] = from_f<DT>(valid ? v : 0.0f);
+        if (at.first && t0 + i < t_end) (yn + (t0 + i) * int64_t(g.d))[at.at] = from_f<DT>(valid ? v : 0.0f);
       }
     }
     if (t0 + kTile < t_end) st.put(bc[buf ^ 1]);
@@ -406,20 +439,36 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanIn<DT> in, ScanGeo g
 // exponentials serve both.  The join kernel then knows the state that enters
 // every chunk and the gradient that comes back into its end.
 
+// The state at every tile of a chunk costs less to keep than to run again: the
+// chunk kernel leaves it (from its zero start) with the sum of D up to there,
+// in the order of its lanes, and the gradient kernel adds what the entering
+// state has become by then, one exponential per state and tile.
+
 template <int DT>
 struct ScanOut {
   Elem<DT>* u;
   Elem<DT>* delta;
   Elem<DT>* gate;
-  float* bc_part;   // [col_blocks][N*L][2][S] sums of db and dc
+  float* bc_part;     // [col_blocks][N*L][2][S] sums of db and dc
   float* param_part;  // [N*chunks][D*S | D | D] sums of da, dskip, ddelta_bias
 };
 
+// Kept states: [workgroup][tile][wavefront][SPL][64 lanes] of four channels
+// each, and the sums of D [workgroup][tile][wavefront][64 lanes].
+struct Kept {
+  float4* h;
+  float* sum;
+};
+template <int SPL>
+__device__ __forceinline__ int64_t kept_at(const ScanGeo& g, int32_t tile) {
+  return ((int64_t(blockIdx.x) * (g.chunk / kTile) + tile) * kWaves + (threadIdx.x >> 6)) * 64 + (threadIdx.x & 63);
+}
+
 template <int DT, int SL, int SPL>
-__global__ __launch_bounds__(256) void scan_bwd_local_kernel(ScanIn<DT> in, ScanGeo g,
+__global__ __launch_bounds__(256, SCAN_OCCL) void scan_bwd_local_kernel(ScanIn<DT> in, ScanGeo g,
                                                              const Elem<DT>* __restrict__ dy,
                                                              float* __restrict__ states, float* __restrict__ backs,
-                                                             float* __restrict__ sums) {
+                                                             float* __restrict__ sums, Kept kept) {
   constexpr int NS = SL * SPL;
   __shared__ __attribute__((aligned(16))) float bc[2][kTile * 2 * NS];
   int64_t n;
@@ -437,26 +486,22 @@ __global__ __launch_bounds__(256) void scan_bwd_local_kernel(ScanIn<DT> in, Scan
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, h[j][i] = 0.0f, p[j][i] = 1.0f, r[j][i] = 0.0f;
-  const float bias = in.delta_bias && at.live ? in.delta_bias[at.d] : 0.0f;
-  const Elem<DT>* un = in.u + n * g.us[0] + at.d;
-  const Elem<DT>* dn = in.delta + n * g.ds[0] + at.d;
-  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] + at.d : nullptr;
-  const Elem<DT>* yn = dy + n * g.ys[0] + at.d;
+  const float bias = in.delta_bias ? in.delta_bias[at.at] : 0.0f;
+  const Elem<DT>* un = in.u + n * g.us[0];
+  const Elem<DT>* dn = in.delta + n * g.ds[0];
+  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] : nullptr;
+  const Elem<DT>* yn = dy + n * g.ys[0];
   const Elem<DT>* bn = in.b + n * g.bs[0];
   const Elem<DT>* cn = in.c + n * g.cs[0];
 
-  Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile], y_t[kTile];
+  Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile] = {}, y_t[kTile];
   StagedBC<DT, NS> st;
   auto fetch = [&](int32_t t0) {
     st.stage(bn, cn, g, t0, t_valid);
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      const bool ok = at.live && t0 + i < t_valid;
-      u_t[i] = ok ? un[(t0 + i) * g.us[1]] : Elem<DT>(0);
-      d_t[i] = ok ? dn[(t0 + i) * g.ds[1]] : Elem<DT>(0);
-      g_t[i] = ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
-      y_t[i] = ok ? yn[(t0 + i) * g.ys[1]] : Elem<DT>(0);
-    }
+    load_tile<DT>(u_t, un, g.us[1], at.at, t0, t_valid);
+    load_tile<DT>(d_t, dn, g.ds[1], at.at, t0, t_valid);
+    load_tile<DT>(y_t, yn, g.ys[1], at.at, t0, t_valid);
+    if (gn) load_tile<DT>(g_t, gn, g.gs[1], at.at, t0, t_valid);
   };
   float sum = 0.0f;
   fetch(t_begin);
@@ -464,25 +509,37 @@ __global__ __launch_bounds__(256) void scan_bwd_local_kernel(ScanIn<DT> in, Scan
   __syncthreads();
   int buf = 0;
   for (int32_t t0 = t_begin; t0 < t_valid; t0 += kTile, buf ^= 1) {
+    if (t0 > t_begin) {
+      const int64_t k = kept_at<SPL>(g, (t0 - t_begin) / kTile);
+      const int64_t w = (k >> 6) * SPL * 64 + (k & 63);
+#pragma unroll
+      for (int i = 0; i < SPL; ++i) kept.h[w + i * 64] = make_float4(h[0][i], h[1][i], h[2][i], h[3][i]);
+      kept.sum[k] = sum;
+    }
     float uf[kTile], df[kTile], gf[kTile], yf[kTile];
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
       uf[i] = to_f<DT>(u_t[i]);
-      df[i] = to_f<DT>(d_t[i]);
+      df[i] = to_f<DT>(d_t[i]) + bias;
       gf[i] = to_f<DT>(g_t[i]);
       yf[i] = to_f<DT>(y_t[i]);
     }
     if (t0 + kTile < t_valid) fetch(t0 + kTile);
+    if (g.softplus) {
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) df[i] = softplus(df[i]);
+    }
+    if (in.gate) {
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) yf[i] *= gf[i] * sigmoid(gf[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
-      float dl = df[i] + bias;
-      if (g.softplus) dl = softplus(dl);
-      dl = t0 + i < t_valid && at.live ? dl : 0.0f;
-      const float gy = in.gate ? yf[i] * gf[i] * sigmoid(gf[i]) : yf[i];
+      const float dl = t0 + i < t_valid && at.live ? df[i] : 0.0f;
       float dq[4], xq[4], gq[4];
       quad_all(dl, dq);
       quad_all(dl * uf[i], xq);
-      quad_all(gy, gq);
+      quad_all(yf[i], gq);
       sum += dl;
       float bf[SPL], cf[SPL];
       lds_states<SPL>(&bc[buf][i * 2 * NS + at.s0], bf);
@@ -496,6 +553,8 @@ __global__ __launch_bounds__(256) void scan_bwd_local_kernel(ScanIn<DT> in, Scan
           p[j][k] *= e;
           r[j][k] = __builtin_fmaf(p[j][k], cf[k] * gq[j], r[j][k]);
         }
+      settle(h);
+      settle(r);
     }
     if (t0 + kTile < t_valid) st.put(bc[buf ^ 1]);
     __syncthreads();
@@ -542,145 +601,126 @@ __global__ __launch_bounds__(256) void scan_bwd_join_kernel(float* __restrict__ 
   }
 }
 
-// Sums over the wavefront's groups (lanes of equal state index): a db and a dc
-// value change places between the halves of the wavefront, so one register
-// holds both from there on.
-__device__ __forceinline__ float swap_halves_add(float x, float y) {  // x's sum in the lower half, y's in the upper
+// x's sum over both halves (or over both rows of a pair) in the lower half
+// (even rows), y's in the upper half (odd rows).
+__device__ __forceinline__ float halves_add(float x, float y) {
   const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y),
                                                   false, false);
   return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
 }
-
-template <int SL>
-__device__ __forceinline__ float row_groups_sum(float v) {  // over the groups of a row of 16 lanes
-  if constexpr (SL <= 8) v += dpp<kRor8>(v);
-  if constexpr (SL <= 4) v += dpp<kRor4>(v);
-  return v;
+__device__ __forceinline__ float rows_add(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y),
+                                                  false, false);
+  return __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
 }
 
-constexpr int kSub = 8;        // positions whose states are in registers together
-constexpr int kSubs = 8;       // sub-chunks of a chunk at most: kSub * kSubs positions
-
-// Sub-chunk after sub-chunk from the end of the chunk: the states that enter
-// each are in LDS (from one sweep along the chunk), its kSub states are run
-// again into registers, then the gradient comes back through them.
-template <int DT, int SL, int SPL>
-__global__ __launch_bounds__(256) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo g, const Elem<DT>* __restrict__ dy,
-                                                       const float* __restrict__ states,
-                                                       const float* __restrict__ backs, ScanOut<DT> out) {
+// db and dc of one position summed over the wavefront's groups (the lanes of
+// equal state index) into out[2][NS]: db and dc part at the halves, then two
+// states at the rows, so every step adds half as many registers; the rest of
+// the sum is within rows of 16 lanes.
+template <int SL, int SPL>
+__device__ __forceinline__ void sum_groups(const float (&db)[SPL], const float (&dc)[SPL], float* out, int s0) {
   constexpr int NS = SL * SPL;
-  static_assert(kSub == kTile, "b and c are staged by sub-chunk");
+  const int lane = threadIdx.x & 63, half = lane >> 5, row = lane >> 4 & 1;
+  float v[SPL];
+#pragma unroll
+  for (int s = 0; s < SPL; ++s) v[s] = halves_add(db[s], dc[s]);
+#pragma unroll
+  for (int s = 0; s < SPL; s += 2) {
+    float w = SPL > 1 ? rows_add(v[s], v[s + 1 < SPL ? s + 1 : s]) : add_row_pairs(v[s]);
+    if constexpr (SL <= 8) w += dpp<kRor8>(w);
+    if constexpr (SL <= 4) w += dpp<kRor4>(w);
+    if ((lane & 15) < SL && s + row < SPL) out[half * NS + s0 + s + row] = w;
+  }
+}
+
+// Tile after tile from the end of the chunk: the tile's states are run again
+// into registers from the kept one, then the gradient comes back through them.
+template <int DT, int SL, int SPL>
+__global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo g, const Elem<DT>* __restrict__ dy,
+                                                       const float* __restrict__ states,
+                                                       const float* __restrict__ backs, Kept kept, ScanOut<DT> out) {
+  constexpr int NS = SL * SPL;
   __shared__ __attribute__((aligned(16))) float bc[kTile * 2 * NS];
-  __shared__ float part[2][kWaves][kSub][2 * NS];
-  __shared__ float kept[kWaves][kSubs - 1][4 * SPL][64];
+  __shared__ float part[2][kWaves][kTile][2 * NS];
   int64_t n;
   int32_t chunk, wave_d0;
   locate<SL, SPL>(g, n, chunk, wave_d0);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int wave = threadIdx.x >> 6;
   const Place<SL, SPL> at(wave_d0, g.d);
   const int32_t len = valid_len(in.lengths, n, g.l);
   const int32_t t_begin = chunk * g.chunk;
   const int32_t t_end = t_begin + g.chunk < g.l ? t_begin + g.chunk : g.l;
   const int32_t t_valid = t_end < len ? t_end : len;
-  const int32_t subs = (t_end - t_begin + kSub - 1) / kSub;
   const int64_t c_id = n * g.chunks + chunk, ds = int64_t(g.d) * g.s;
 
-  float a2[4][SPL], h[4][SPL], carry[4][SPL], da[4][SPL];
+  float a2[4][SPL], carry[4][SPL], da[4][SPL];
   load_states<SL, SPL>(a2, in.a, at, g);
-  load_states<SL, SPL>(h, states + c_id * ds, at, g);
   load_states<SL, SPL>(carry, backs + c_id * ds, at, g);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, da[j][i] = 0.0f;
-  const float bias = in.delta_bias && at.live ? in.delta_bias[at.d] : 0.0f;
-  const float skip = in.skip && at.live ? in.skip[at.d] : 0.0f;
-  const Elem<DT>* un = in.u + n * g.us[0] + at.d;
-  const Elem<DT>* dn = in.delta + n * g.ds[0] + at.d;
-  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] + at.d : nullptr;
-  const Elem<DT>* yn = dy + n * g.ys[0] + at.d;
+  const float bias = in.delta_bias ? in.delta_bias[at.at] : 0.0f;
+  const float skip = in.skip ? in.skip[at.at] : 0.0f;
+  const Elem<DT>* un = in.u + n * g.us[0];
+  const Elem<DT>* dn = in.delta + n * g.ds[0];
+  const Elem<DT>* gn = in.gate ? in.gate + n * g.gs[0] : nullptr;
+  const Elem<DT>* yn = dy + n * g.ys[0];
   const Elem<DT>* bn = in.b + n * g.bs[0];
   const Elem<DT>* cn = in.c + n * g.cs[0];
-  const int64_t o_n = n * g.l * int64_t(g.d) + at.d;
+  const int64_t out_n = n * g.l * int64_t(g.d);
 
   StagedBC<DT, NS> st;
-  // D and u of a sub-chunk's positions, 0 past the valid ones
-  auto steps = [&](int32_t t0, float (&df)[kSub], float (&uf)[kSub], float (&sg)[kSub]) {
-    Elem<DT> u_t[kSub], d_t[kSub];
-#pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-      const bool ok = at.live && t0 + i < t_valid;
-      u_t[i] = ok ? un[(t0 + i) * g.us[1]] : Elem<DT>(0);
-      d_t[i] = ok ? dn[(t0 + i) * g.ds[1]] : Elem<DT>(0);
-    }
-#pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-      uf[i] = to_f<DT>(u_t[i]);
-      float dl = to_f<DT>(d_t[i]) + bias;
-      sg[i] = 1.0f;
-      if (g.softplus) dl = softplus(dl, sg[i]);
-      df[i] = t0 + i < t_valid && at.live ? dl : 0.0f;
-    }
-  };
-  float df[kSub], uf[kSub], sg[kSub];
-  for (int32_t k = 0; k < subs - 1; ++k) {
-    const int32_t t0 = t_begin + k * kSub;
-    st.stage(bn, cn, g, t0, t_valid);
-    steps(t0, df, uf, sg);
-    __syncthreads();
-    st.put(bc);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-      float dq[4], xq[4], bf[SPL];
-      quad_all(df[i], dq);
-      quad_all(df[i] * uf[i], xq);
-      lds_states<SPL>(&bc[i * 2 * NS + at.s0], bf);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int s = 0; s < SPL; ++s)
-          h[j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq[j] * a2[j][s]), h[j][s], xq[j] * bf[s]);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int s = 0; s < SPL; ++s) kept[wave][k][j * SPL + s][lane] = h[j][s];
-  }
-
   float dskip = 0.0f, dbias = 0.0f;
   const int64_t rows = (int64_t(gridDim.x) / (int64_t(g.col_blocks) * g.chunks)) * g.l;  // N * L
   const int64_t col = blockIdx.x % g.col_blocks;
-  for (int32_t k = subs - 1; k >= 0; --k) {
-    const int32_t t0 = t_begin + k * kSub;
+  for (int32_t k = (t_end - t_begin + kTile - 1) / kTile - 1; k >= 0; --k) {
+    const int32_t t0 = t_begin + k * kTile;
     st.stage(bn, cn, g, t0, t_valid);
-    steps(t0, df, uf, sg);
-    float yf[kSub], zf[kSub];
+    float df[kTile], uf[kTile], sg[kTile], yf[kTile], zf[kTile];
     {
-      Elem<DT> y_t[kSub], g_t[kSub];
+      Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile] = {}, y_t[kTile];
+      load_tile<DT>(u_t, un, g.us[1], at.at, t0, t_valid);
+      load_tile<DT>(d_t, dn, g.ds[1], at.at, t0, t_valid);
+      load_tile<DT>(y_t, yn, g.ys[1], at.at, t0, t_valid);
+      if (gn) load_tile<DT>(g_t, gn, g.gs[1], at.at, t0, t_valid);
 #pragma unroll
-      for (int i = 0; i < kSub; ++i) {
-        const bool ok = at.live && t0 + i < t_valid;
-        y_t[i] = ok ? yn[(t0 + i) * g.ys[1]] : Elem<DT>(0);
-        g_t[i] = ok && gn ? gn[(t0 + i) * g.gs[1]] : Elem<DT>(0);
+      for (int i = 0; i < kTile; ++i) {
+        uf[i] = to_f<DT>(u_t[i]);
+        df[i] = to_f<DT>(d_t[i]) + bias;
+        yf[i] = to_f<DT>(y_t[i]);
+        zf[i] = to_f<DT>(g_t[i]);
+        sg[i] = 1.0f;
       }
+    }
+    // the state that enters the tile
+    float hs[kTile + 1][4][SPL];
+    load_states<SL, SPL>(hs[0], states + c_id * ds, at, g);
+    if (k > 0 && t0 < t_valid) {
+      const int64_t o = kept_at<SPL>(g, k);
+      const int64_t w = (o >> 6) * SPL * 64 + (o & 63);
+      float sq[4];
+      quad_all(kept.sum[o], sq);
 #pragma unroll
-      for (int i = 0; i < kSub; ++i) yf[i] = to_f<DT>(y_t[i]), zf[i] = to_f<DT>(g_t[i]);
+      for (int i = 0; i < SPL; ++i) {
+        const float4 f = kept.h[w + i * 64];
+        const float hk[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          hs[0][j][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(sq[j] * a2[j][i]), hs[0][j][i], hk[j]);
+      }
     }
     __syncthreads();
     st.put(bc);
     __syncthreads();
-    float hs[kSub + 1][4][SPL];
-    if (k > 0) {
+    if (g.softplus) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int s = 0; s < SPL; ++s) hs[0][j][s] = kept[wave][k - 1][j * SPL + s][lane];
-    } else {
-      load_states<SL, SPL>(hs[0], states + c_id * ds, at, g);
+      for (int i = 0; i < kTile; ++i) df[i] = softplus(df[i], sg[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
+    for (int i = 0; i < kTile; ++i) {
+      df[i] = t0 + i < t_valid && at.live ? df[i] : 0.0f;
       float dq[4], xq[4], bf[SPL];
       quad_all(df[i], dq);
       quad_all(df[i] * uf[i], xq);
@@ -690,10 +730,10 @@ __global__ __launch_bounds__(256) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo g,
 #pragma unroll
         for (int s = 0; s < SPL; ++s)
           hs[i + 1][j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq[j] * a2[j][s]), hs[i][j][s], xq[j] * bf[s]);
+      settle(hs[i + 1]);
     }
-    float (&pt)[kSub][2 * NS] = part[k & 1][wave];
 #pragma unroll
-    for (int i = kSub - 1; i >= 0; --i) {
+    for (int i = kTile - 1; i >= 0; --i) {
       const float z = zf[i];
       const float sz = in.gate ? sigmoid(z) : 0.0f;
       const float gy = in.gate ? yf[i] * z * sz : yf[i];
@@ -723,34 +763,32 @@ __global__ __launch_bounds__(256) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo g,
           carry[j][s] = e * gr;
         }
       }
+      settle(carry);
+      settle(da);
       const float yo = own_sum<SL>(yq), bo = own_sum<SL>(bq), eo = own_sum<SL>(eq);
       const bool valid = t0 + i < t_valid && at.live;
       const float dd = valid ? (eo * kLn2 + uf[i] * bo) * sg[i] : 0.0f;
       dbias += dd;
       dskip = __builtin_fmaf(gy, uf[i], dskip);
       if (at.first && t0 + i < t_end) {
-        const int64_t o = o_n + (t0 + i) * int64_t(g.d);
-        out.u[o] = from_f<DT>(valid ? __builtin_fmaf(df[i], bo, skip * gy) : 0.0f);
-        out.delta[o] = from_f<DT>(dd);
+        const int64_t o = out_n + (t0 + i) * int64_t(g.d);
+        (out.u + o)[at.at] = from_f<DT>(valid ? __builtin_fmaf(df[i], bo, skip * gy) : 0.0f);
+        (out.delta + o)[at.at] = from_f<DT>(dd);
         if (in.gate) {
           const float dz = yf[i] * __builtin_fmaf(skip, uf[i], yo) * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
-          out.gate[o] = from_f<DT>(valid ? dz : 0.0f);
+          (out.gate + o)[at.at] = from_f<DT>(valid ? dz : 0.0f);
         }
       }
-      // over the wavefront's channels
-#pragma unroll
-      for (int s = 0; s < SPL; ++s) {
-        const float v = row_groups_sum<SL>(add_row_pairs(swap_halves_add(db[s], dc[s])));
-        if ((lane & 31) < SL) pt[i][(lane >> 5) * NS + at.s0 + s] = v;
-      }
+      sum_groups<SL, SPL>(db, dc, part[k & 1][wave][i], at.s0);
     }
     __syncthreads();
-    // the workgroup's channels; the buffer is used again two sub-chunks later
-    for (int i = threadIdx.x; i < kSub * 2 * NS; i += blockDim.x) {
+    // the workgroup's channels; the buffer is used again two tiles later
+    for (int i = threadIdx.x; i < kTile * 2 * NS; i += 256) {
       const int t = i / (2 * NS), q = i % (2 * NS), which = q / NS, s = q % NS;
       if (t0 + t >= t_valid || s >= g.s) continue;
       float v = part[k & 1][0][t][q];
-      for (int w = 1; w < waves; ++w) v += part[k & 1][w][t][q];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += part[k & 1][w][t][q];
       out.bc_part[((col * rows + n * g.l + t0 + t) * 2 + which) * g.s + s] = v;
     }
   }
@@ -831,13 +869,10 @@ auto with_dtype(int32_t dt, F&& f) {
   return f(Int<CNHWC_BF16>{});
 }
 
-int32_t channels_per_wave(int32_t s) { return s <= 16 ? 64 : (s <= 32 ? 32 : 16); }
-
-// Wavefronts of a workgroup and workgroups along the channels.
-void columns(const cnhwc_scan_desc_t& d, int32_t* waves, int32_t* col_blocks) {
-  const int64_t w = ceil_div(d.d, channels_per_wave(d.s));
-  *waves = int32_t(w < kWaves ? w : kWaves);
-  *col_blocks = int32_t(ceil_div(w, *waves));
+// Workgroups along the channels, of kWaves wavefronts each.
+int32_t columns(const cnhwc_scan_desc_t& d) {
+  const int64_t channels = d.s <= 16 ? 64 : (d.s <= 32 ? 32 : 16);  // per wavefront, as Place has them
+  return int32_t(ceil_div(d.d, channels * kWaves));
 }
 
 // Positions per chunk of the forward pass.
@@ -851,9 +886,7 @@ void columns(const cnhwc_scan_desc_t& d, int32_t* waves, int32_t* col_blocks) {
 #define SCAN_MIN 32
 #endif
 int32_t fwd_chunk(const cnhwc_scan_desc_t& d) {
-  int32_t waves, cols;
-  columns(d, &waves, &cols);
-  const int64_t one = d.n * cols * waves;
+  const int64_t one = d.n * columns(d) * kWaves;
   int64_t chunk = d.l;
   if (one < SCAN_ONE) {
     chunk = ceil_div(d.l * one, SCAN_WAVES);
@@ -862,7 +895,10 @@ int32_t fwd_chunk(const cnhwc_scan_desc_t& d) {
   return int32_t(ceil_div(chunk, kTile) * kTile);
 }
 
-constexpr int32_t kBwdChunk = kSub * kSubs;
+#ifndef SCAN_BC
+#define SCAN_BC 64
+#endif
+constexpr int32_t kBwdChunk = SCAN_BC;
 
 uint64_t fwd_bytes(const cnhwc_scan_desc_t& d) {
   const int64_t chunks = ceil_div(d.l, fwd_chunk(d));
@@ -870,11 +906,10 @@ uint64_t fwd_bytes(const cnhwc_scan_desc_t& d) {
 }
 
 struct BwdLayout {
-  uint64_t states, backs, sums, bc, params, total;
+  uint64_t states, backs, sums, bc, params, kept_h, kept_sum, total;
 };
 BwdLayout bwd_layout(const cnhwc_scan_desc_t& d) {
-  int32_t waves, cols;
-  columns(d, &waves, &cols);
+  const uint64_t cols = columns(d);
   const uint64_t nc = uint64_t(d.n) * ceil_div(d.l, kBwdChunk), ds = uint64_t(d.d) * d.s;
   BwdLayout L;
   uint64_t at = 0;
@@ -886,8 +921,12 @@ BwdLayout bwd_layout(const cnhwc_scan_desc_t& d) {
   L.states = take(nc * ds);
   L.backs = take(nc * ds);
   L.sums = take(nc * d.d);
-  L.bc = take(uint64_t(cols) * d.n * d.l * 2 * d.s);
+  L.bc = take(cols * d.n * d.l * 2 * d.s);
   L.params = take(nc * (ds + 2 * uint64_t(d.d)));
+  const uint64_t lanes = nc * cols * (kBwdChunk / kTile) * 256;
+  const uint64_t spl = d.s <= 4 ? 1 : (d.s <= 8 ? 2 : 4);
+  L.kept_h = take(lanes * 4 * spl);
+  L.kept_sum = take(lanes);
   L.total = at;
   return L;
 }
@@ -955,11 +994,10 @@ extern "C" cnhwc_status_t cnhwc_scan_fwd(const cnhwc_scan_desc_t* desc, const cn
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   ScanGeo g = geo_of(d);
-  int32_t waves;
-  columns(d, &waves, &g.col_blocks);
+  g.col_blocks = columns(d);
   g.chunk = fwd_chunk(d);
   g.chunks = int32_t(ceil_div(d.l, g.chunk));
-  const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(waves * 64);
+  const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(256);
   float* states = static_cast<float*>(workspace);
   float* sums = states + d.n * g.chunks * d.d * d.s;
   return with_dtype(d.dtype, [&](auto dt) {
@@ -1020,17 +1058,17 @@ extern "C" cnhwc_status_t cnhwc_scan_bwd(const cnhwc_scan_desc_t* desc, const cn
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   ScanGeo g = geo_of(d);
-  int32_t waves;
-  columns(d, &waves, &g.col_blocks);
+  g.col_blocks = columns(d);
   g.chunk = kBwdChunk;
   g.chunks = int32_t(ceil_div(d.l, g.chunk));
-  const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(waves * 64);
+  const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(256);
   char* ws = static_cast<char*>(workspace);
   float* states = reinterpret_cast<float*>(ws + L.states);
   float* backs = reinterpret_cast<float*>(ws + L.backs);
   float* sums = reinterpret_cast<float*>(ws + L.sums);
   float* bc = reinterpret_cast<float*>(ws + L.bc);
   float* params = reinterpret_cast<float*>(ws + L.params);
+  const Kept kept{reinterpret_cast<float4*>(ws + L.kept_h), reinterpret_cast<float*>(ws + L.kept_sum)};
   return with_dtype(d.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     using E = Elem<DT>;
@@ -1040,11 +1078,12 @@ extern "C" cnhwc_status_t cnhwc_scan_bwd(const cnhwc_scan_desc_t* desc, const cn
                          params};
     with_shape(d.s, [&](auto sh) {
       constexpr int SL = decltype(sh)::sl, SPL = decltype(sh)::spl;
-      hipLaunchKernelGGL((scan_bwd_local_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, sums);
+      hipLaunchKernelGGL((scan_bwd_local_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, sums,
+                         kept);
       const int64_t total = d.n * d.d * d.s;
       hipLaunchKernelGGL(scan_bwd_join_kernel, grid_of(ceil_div(total, 256)), dim3(256), 0, s, states, backs, sums,
                          in->a, in->state, dstate_out, grads->state, g, total);
-      hipLaunchKernelGGL((scan_bwd_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, so);
+      hipLaunchKernelGGL((scan_bwd_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, kept, so);
     });
     const int64_t bc_total = d.n * d.l * 2 * d.s;
     hipLaunchKernelGGL((scan_bwd_bc_kernel<DT>), grid_of(ceil_div(bc_total, 256)), dim3(256), 0, s, bc, in->lengths,

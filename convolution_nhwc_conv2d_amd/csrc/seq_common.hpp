@@ -82,7 +82,7 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;         // lanes 1032, 2301 of a quad
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kQuadReverse = 0x1B;  // lanes 1032, 2301, 3210 of a quad
 constexpr int kHalfMirror = 0x141, kRowMirror = 0x140;    // reversed 8 or 16 lanes
 constexpr int kRor8 = 0x128, kRor4 = 0x124;               // rows of 16 rotated
 constexpr int kQuadBcast = 0x55;                          // times j: lane j of each quad
