@@ -33,6 +33,7 @@ namespace seq {
 namespace {
 
 constexpr int kTile = 8;    // positions whose loads are issued together
+constexpr int kHalf = kTile / 2;
 constexpr int kWaves = 4;   // wavefronts of a workgroup
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
@@ -138,12 +139,15 @@ __device__ __forceinline__ void store_states(const float (&h)[4][SPL], float* __
 // The values are computed here and not later: without this the compiler moves
 // a tile's whole arithmetic behind the next tile's staging and holds the
 // operands of all its positions in registers meanwhile.
+template <int N>
+__device__ __forceinline__ void settle(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
 template <int SPL>
 __device__ __forceinline__ void settle(float (&h)[4][SPL]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int i = 0; i < SPL; ++i) asm volatile("" : "+v"(h[j][i]));
+  for (int j = 0; j < 4; ++j) settle(h[j]);
 }
 
 // One float of each lane of the quad, in all four.
@@ -601,6 +605,22 @@ __global__ __launch_bounds__(256) void scan_bwd_join_kernel(float* __restrict__ 
   }
 }
 
+// Two elements as they were loaded, in one register where they are 16 bits.
+template <int DT>
+struct Two {
+  uint32_t v;
+  __device__ __forceinline__ void set(uint16_t a, uint16_t b) { v = uint32_t(b) << 16 | a; }
+  __device__ __forceinline__ float first() const { return to_f<DT>(uint16_t(v)); }
+  __device__ __forceinline__ float second() const { return to_f<DT>(uint16_t(v >> 16)); }
+};
+template <>
+struct Two<CNHWC_F32> {
+  float a, b;
+  __device__ __forceinline__ void set(float x, float y) { a = x, b = y; }
+  __device__ __forceinline__ float first() const { return a; }
+  __device__ __forceinline__ float second() const { return b; }
+};
+
 // x's sum over both halves (or over both rows of a pair) in the lower half
 // (even rows), y's in the upper half (odd rows).
 __device__ __forceinline__ float halves_add(float x, float y) {
@@ -643,10 +663,11 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
   constexpr int NS = SL * SPL;
   __shared__ __attribute__((aligned(16))) float bc[kTile * 2 * NS];
   __shared__ float part[2][kWaves][kTile][2 * NS];
+  __shared__ float4 enter[kWaves][SPL][64];  // the state that enters the chunk
   int64_t n;
   int32_t chunk, wave_d0;
   locate<SL, SPL>(g, n, chunk, wave_d0);
-  const int wave = threadIdx.x >> 6;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const Place<SL, SPL> at(wave_d0, g.d);
   const int32_t len = valid_len(in.lengths, n, g.l);
   const int32_t t_begin = chunk * g.chunk;
@@ -655,6 +676,9 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
   const int64_t c_id = n * g.chunks + chunk, ds = int64_t(g.d) * g.s;
 
   float a2[4][SPL], carry[4][SPL], da[4][SPL];
+  load_states<SL, SPL>(a2, states + c_id * ds, at, g);
+#pragma unroll
+  for (int i = 0; i < SPL; ++i) enter[wave][i][lane] = make_float4(a2[0][i], a2[1][i], a2[2][i], a2[3][i]);
   load_states<SL, SPL>(a2, in.a, at, g);
   load_states<SL, SPL>(carry, backs + c_id * ds, at, g);
 #pragma unroll
@@ -678,25 +702,29 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
   for (int32_t k = (t_end - t_begin + kTile - 1) / kTile - 1; k >= 0; --k) {
     const int32_t t0 = t_begin + k * kTile;
     st.stage(bn, cn, g, t0, t_valid);
-    float df[kTile], uf[kTile], sg[kTile], yf[kTile], zf[kTile];
+    float df[kTile], sg[kTile];
+    Elem<DT> u_t[kTile];
+    Two<DT> yz[kTile];  // dy and gate
+    load_tile<DT>(u_t, un, g.us[1], at.at, t0, t_valid);
     {
-      Elem<DT> u_t[kTile], d_t[kTile], g_t[kTile] = {}, y_t[kTile];
-      load_tile<DT>(u_t, un, g.us[1], at.at, t0, t_valid);
+      Elem<DT> d_t[kTile], g_t[kTile] = {}, y_t[kTile];
       load_tile<DT>(d_t, dn, g.ds[1], at.at, t0, t_valid);
       load_tile<DT>(y_t, yn, g.ys[1], at.at, t0, t_valid);
       if (gn) load_tile<DT>(g_t, gn, g.gs[1], at.at, t0, t_valid);
 #pragma unroll
       for (int i = 0; i < kTile; ++i) {
-        uf[i] = to_f<DT>(u_t[i]);
         df[i] = to_f<DT>(d_t[i]) + bias;
-        yf[i] = to_f<DT>(y_t[i]);
-        zf[i] = to_f<DT>(g_t[i]);
+        yz[i].set(y_t[i], g_t[i]);
         sg[i] = 1.0f;
       }
     }
     // the state that enters the tile
-    float hs[kTile + 1][4][SPL];
-    load_states<SL, SPL>(hs[0], states + c_id * ds, at, g);
+    float h0[4][SPL];
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+      const float4 f = enter[wave][i][lane];
+      h0[0][i] = f.x, h0[1][i] = f.y, h0[2][i] = f.z, h0[3][i] = f.w;
+    }
     if (k > 0 && t0 < t_valid) {
       const int64_t o = kept_at<SPL>(g, k);
       const int64_t w = (o >> 6) * SPL * 64 + (o & 63);
@@ -708,7 +736,7 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
         const float hk[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          hs[0][j][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(sq[j] * a2[j][i]), hs[0][j][i], hk[j]);
+          h0[j][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(sq[j] * a2[j][i]), h0[j][i], hk[j]);
       }
     }
     __syncthreads();
@@ -718,31 +746,56 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
 #pragma unroll
       for (int i = 0; i < kTile; ++i) df[i] = softplus(df[i], sg[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      df[i] = t0 + i < t_valid && at.live ? df[i] : 0.0f;
+    // one position further; what a position needs of its quad and of b is made
+    // again at each use (again() hides that it is the same), for the registers
+    auto again = [](float v) {
+      asm volatile("" : "+v"(v));
+      return v;
+    };
+    auto advance = [&](int i, const float (&from)[4][SPL], float (&to)[4][SPL]) {
       float dq[4], xq[4], bf[SPL];
-      quad_all(df[i], dq);
-      quad_all(df[i] * uf[i], xq);
-      lds_states<SPL>(&bc[i * 2 * NS + at.s0], bf);
+      const float dl = again(df[i]);
+      quad_all(dl, dq);
+      quad_all(dl * to_f<DT>(u_t[i]), xq);
+      int s0 = at.s0;
+      asm volatile("" : "+v"(s0));
+      lds_states<SPL>(&bc[i * 2 * NS + s0], bf);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int s = 0; s < SPL; ++s)
-          hs[i + 1][j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq[j] * a2[j][s]), hs[i][j][s], xq[j] * bf[s]);
-      settle(hs[i + 1]);
-    }
+          to[j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq[j] * a2[j][s]), from[j][s], xq[j] * bf[s]);
+      settle(to);
+    };
+#pragma unroll
+    for (int i = 0; i < kTile; ++i) df[i] = t0 + i < t_valid && at.live ? df[i] : 0.0f;
+    // half a tile's states are held at a time: all eight would take 64 registers more
+    float hs[kHalf + 1][4][SPL];
+    advance(0, h0, hs[0]);
+#pragma unroll
+    for (int i = 1; i < kHalf; ++i) advance(i, hs[0], hs[0]);
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) advance(kHalf + i, hs[i], hs[i + 1]);
 #pragma unroll
     for (int i = kTile - 1; i >= 0; --i) {
-      const float z = zf[i];
+      if (i == kHalf - 1) {
+#pragma unroll
+        for (int q = 0; q < kHalf; ++q) advance(q, q == 0 ? h0 : hs[q], hs[q + 1]);
+      }
+      const float (&before)[4][SPL] = i == 0 ? h0 : hs[i % kHalf];
+      const float (&after)[4][SPL] = hs[i % kHalf + 1];
+      const float u = to_f<DT>(u_t[i]), yg = yz[i].first(), z = yz[i].second();
       const float sz = in.gate ? sigmoid(z) : 0.0f;
-      const float gy = in.gate ? yf[i] * z * sz : yf[i];
+      const float gy = in.gate ? yg * z * sz : yg;
       float dq[4], xq[4], gq[4], bf[SPL], cf[SPL], db[SPL], dc[SPL];
-      quad_all(df[i], dq);
-      quad_all(df[i] * uf[i], xq);
+      const float dl = again(df[i]);
+      quad_all(dl, dq);
+      quad_all(dl * u, xq);
       quad_all(gy, gq);
-      lds_states<SPL>(&bc[i * 2 * NS + at.s0], bf);
-      lds_states<SPL>(&bc[i * 2 * NS + NS + at.s0], cf);
+      int s0 = at.s0;
+      asm volatile("" : "+v"(s0));
+      lds_states<SPL>(&bc[i * 2 * NS + s0], bf);
+      lds_states<SPL>(&bc[i * 2 * NS + NS + s0], cf);
 #pragma unroll
       for (int s = 0; s < SPL; ++s) db[s] = dc[s] = 0.0f;
       float yq[4], bq[4], eq[4];
@@ -753,29 +806,31 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
         for (int s = 0; s < SPL; ++s) {
           const float e = __builtin_amdgcn_exp2f(dq[j] * a2[j][s]);
           const float gr = __builtin_fmaf(cf[s], gq[j], carry[j][s]);
-          const float w = gr * (e * hs[i][j][s]);
-          yq[j] = __builtin_fmaf(hs[i + 1][j][s], cf[s], yq[j]);
+          const float w = gr * (e * before[j][s]);
+          yq[j] = __builtin_fmaf(after[j][s], cf[s], yq[j]);
           bq[j] = __builtin_fmaf(gr, bf[s], bq[j]);
           eq[j] = __builtin_fmaf(w, a2[j][s], eq[j]);
           da[j][s] = __builtin_fmaf(w, dq[j], da[j][s]);
           db[s] = __builtin_fmaf(gr, xq[j], db[s]);
-          dc[s] = __builtin_fmaf(hs[i + 1][j][s], gq[j], dc[s]);
+          dc[s] = __builtin_fmaf(after[j][s], gq[j], dc[s]);
           carry[j][s] = e * gr;
         }
       }
       settle(carry);
       settle(da);
+      settle(db);
+      settle(dc);
       const float yo = own_sum<SL>(yq), bo = own_sum<SL>(bq), eo = own_sum<SL>(eq);
       const bool valid = t0 + i < t_valid && at.live;
-      const float dd = valid ? (eo * kLn2 + uf[i] * bo) * sg[i] : 0.0f;
+      const float dd = valid ? (eo * kLn2 + u * bo) * sg[i] : 0.0f;
       dbias += dd;
-      dskip = __builtin_fmaf(gy, uf[i], dskip);
+      dskip = __builtin_fmaf(gy, u, dskip);
       if (at.first && t0 + i < t_end) {
         const int64_t o = out_n + (t0 + i) * int64_t(g.d);
         (out.u + o)[at.at] = from_f<DT>(valid ? __builtin_fmaf(df[i], bo, skip * gy) : 0.0f);
         (out.delta + o)[at.at] = from_f<DT>(dd);
         if (in.gate) {
-          const float dz = yf[i] * __builtin_fmaf(skip, uf[i], yo) * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
+          const float dz = yg * __builtin_fmaf(skip, u, yo) * sz * __builtin_fmaf(z, 1.0f - sz, 1.0f);
           (out.gate + o)[at.at] = from_f<DT>(valid ? dz : 0.0f);
         }
       }
