@@ -150,12 +150,45 @@ __device__ __forceinline__ void settle(float (&h)[4][SPL]) {
   for (int j = 0; j < 4; ++j) settle(h[j]);
 }
 
-// One float of each lane of the quad, in all four.
-__device__ __forceinline__ void quad_all(float v, float (&out)[4]) {
-  out[0] = dpp<0>(v);
-  out[1] = dpp<1 * kQuadBcast>(v);
-  out[2] = dpp<2 * kQuadBcast>(v);
-  out[3] = dpp<3 * kQuadBcast>(v);
+template <int SPL>
+__device__ __forceinline__ void copy(const float (&from)[4][SPL], float (&to)[4][SPL]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) to[j][i] = from[j][i];
+}
+
+// The value of lane j of the quad (j a constant after unrolling): as an operand
+// of a product it costs no instruction of its own.
+__device__ __forceinline__ float quad_lane(float v, int j) {
+  switch (j) {
+    case 0: return dpp<0 * kQuadBcast>(v);
+    case 1: return dpp<1 * kQuadBcast>(v);
+    case 2: return dpp<2 * kQuadBcast>(v);
+    default: return dpp<3 * kQuadBcast>(v);
+  }
+}
+
+// Four channels by SPL states per lane, in the order of the lanes:
+// [workgroup][wavefront][SPL][64 lanes] of the four channels' values.
+template <int SPL>
+__device__ __forceinline__ int64_t lane_order(int64_t workgroup) {
+  return (workgroup * kWaves + (threadIdx.x >> 6)) * (SPL * 64) + (threadIdx.x & 63);
+}
+template <int SPL>
+__device__ __forceinline__ void put_lanes(float4* __restrict__ p, int64_t workgroup, const float (&h)[4][SPL]) {
+  const int64_t at = lane_order<SPL>(workgroup);
+#pragma unroll
+  for (int i = 0; i < SPL; ++i) p[at + i * 64] = make_float4(h[0][i], h[1][i], h[2][i], h[3][i]);
+}
+template <int SPL>
+__device__ __forceinline__ void get_lanes(const float4* __restrict__ p, int64_t workgroup, float (&h)[4][SPL]) {
+  const int64_t at = lane_order<SPL>(workgroup);
+#pragma unroll
+  for (int i = 0; i < SPL; ++i) {
+    const float4 f = p[at + i * 64];
+    h[0][i] = f.x, h[1][i] = f.y, h[2][i] = f.z, h[3][i] = f.w;
+  }
 }
 
 // Of the four channels' sums over the group's lanes, the own channel's: lanes
@@ -210,37 +243,29 @@ __device__ __forceinline__ void lds_states(const float* p, float (&f)[SPL]) {
 
 // Workgroup -> sequence, chunk, first channel of this wavefront.
 template <int SL, int SPL>
-__device__ __forceinline__ void locate(const ScanGeo& g, int64_t& n, int32_t& chunk, int32_t& wave_d0) {
+__device__ __forceinline__ void locate(const ScanGeo& g, int32_t chunks, int64_t& n, int32_t& chunk,
+                                       int32_t& wave_d0) {
   const int64_t row = blockIdx.x / g.col_blocks;
   const int32_t col = int32_t(blockIdx.x - row * g.col_blocks);
-  n = row / g.chunks;
-  chunk = int32_t(row - n * g.chunks);
+  n = row / chunks;
+  chunk = int32_t(row - n * chunks);
   wave_d0 = __builtin_amdgcn_readfirstlane((col * kWaves + int32_t(threadIdx.x >> 6)) * Place<SL, SPL>::kChannels);
 }
 
-#ifndef SCAN_OCCL
-#define SCAN_OCCL 2
-#endif
-#ifndef SCAN_OCCB
-#define SCAN_OCCB 2
-#endif
-#ifndef SCAN_OCC
-#define SCAN_OCC 1
-#endif
 // ---------------------------------------------------------------- forward
 
-// LOCAL: the chunk from a zero state; ends [n,chunk,D,S] and sums [n,chunk,D].
-// Otherwise the outputs, from the entering states `starts` ([n,chunk,D,S], or
-// the initial state where there is one chunk) and, with one chunk, state_out.
+// LOCAL: every chunk but the last of its sequence from a zero state; its end
+// state and sum of D, in lane order.  Otherwise the outputs, from the entering
+// states (the first chunk's is the initial one), and the final state.
 template <int DT, int SL, int SPL, bool LOCAL>
-__global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g, Elem<DT>* __restrict__ y,
-                                                       float* __restrict__ states, float* __restrict__ sums,
+__global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g, Elem<DT>* __restrict__ y,
+                                                       float4* __restrict__ states, float* __restrict__ sums,
                                                        float* __restrict__ state_out) {
   constexpr int NS = SL * SPL;
   __shared__ __attribute__((aligned(16))) float bc[2][kTile * 2 * NS];
   int64_t n;
   int32_t chunk, wave_d0;
-  locate<SL, SPL>(g, n, chunk, wave_d0);
+  locate<SL, SPL>(g, LOCAL ? g.chunks - 1 : g.chunks, n, chunk, wave_d0);
   const Place<SL, SPL> at(wave_d0, g.d);
   const int32_t len = valid_len(in.lengths, n, g.l);
   const int32_t t_begin = chunk * g.chunk;
@@ -255,7 +280,7 @@ __global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, 
     for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, h[j][i] = 0.0f;
   const int64_t ds = int64_t(g.d) * g.s;
   if constexpr (!LOCAL) {
-    if (g.chunks > 1) load_states<SL, SPL>(h, states + (n * g.chunks + chunk) * ds, at, g);
+    if (chunk > 0) get_lanes<SPL>(states, blockIdx.x, h);
     else if (in.state) load_states<SL, SPL>(h, in.state + n * ds, at, g);
   }
   const float bias = in.delta_bias ? in.delta_bias[at.at] : 0.0f;
@@ -302,9 +327,7 @@ __global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, 
     for (int i = 0; i < kTile; ++i) {
       const bool valid = t0 + i < t_valid;
       const float dl = valid && at.live ? df[i] : 0.0f;
-      float dq[4], xq[4];
-      quad_all(dl, dq);
-      quad_all(dl * uf[i], xq);
+      const float dx = dl * uf[i];
       if (LOCAL) sum += dl;
       float bf[SPL], cf[SPL], yq[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       lds_states<SPL>(&bc[buf][i * 2 * NS + at.s0], bf);
@@ -313,8 +336,8 @@ __global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, 
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int k = 0; k < SPL; ++k) {
-          const float e = __builtin_amdgcn_exp2f(dq[j] * a2[j][k]);
-          h[j][k] = __builtin_fmaf(e, h[j][k], xq[j] * bf[k]);
+          const float e = __builtin_amdgcn_exp2f(quad_lane(dl, j) * a2[j][k]);
+          h[j][k] = __builtin_fmaf(e, h[j][k], quad_lane(dx, j) * bf[k]);
           if (!LOCAL) yq[j] = __builtin_fmaf(h[j][k], cf[k], yq[j]);
         }
       settle(h);
@@ -328,48 +351,78 @@ __global__ __launch_bounds__(256, SCAN_OCC) void scan_fwd_kernel(ScanIn<DT> in, 
     __syncthreads();
   }
   if constexpr (LOCAL) {
-    store_states<SL, SPL>(h, states + (n * g.chunks + chunk) * ds, at, g);
-    if (at.first) sums[(n * g.chunks + chunk) * int64_t(g.d) + at.d] = sum;
+    // at the next chunk's place, which this chunk's end enters
+    const int64_t next = blockIdx.x + (n + 1) * g.col_blocks;
+    put_lanes<SPL>(states, next, h);
+    sums[next * 256 + threadIdx.x] = sum;
   } else {
-    if (state_out) store_states<SL, SPL>(h, state_out + n * ds, at, g);
+    if (state_out && chunk == g.chunks - 1) store_states<SL, SPL>(h, state_out + n * ds, at, g);
   }
 }
 
-// Ends -> entering states of one (sequence, channel, state), in place; returns
-// the final state.  The chunks' values are loaded kJoin at a time: what they
-// are is known beforehand, only the sum along them is serial.
+// One value of the lane order: its sequence, place within a workgroup's chunks,
+// channel, state and decay.
+template <int SL, int SPL>
+struct Column {
+  int64_t n, at, step;      // first chunk's float in the lane order, floats to the next chunk
+  int64_t sum_at, sum_step;
+  int64_t user;             // in [N,D,S]
+  float a2;
+  bool live;
+  __device__ __forceinline__ Column(int64_t id, const float* __restrict__ a, const ScanGeo& g) {
+    constexpr int kWave = SPL * 64 * 4, kGroup = kWaves * kWave;  // floats
+    const int64_t per = int64_t(g.col_blocks) * kGroup;
+    n = id / per;
+    const int64_t r = id - n * per;
+    const int32_t wave = int32_t(r / kWave), q = int32_t(r % kWave);  // wavefront along the channels
+    const int32_t i = q / 256, lane = q / 4 % 64, j = q % 4;
+    const int64_t d = int64_t(wave) * Place<SL, SPL>::kChannels + lane / SL * 4 + j;
+    const int32_t s = lane % SL * SPL + i;
+    at = n * g.chunks * per + r;
+    step = per;
+    sum_at = (n * g.chunks * int64_t(g.col_blocks) * kWaves + wave) * 64 + (lane & ~3) + j;
+    sum_step = int64_t(g.col_blocks) * kWaves * 64;
+    live = d < g.d && s < g.s;
+    user = (n * g.d + d) * g.s + s;
+    a2 = live ? a[d * g.s + s] * kLog2e : 0.0f;
+  }
+};
+
+// The entering states of one value, in place, from its chunks' end states and
+// sums of D, of which chunk k's stand at k + ahead; returns the final state
+// where ahead is 0.  The chunks' values are loaded kJoin at a time: only the sum
+// along them is serial.
 constexpr int kJoin = 16;
-__device__ __forceinline__ float join_forward(float* state, const float* sum, float a2, float h, const ScanGeo& g) {
-  const int64_t ds = int64_t(g.d) * g.s;
-  for (int32_t k0 = 0; k0 < g.chunks; k0 += kJoin) {
+template <int SL, int SPL>
+__device__ __forceinline__ float join_forward(float* states, const float* sums, float h, const Column<SL, SPL>& c,
+                                              const ScanGeo& g, int ahead) {
+  for (int32_t k0 = ahead; k0 < g.chunks; k0 += kJoin) {
     float p[kJoin], e[kJoin];
 #pragma unroll
     for (int i = 0; i < kJoin; ++i) {
       const bool ok = k0 + i < g.chunks;
-      p[i] = ok ? state[(k0 + i) * ds] : 0.0f;
-      e[i] = ok ? sum[(k0 + i) * int64_t(g.d)] : 0.0f;
+      p[i] = ok ? states[c.at + (k0 + i) * c.step] : 0.0f;
+      e[i] = ok ? sums[c.sum_at + (k0 + i) * c.sum_step] : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < kJoin; ++i) {
       if (k0 + i >= g.chunks) break;
-      state[(k0 + i) * ds] = h;
-      h = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * e[i]), h, p[i]);
+      const float next = __builtin_fmaf(__builtin_amdgcn_exp2f(c.a2 * e[i]), h, p[i]);
+      states[c.at + (k0 + i) * c.step] = ahead ? next : h;
+      h = next;
     }
   }
   return h;
 }
 
-// Along the chunks: ends -> entering states, in place, and the final state.
+// Along the chunks: the states that enter all but the first.
+template <int SL, int SPL>
 __global__ __launch_bounds__(256) void scan_join_kernel(float* __restrict__ states, const float* __restrict__ sums,
                                                         const float* __restrict__ a, const float* __restrict__ state,
-                                                        float* __restrict__ state_out, ScanGeo g, int64_t total) {
-  const int64_t ds = int64_t(g.d) * g.s;
+                                                        ScanGeo g, int64_t total) {
   for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
-    const int64_t n = id / ds, at = id - n * ds, d = at / g.s;
-    const float a2 = a[at] * kLog2e;
-    float h = state ? state[id] : 0.0f;
-    h = join_forward(states + n * g.chunks * ds + at, sums + n * g.chunks * int64_t(g.d) + d, a2, h, g);
-    if (state_out) state_out[id] = h;
+    const Column<SL, SPL> c(id, a, g);
+    join_forward(states, sums, state && c.live ? state[c.user] : 0.0f, c, g, 1);
   }
 }
 
@@ -457,27 +510,22 @@ struct ScanOut {
   float* param_part;  // [N*chunks][D*S | D | D] sums of da, dskip, ddelta_bias
 };
 
-// Kept states: [workgroup][tile][wavefront][SPL][64 lanes] of four channels
-// each, and the sums of D [workgroup][tile][wavefront][64 lanes].
+// The kept states in lane order, [workgroup][tile], and their sums of D.
 struct Kept {
   float4* h;
   float* sum;
 };
-template <int SPL>
-__device__ __forceinline__ int64_t kept_at(const ScanGeo& g, int32_t tile) {
-  return ((int64_t(blockIdx.x) * (g.chunk / kTile) + tile) * kWaves + (threadIdx.x >> 6)) * 64 + (threadIdx.x & 63);
-}
 
 template <int DT, int SL, int SPL>
-__global__ __launch_bounds__(256, SCAN_OCCL) void scan_bwd_local_kernel(ScanIn<DT> in, ScanGeo g,
+__global__ __launch_bounds__(256, 2) void scan_bwd_local_kernel(ScanIn<DT> in, ScanGeo g,
                                                              const Elem<DT>* __restrict__ dy,
-                                                             float* __restrict__ states, float* __restrict__ backs,
+                                                             float4* __restrict__ states, float4* __restrict__ backs,
                                                              float* __restrict__ sums, Kept kept) {
   constexpr int NS = SL * SPL;
   __shared__ __attribute__((aligned(16))) float bc[2][kTile * 2 * NS];
   int64_t n;
   int32_t chunk, wave_d0;
-  locate<SL, SPL>(g, n, chunk, wave_d0);
+  locate<SL, SPL>(g, g.chunks, n, chunk, wave_d0);
   const Place<SL, SPL> at(wave_d0, g.d);
   const int32_t len = valid_len(in.lengths, n, g.l);
   const int32_t t_begin = chunk * g.chunk;
@@ -514,11 +562,9 @@ __global__ __launch_bounds__(256, SCAN_OCCL) void scan_bwd_local_kernel(ScanIn<D
   int buf = 0;
   for (int32_t t0 = t_begin; t0 < t_valid; t0 += kTile, buf ^= 1) {
     if (t0 > t_begin) {
-      const int64_t k = kept_at<SPL>(g, (t0 - t_begin) / kTile);
-      const int64_t w = (k >> 6) * SPL * 64 + (k & 63);
-#pragma unroll
-      for (int i = 0; i < SPL; ++i) kept.h[w + i * 64] = make_float4(h[0][i], h[1][i], h[2][i], h[3][i]);
-      kept.sum[k] = sum;
+      const int64_t k = int64_t(blockIdx.x) * (g.chunk / kTile) + (t0 - t_begin) / kTile;
+      put_lanes<SPL>(kept.h, k, h);
+      kept.sum[k * 256 + threadIdx.x] = sum;
     }
     float uf[kTile], df[kTile], gf[kTile], yf[kTile];
 #pragma unroll
@@ -540,10 +586,7 @@ __global__ __launch_bounds__(256, SCAN_OCCL) void scan_bwd_local_kernel(ScanIn<D
 #pragma unroll
     for (int i = 0; i < kTile; ++i) {
       const float dl = t0 + i < t_valid && at.live ? df[i] : 0.0f;
-      float dq[4], xq[4], gq[4];
-      quad_all(dl, dq);
-      quad_all(dl * uf[i], xq);
-      quad_all(yf[i], gq);
+      const float dx = dl * uf[i];
       sum += dl;
       float bf[SPL], cf[SPL];
       lds_states<SPL>(&bc[buf][i * 2 * NS + at.s0], bf);
@@ -552,10 +595,10 @@ __global__ __launch_bounds__(256, SCAN_OCCL) void scan_bwd_local_kernel(ScanIn<D
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int k = 0; k < SPL; ++k) {
-          const float e = __builtin_amdgcn_exp2f(dq[j] * a2[j][k]);
-          h[j][k] = __builtin_fmaf(e, h[j][k], xq[j] * bf[k]);
+          const float e = __builtin_amdgcn_exp2f(quad_lane(dl, j) * a2[j][k]);
+          h[j][k] = __builtin_fmaf(e, h[j][k], quad_lane(dx, j) * bf[k]);
           p[j][k] *= e;
-          r[j][k] = __builtin_fmaf(p[j][k], cf[k] * gq[j], r[j][k]);
+          r[j][k] = __builtin_fmaf(p[j][k], quad_lane(yf[i], j) * cf[k], r[j][k]);
         }
       settle(h);
       settle(r);
@@ -563,45 +606,40 @@ __global__ __launch_bounds__(256, SCAN_OCCL) void scan_bwd_local_kernel(ScanIn<D
     if (t0 + kTile < t_valid) st.put(bc[buf ^ 1]);
     __syncthreads();
   }
-  const int64_t c = n * g.chunks + chunk, ds = int64_t(g.d) * g.s;
-  store_states<SL, SPL>(h, states + c * ds, at, g);
-  store_states<SL, SPL>(r, backs + c * ds, at, g);
-  if (at.first) sums[c * int64_t(g.d) + at.d] = sum;
+  put_lanes<SPL>(states, blockIdx.x, h);
+  put_lanes<SPL>(backs, blockIdx.x, r);
+  sums[int64_t(blockIdx.x) * 256 + threadIdx.x] = sum;
 }
 
 // In place: ends -> entering states; what each chunk passes back -> the
 // gradient that enters at its end.  dstate: the initial state's gradient.
+template <int SL, int SPL>
 __global__ __launch_bounds__(256) void scan_bwd_join_kernel(float* __restrict__ states, float* __restrict__ backs,
                                                             const float* __restrict__ sums,
                                                             const float* __restrict__ a,
                                                             const float* __restrict__ state,
                                                             const float* __restrict__ dstate_out,
                                                             float* __restrict__ dstate, ScanGeo g, int64_t total) {
-  const int64_t ds = int64_t(g.d) * g.s;
   for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
-    const int64_t n = id / ds, at = id - n * ds, d = at / g.s;
-    const float a2 = a[at] * kLog2e;
-    float h = state ? state[id] : 0.0f;
-    float* back = backs + n * g.chunks * ds + at;
-    const float* sum = sums + n * g.chunks * int64_t(g.d) + d;
-    join_forward(states + n * g.chunks * ds + at, sum, a2, h, g);
-    float r = dstate_out ? dstate_out[id] : 0.0f;
+    const Column<SL, SPL> c(id, a, g);
+    join_forward(states, sums, state && c.live ? state[c.user] : 0.0f, c, g, 0);
+    float r = dstate_out && c.live ? dstate_out[c.user] : 0.0f;
     for (int32_t k0 = g.chunks - 1; k0 >= 0; k0 -= kJoin) {
       float p[kJoin], e[kJoin];
 #pragma unroll
       for (int i = 0; i < kJoin; ++i) {
         const bool ok = k0 - i >= 0;
-        p[i] = ok ? back[(k0 - i) * ds] : 0.0f;
-        e[i] = ok ? sum[(k0 - i) * int64_t(g.d)] : 0.0f;
+        p[i] = ok ? backs[c.at + (k0 - i) * c.step] : 0.0f;
+        e[i] = ok ? sums[c.sum_at + (k0 - i) * c.sum_step] : 0.0f;
       }
 #pragma unroll
       for (int i = 0; i < kJoin; ++i) {
         if (k0 - i < 0) break;
-        back[(k0 - i) * ds] = r;
-        r = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * e[i]), r, p[i]);
+        backs[c.at + (k0 - i) * c.step] = r;
+        r = __builtin_fmaf(__builtin_amdgcn_exp2f(c.a2 * e[i]), r, p[i]);
       }
     }
-    if (dstate) dstate[id] = r;
+    if (dstate && c.live) dstate[c.user] = r;
   }
 }
 
@@ -657,16 +695,21 @@ __device__ __forceinline__ void sum_groups(const float (&db)[SPL], const float (
 // Tile after tile from the end of the chunk: the tile's states are run again
 // into registers from the kept one, then the gradient comes back through them.
 template <int DT, int SL, int SPL>
-__global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo g, const Elem<DT>* __restrict__ dy,
-                                                       const float* __restrict__ states,
-                                                       const float* __restrict__ backs, Kept kept, ScanOut<DT> out) {
+__global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo g, const Elem<DT>* __restrict__ dy,
+                                                       const float4* __restrict__ states,
+                                                       const float4* __restrict__ backs, Kept kept, ScanOut<DT> out) {
   constexpr int NS = SL * SPL;
+  // LDS for two workgroups per compute unit: up to 16 states it holds the lower
+  // half tile's states and two sets of partial sums, up to 32 one set
+  constexpr bool kSaveLow = NS <= 32;
+  constexpr int kParts = NS <= 16 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) float bc[kTile * 2 * NS];
-  __shared__ float part[2][kWaves][kTile][2 * NS];
-  __shared__ float4 enter[kWaves][SPL][64];  // the state that enters the chunk
+  __shared__ float part[kParts][kWaves][kTile][2 * NS];
+  __shared__ float4 enter[kWaves][SPL][64];                // the state that enters the chunk
+  __shared__ float4 low[kSaveLow ? kHalf - 1 : 1][kWaves][SPL][64];  // states 1, 2, 3 of a tile
   int64_t n;
   int32_t chunk, wave_d0;
-  locate<SL, SPL>(g, n, chunk, wave_d0);
+  locate<SL, SPL>(g, g.chunks, n, chunk, wave_d0);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const Place<SL, SPL> at(wave_d0, g.d);
   const int32_t len = valid_len(in.lengths, n, g.l);
@@ -676,11 +719,10 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
   const int64_t c_id = n * g.chunks + chunk, ds = int64_t(g.d) * g.s;
 
   float a2[4][SPL], carry[4][SPL], da[4][SPL];
-  load_states<SL, SPL>(a2, states + c_id * ds, at, g);
 #pragma unroll
-  for (int i = 0; i < SPL; ++i) enter[wave][i][lane] = make_float4(a2[0][i], a2[1][i], a2[2][i], a2[3][i]);
+  for (int i = 0; i < SPL; ++i) enter[wave][i][lane] = states[lane_order<SPL>(blockIdx.x) + i * 64];
   load_states<SL, SPL>(a2, in.a, at, g);
-  load_states<SL, SPL>(carry, backs + c_id * ds, at, g);
+  get_lanes<SPL>(backs, blockIdx.x, carry);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -726,18 +768,15 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
       h0[0][i] = f.x, h0[1][i] = f.y, h0[2][i] = f.z, h0[3][i] = f.w;
     }
     if (k > 0 && t0 < t_valid) {
-      const int64_t o = kept_at<SPL>(g, k);
-      const int64_t w = (o >> 6) * SPL * 64 + (o & 63);
-      float sq[4];
-      quad_all(kept.sum[o], sq);
+      const int64_t o = int64_t(blockIdx.x) * (g.chunk / kTile) + k;
+      const float sum = kept.sum[o * 256 + threadIdx.x];
+      float hk[4][SPL];
+      get_lanes<SPL>(kept.h, o, hk);
 #pragma unroll
-      for (int i = 0; i < SPL; ++i) {
-        const float4 f = kept.h[w + i * 64];
-        const float hk[4] = {f.x, f.y, f.z, f.w};
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          h0[j][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(sq[j] * a2[j][i]), h0[j][i], hk[j]);
-      }
+        for (int i = 0; i < SPL; ++i)
+          h0[j][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(quad_lane(sum, j) * a2[j][i]), h0[j][i], hk[j][i]);
     }
     __syncthreads();
     st.put(bc);
@@ -748,15 +787,14 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
     }
     // one position further; what a position needs of its quad and of b is made
     // again at each use (again() hides that it is the same), for the registers
-    auto again = [](float v) {
+    auto again = [](float v) __attribute__((always_inline)) {
       asm volatile("" : "+v"(v));
       return v;
     };
-    auto advance = [&](int i, const float (&from)[4][SPL], float (&to)[4][SPL]) {
-      float dq[4], xq[4], bf[SPL];
+    auto advance = [&](int i, const float (&from)[4][SPL], float (&to)[4][SPL]) __attribute__((always_inline)) {
+      float bf[SPL];
       const float dl = again(df[i]);
-      quad_all(dl, dq);
-      quad_all(dl * to_f<DT>(u_t[i]), xq);
+      const float dx = dl * to_f<DT>(u_t[i]);
       int s0 = at.s0;
       asm volatile("" : "+v"(s0));
       lds_states<SPL>(&bc[i * 2 * NS + s0], bf);
@@ -764,34 +802,35 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int s = 0; s < SPL; ++s)
-          to[j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq[j] * a2[j][s]), from[j][s], xq[j] * bf[s]);
+          to[j][s] = __builtin_fmaf(__builtin_amdgcn_exp2f(quad_lane(dl, j) * a2[j][s]), from[j][s],
+                                    quad_lane(dx, j) * bf[s]);
       settle(to);
     };
 #pragma unroll
     for (int i = 0; i < kTile; ++i) df[i] = t0 + i < t_valid && at.live ? df[i] : 0.0f;
-    // half a tile's states are held at a time: all eight would take 64 registers more
+    // half a tile's states are held at a time (all eight would take 64 registers
+    // more); those of the lower half wait in LDS, or are made again
     float hs[kHalf + 1][4][SPL];
-    advance(0, h0, hs[0]);
 #pragma unroll
-    for (int i = 1; i < kHalf; ++i) advance(i, hs[0], hs[0]);
+    for (int i = 0; i < kHalf; ++i) {
+      if (i == 0) advance(0, h0, hs[0]);
+      else advance(i, hs[0], hs[0]);
+      if (kSaveLow && i < kHalf - 1) {
+#pragma unroll
+        for (int s = 0; s < SPL; ++s)
+          low[i][wave][s][lane] = make_float4(hs[0][0][s], hs[0][1][s], hs[0][2][s], hs[0][3][s]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) advance(kHalf + i, hs[i], hs[i + 1]);
-#pragma unroll
-    for (int i = kTile - 1; i >= 0; --i) {
-      if (i == kHalf - 1) {
-#pragma unroll
-        for (int q = 0; q < kHalf; ++q) advance(q, q == 0 ? h0 : hs[q], hs[q + 1]);
-      }
-      const float (&before)[4][SPL] = i == 0 ? h0 : hs[i % kHalf];
-      const float (&after)[4][SPL] = hs[i % kHalf + 1];
+    // the gradient comes back through position i, from state `before` to `after`
+    auto back = [&](int i, const float (&before)[4][SPL], const float (&after)[4][SPL]) __attribute__((always_inline)) {
       const float u = to_f<DT>(u_t[i]), yg = yz[i].first(), z = yz[i].second();
       const float sz = in.gate ? sigmoid(z) : 0.0f;
       const float gy = in.gate ? yg * z * sz : yg;
-      float dq[4], xq[4], gq[4], bf[SPL], cf[SPL], db[SPL], dc[SPL];
+      float bf[SPL], cf[SPL], db[SPL], dc[SPL];
       const float dl = again(df[i]);
-      quad_all(dl, dq);
-      quad_all(dl * u, xq);
-      quad_all(gy, gq);
+      const float dx = dl * u;
       int s0 = at.s0;
       asm volatile("" : "+v"(s0));
       lds_states<SPL>(&bc[i * 2 * NS + s0], bf);
@@ -804,16 +843,16 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
         yq[j] = bq[j] = eq[j] = 0.0f;
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-          const float e = __builtin_amdgcn_exp2f(dq[j] * a2[j][s]);
-          const float gr = __builtin_fmaf(cf[s], gq[j], carry[j][s]);
-          const float w = gr * (e * before[j][s]);
+          const float e = __builtin_amdgcn_exp2f(quad_lane(dl, j) * a2[j][s]);
+          const float gr = __builtin_fmaf(quad_lane(gy, j), cf[s], carry[j][s]);
+          carry[j][s] = e * gr;  // h[t-1]'s gradient
+          const float w = carry[j][s] * before[j][s];
           yq[j] = __builtin_fmaf(after[j][s], cf[s], yq[j]);
           bq[j] = __builtin_fmaf(gr, bf[s], bq[j]);
           eq[j] = __builtin_fmaf(w, a2[j][s], eq[j]);
-          da[j][s] = __builtin_fmaf(w, dq[j], da[j][s]);
-          db[s] = __builtin_fmaf(gr, xq[j], db[s]);
-          dc[s] = __builtin_fmaf(after[j][s], gq[j], dc[s]);
-          carry[j][s] = e * gr;
+          da[j][s] = __builtin_fmaf(quad_lane(dl, j), w, da[j][s]);
+          db[s] = __builtin_fmaf(quad_lane(dx, j), gr, db[s]);
+          dc[s] = __builtin_fmaf(quad_lane(gy, j), after[j][s], dc[s]);
         }
       }
       settle(carry);
@@ -834,16 +873,36 @@ __global__ __launch_bounds__(256, SCAN_OCCB) void scan_bwd_kernel(ScanIn<DT> in,
           (out.gate + o)[at.at] = from_f<DT>(valid ? dz : 0.0f);
         }
       }
-      sum_groups<SL, SPL>(db, dc, part[k & 1][wave][i], at.s0);
+      sum_groups<SL, SPL>(db, dc, part[k % kParts][wave][i], at.s0);
+    };
+#pragma unroll
+    for (int i = kHalf - 1; i >= 0; --i) back(kHalf + i, hs[i], hs[i + 1]);
+    copy(hs[0], hs[kHalf]);
+    copy(h0, hs[0]);
+#pragma unroll
+    for (int i = 0; i < kHalf - 1; ++i) {
+      if constexpr (kSaveLow) {
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+          const float4 f = low[i][wave][s][lane];
+          hs[i + 1][0][s] = f.x, hs[i + 1][1][s] = f.y, hs[i + 1][2][s] = f.z, hs[i + 1][3][s] = f.w;
+        }
+      } else {
+        advance(i, hs[i], hs[i + 1]);
+      }
     }
+#pragma unroll
+    for (int i = kHalf - 1; i >= 0; --i) back(i, hs[i], hs[i + 1]);
     __syncthreads();
-    // the workgroup's channels; the buffer is used again two tiles later
+    // the workgroup's channels.  The next tile's barriers stand between these
+    // reads and the writes of the tile after it; with one buffer, its first one
+    // between these reads and its own writes.
     for (int i = threadIdx.x; i < kTile * 2 * NS; i += 256) {
       const int t = i / (2 * NS), q = i % (2 * NS), which = q / NS, s = q % NS;
       if (t0 + t >= t_valid || s >= g.s) continue;
-      float v = part[k & 1][0][t][q];
+      float v = part[k % kParts][0][t][q];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += part[k & 1][w][t][q];
+      for (int w = 1; w < kWaves; ++w) v += part[k % kParts][w][t][q];
       out.bc_part[((col * rows + n * g.l + t0 + t) * 2 + which) * g.s + s] = v;
     }
   }
@@ -930,42 +989,50 @@ int32_t columns(const cnhwc_scan_desc_t& d) {
   return int32_t(ceil_div(d.d, channels * kWaves));
 }
 
-// Positions per chunk of the forward pass.
-#ifndef SCAN_WAVES
-#define SCAN_WAVES 4096
-#endif
-#ifndef SCAN_ONE
-#define SCAN_ONE 1024
-#endif
-#ifndef SCAN_MIN
-#define SCAN_MIN 32
-#endif
+// Positions per chunk of the forward pass.  Chunks cost a second run over the
+// data, so there is one where 1024 wavefronts (one for each SIMD) come without
+// them: 32 sequences of 512 x 2048 channels take 233 us so, 273 us in two
+// chunks.  Otherwise enough of them for 4096 wavefronts (16384 x 2048 channels:
+// 292 us; 2048 wavefronts 316, 8192 322 us), of at least 32 positions.
 int32_t fwd_chunk(const cnhwc_scan_desc_t& d) {
   const int64_t one = d.n * columns(d) * kWaves;
   int64_t chunk = d.l;
-  if (one < SCAN_ONE) {
-    chunk = ceil_div(d.l * one, SCAN_WAVES);
-    chunk = chunk < SCAN_MIN ? SCAN_MIN : chunk;
+  if (one < 1024) {
+    chunk = ceil_div(d.l * one, 4096);
+    chunk = chunk < 32 ? 32 : chunk;
   }
   return int32_t(ceil_div(chunk, kTile) * kTile);
 }
 
-#ifndef SCAN_BC
-#define SCAN_BC 64
-#endif
-constexpr int32_t kBwdChunk = SCAN_BC;
+// Positions per chunk of the backward pass: enough chunks for 2048 wavefronts,
+// the two that each SIMD holds, but at most 128 positions, at least 16.
+// (4 x 1024 x 1024 channels, 32 states: chunks of 128 take 208 us, of 64 212, of
+// 32 228 us; 8 x 2048 x 2048 channels, 16 states: 256 744 us, 128 740, 64 747.)
+int32_t bwd_chunk(const cnhwc_scan_desc_t& d) {
+  int64_t chunk = ceil_div(d.l * d.n * columns(d) * kWaves, 2048);
+  chunk = chunk < 16 ? 16 : (chunk > 128 ? 128 : chunk);
+  return int32_t(ceil_div(chunk, kTile) * kTile);
+}
 
-uint64_t fwd_bytes(const cnhwc_scan_desc_t& d) {
+// States per lane.
+uint64_t lane_states(int32_t s) { return s <= 4 ? 1 : (s <= 8 ? 2 : 4); }
+
+struct FwdLayout {
+  uint64_t states, sums, total;
+};
+FwdLayout fwd_layout(const cnhwc_scan_desc_t& d) {
   const int64_t chunks = ceil_div(d.l, fwd_chunk(d));
-  return chunks > 1 ? align_up(uint64_t(d.n) * chunks * d.d * (d.s + 1) * 4, 256) : 0;
+  const uint64_t lanes = uint64_t(d.n) * chunks * columns(d) * kWaves * 64;
+  if (chunks == 1) return {0, 0, 0};
+  return {0, lanes * lane_states(d.s) * 16, lanes * (lane_states(d.s) * 16 + 4)};
 }
 
 struct BwdLayout {
   uint64_t states, backs, sums, bc, params, kept_h, kept_sum, total;
 };
 BwdLayout bwd_layout(const cnhwc_scan_desc_t& d) {
-  const uint64_t cols = columns(d);
-  const uint64_t nc = uint64_t(d.n) * ceil_div(d.l, kBwdChunk), ds = uint64_t(d.d) * d.s;
+  const uint64_t cols = columns(d), chunk = bwd_chunk(d), ds = uint64_t(d.d) * d.s;
+  const uint64_t nc = uint64_t(d.n) * ceil_div(d.l, chunk), lanes = nc * cols * kWaves * 64;
   BwdLayout L;
   uint64_t at = 0;
   auto take = [&](uint64_t floats) {
@@ -973,15 +1040,13 @@ BwdLayout bwd_layout(const cnhwc_scan_desc_t& d) {
     at = align_up(at + floats * 4, 256);
     return o;
   };
-  L.states = take(nc * ds);
-  L.backs = take(nc * ds);
-  L.sums = take(nc * d.d);
+  L.states = take(lanes * lane_states(d.s) * 4);
+  L.backs = take(lanes * lane_states(d.s) * 4);
+  L.sums = take(lanes);
   L.bc = take(cols * d.n * d.l * 2 * d.s);
   L.params = take(nc * (ds + 2 * uint64_t(d.d)));
-  const uint64_t lanes = nc * cols * (kBwdChunk / kTile) * 256;
-  const uint64_t spl = d.s <= 4 ? 1 : (d.s <= 8 ? 2 : 4);
-  L.kept_h = take(lanes * 4 * spl);
-  L.kept_sum = take(lanes);
+  L.kept_h = take(lanes * (chunk / kTile) * lane_states(d.s) * 4);
+  L.kept_sum = take(lanes * (chunk / kTile));
   L.total = at;
   return L;
 }
@@ -997,7 +1062,7 @@ cnhwc_status_t check_desc(const cnhwc_scan_desc_t* d, bool bwd) {
   if (d->s > CNHWC_SCAN_MAX_STATE) return CNHWC_ERR_UNSUPPORTED;
   // positions fit 32 bits with a chunk's overhang; grids and offsets stay in range
   if (d->l > INT_MAX - 1024 || d->d > (1ll << 23) || !dense_ok(d->n, d->l, d->d * d->s) ||
-      d->n * ceil_div(d->l, kBwdChunk) * ceil_div(d->d, 16) > (1ll << 24))
+      d->n * ceil_div(d->l, 16) * ceil_div(d->d, 64) > (1ll << 23))
     return CNHWC_ERR_UNSUPPORTED;
   return CNHWC_OK;
 }
@@ -1027,7 +1092,7 @@ extern "C" cnhwc_status_t cnhwc_scan_fwd_workspace(const cnhwc_scan_desc_t* desc
   const cnhwc_status_t st = check_desc(desc, false);
   if (st != CNHWC_OK) return st;
   if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
-  *bytes = fwd_bytes(*desc);
+  *bytes = fwd_layout(*desc).total;
   return CNHWC_OK;
 }
 
@@ -1038,7 +1103,8 @@ extern "C" cnhwc_status_t cnhwc_scan_fwd(const cnhwc_scan_desc_t* desc, const cn
   if (st != CNHWC_OK) return st;
   if (!in) return CNHWC_ERR_INVALID_ARGUMENT;
   const cnhwc_scan_desc_t& d = *desc;
-  const uint64_t need = fwd_bytes(d);
+  const FwdLayout L = fwd_layout(d);
+  const uint64_t need = L.total;
   if (workspace_bytes < need) return CNHWC_ERR_WORKSPACE_TOO_SMALL;
   const uint64_t es = dtype_size(d.dtype);
   Buffers bf;
@@ -1054,7 +1120,8 @@ extern "C" cnhwc_status_t cnhwc_scan_fwd(const cnhwc_scan_desc_t* desc, const cn
   g.chunks = int32_t(ceil_div(d.l, g.chunk));
   const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(256);
   float* states = static_cast<float*>(workspace);
-  float* sums = states + d.n * g.chunks * d.d * d.s;
+  float4* states4 = static_cast<float4*>(workspace);
+  float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.sums);
   return with_dtype(d.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     const ScanIn<DT> si = inputs_of<DT>(*in);
@@ -1062,13 +1129,14 @@ extern "C" cnhwc_status_t cnhwc_scan_fwd(const cnhwc_scan_desc_t* desc, const cn
     return with_shape(d.s, [&](auto sh) {
       constexpr int SL = decltype(sh)::sl, SPL = decltype(sh)::spl;
       if (g.chunks > 1) {
-        hipLaunchKernelGGL((scan_fwd_kernel<DT, SL, SPL, true>), grid, block, 0, s, si, g, yo, states, sums, nullptr);
-        const int64_t total = d.n * d.d * d.s;
-        hipLaunchKernelGGL(scan_join_kernel, grid_of(ceil_div(total, 256)), dim3(256), 0, s, states, sums, in->a,
-                           in->state, state_out, g, total);
+        const dim3 all_but_last(unsigned(d.n * (g.chunks - 1) * g.col_blocks));
+        hipLaunchKernelGGL((scan_fwd_kernel<DT, SL, SPL, true>), all_but_last, block, 0, s, si, g, yo, states4, sums,
+                           nullptr);
+        const int64_t total = d.n * g.col_blocks * (kWaves * 64 * 4 * SPL);
+        hipLaunchKernelGGL((scan_join_kernel<SL, SPL>), grid_of(ceil_div(total, 256)), dim3(256), 0, s, states, sums,
+                           in->a, in->state, g, total);
       }
-      hipLaunchKernelGGL((scan_fwd_kernel<DT, SL, SPL, false>), grid, block, 0, s, si, g, yo, states, sums,
-                         g.chunks > 1 ? nullptr : state_out);
+      hipLaunchKernelGGL((scan_fwd_kernel<DT, SL, SPL, false>), grid, block, 0, s, si, g, yo, states4, sums, state_out);
       return hipGetLastError() == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
     });
   });
@@ -1114,7 +1182,7 @@ extern "C" cnhwc_status_t cnhwc_scan_bwd(const cnhwc_scan_desc_t* desc, const cn
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   ScanGeo g = geo_of(d);
   g.col_blocks = columns(d);
-  g.chunk = kBwdChunk;
+  g.chunk = bwd_chunk(d);
   g.chunks = int32_t(ceil_div(d.l, g.chunk));
   const dim3 grid(unsigned(d.n * g.chunks * g.col_blocks)), block(256);
   char* ws = static_cast<char*>(workspace);
@@ -1133,12 +1201,13 @@ extern "C" cnhwc_status_t cnhwc_scan_bwd(const cnhwc_scan_desc_t* desc, const cn
                          params};
     with_shape(d.s, [&](auto sh) {
       constexpr int SL = decltype(sh)::sl, SPL = decltype(sh)::spl;
-      hipLaunchKernelGGL((scan_bwd_local_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, sums,
+      float4 *states4 = reinterpret_cast<float4*>(states), *backs4 = reinterpret_cast<float4*>(backs);
+      hipLaunchKernelGGL((scan_bwd_local_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states4, backs4, sums,
                          kept);
-      const int64_t total = d.n * d.d * d.s;
-      hipLaunchKernelGGL(scan_bwd_join_kernel, grid_of(ceil_div(total, 256)), dim3(256), 0, s, states, backs, sums,
-                         in->a, in->state, dstate_out, grads->state, g, total);
-      hipLaunchKernelGGL((scan_bwd_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states, backs, kept, so);
+      const int64_t total = d.n * g.col_blocks * (kWaves * 64 * 4 * SPL);
+      hipLaunchKernelGGL((scan_bwd_join_kernel<SL, SPL>), grid_of(ceil_div(total, 256)), dim3(256), 0, s, states,
+                         backs, sums, in->a, in->state, dstate_out, grads->state, g, total);
+      hipLaunchKernelGGL((scan_bwd_kernel<DT, SL, SPL>), grid, block, 0, s, si, g, gy, states4, backs4, kept, so);
     });
     const int64_t bc_total = d.n * d.l * 2 * d.s;
     hipLaunchKernelGGL((scan_bwd_bc_kernel<DT>), grid_of(ceil_div(bc_total, 256)), dim3(256), 0, s, bc, in->lengths,

@@ -119,7 +119,7 @@ __device__ __forceinline__ float exp_full(float x) {
   constexpr float hi = 1.44269502f, lo = 1.92596299e-8f;  // log2(e) = hi + lo
   x = x < -110.0f ? -110.0f : x;
   const float t = x * hi;
-  const float r = __builtin_fmaf(x, hi, -t) + x * lo;
+  const float r = __builtin_fmaf(x, lo, __builtin_fmaf(x, hi, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e, r * 0.693147181f, e);
 }
@@ -136,25 +136,18 @@ __device__ __forceinline__ float sigmoid(float x) {
   return rcp_full(1.0f + exp_full(n));
 }
 
-// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  With
-// q = e / (2 + e) <= 1/3, log(1 + e) = 2 atanh(q) = 2 q (1 + q^2/3 + q^4/5 + ...):
-// nine terms leave 2^-29 of the value.  Also s = 1 / (1 + e^-x), its derivative.
+// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1], and its
+// derivative s = 1 / (1 + e^-x).  log(1 + e) is taken of the rounded w = 1 + e
+// and corrected by what the rounding left out, (e - (w - 1)) / w: within 2^-21.9
+// of the value over all x down to -87, where it becomes 0 (measured; the
+// logarithm alone would lose every digit of a small e).
 __device__ __forceinline__ float softplus(float x, float& s) {
   const float e = exp_full(-__builtin_fabsf(x));
-  const float q = e * rcp_full(2.0f + e);
-  const float q2 = q * q;
-  float p = 1.0f / 17.0f;
-  p = __builtin_fmaf(p, q2, 1.0f / 15.0f);
-  p = __builtin_fmaf(p, q2, 1.0f / 13.0f);
-  p = __builtin_fmaf(p, q2, 1.0f / 11.0f);
-  p = __builtin_fmaf(p, q2, 1.0f / 9.0f);
-  p = __builtin_fmaf(p, q2, 1.0f / 7.0f);
-  p = __builtin_fmaf(p, q2, 1.0f / 5.0f);
-  p = __builtin_fmaf(p, q2, 1.0f / 3.0f);
-  p = __builtin_fmaf(p, q2, 1.0f);
-  const float inv = rcp_full(1.0f + e);
+  const float w = 1.0f + e;
+  const float inv = rcp_full(w);
+  const float left = e - (w - 1.0f);
   s = x < 0.0f ? e * inv : inv;
-  return (x > 0.0f ? x : 0.0f) + 2.0f * q * p;
+  return (x > 0.0f ? x : 0.0f) + __builtin_fmaf(__builtin_amdgcn_logf(w), 0.693147181f, left * inv);
 }
 __device__ __forceinline__ float softplus(float x) {
   float s;
