@@ -72,6 +72,21 @@ __device__ __forceinline__ Pack<DT, V> load_row(const Elem<DT>* __restrict__ x, 
   return Pack<DT, V>{};
 }
 
+// kBatch rows from r on, all of them rows of x where the fast path holds.
+template <int DT, int V, int K>
+__device__ __forceinline__ void load_rows(Pack<DT, V> (&p)[kBatch], const Elem<DT>* __restrict__ x,
+                                          const Elem<DT>* __restrict__ state, int64_t xs1, int32_t c, int64_t r,
+                                          int32_t len) {
+  if (r >= 0 && r + kBatch <= len) {
+    const Elem<DT>* row = x + r * xs1;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) p[i] = load_pack<DT, V>(row + i * xs1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) p[i] = load_row<DT, V, K>(x, state, xs1, c, r + i, len);
+  }
+}
+
 template <int DT, int V, int K>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(
     const Elem<DT>* __restrict__ x, const Elem<DT>* __restrict__ wp, const Elem<DT>* __restrict__ bp,
@@ -96,10 +111,11 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(
       for (int v = 0; v < V; ++v) win[k + 1][v] = to_f<DT>(p.e[v]);
     }
     const int32_t end = t0 + g.run < g.l ? t0 + g.run : g.l;
-    for (int32_t tb = t0; tb < end; tb += kBatch) {
-      Pack<DT, V> p[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) p[i] = load_row<DT, V, K>(xn, sn, g.xs[1], g.c, tb + i, len);
+    const int32_t live = end < len ? end : len;
+    Pack<DT, V> p[kBatch], next[kBatch];
+    load_rows<DT, V, K>(p, xn, sn, g.xs[1], g.c, t0, len);
+    for (int32_t tb = t0; tb < live; tb += kBatch) {
+      load_rows<DT, V, K>(next, xn, sn, g.xs[1], g.c, tb + kBatch, tb + kBatch < live ? len : 0);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int32_t t = tb + i;
@@ -107,21 +123,21 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(
         for (int k = 0; k < K - 1; ++k)
 #pragma unroll
           for (int v = 0; v < V; ++v) win[k][v] = win[k + 1][v];
-#pragma unroll
-        for (int v = 0; v < V; ++v) win[K - 1][v] = to_f<DT>(p[i].e[v]);
-        if (t >= end) continue;
         Pack<DT, V> o;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+          win[K - 1][v] = to_f<DT>(p[i].e[v]);
           float a = tap.b[v];
 #pragma unroll
           for (int k = 0; k < K; ++k) a = __builtin_fmaf(tap.w[v][k], win[k][v], a);
-          if (g.act == CNHWC_ACT_SILU) a *= sigmoid(a);
-          o.e[v] = t < len ? from_f<DT>(a) : Elem<DT>(0);
+          if (g.act == CNHWC_ACT_SILU) a *= sigmoid_for<DT>(a);
+          o.e[v] = from_f<DT>(a);
         }
-        store_pack<DT, V>(yn + t * int64_t(g.c), o);
+        if (t < live) store_pack<DT, V>(yn + t * int64_t(g.c), o);
+        p[i] = next[i];
       }
     }
+    for (int32_t t = t0 > len ? t0 : len; t < end; ++t) store_pack<DT, V>(yn + t * int64_t(g.c), Pack<DT, V>{});
     if (K > 1 && state_out && t0 == 0) {
       Elem<DT>* so = state_out + n * (K - 1) * int64_t(g.c) + c0;
 #pragma unroll
@@ -154,7 +170,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(
       float a = tap.b[v];
 #pragma unroll
       for (int k = 0; k < K; ++k) a = __builtin_fmaf(tap.w[v][k], to_f<DT>(row[k].e[v]), a);
-      if (g.act == CNHWC_ACT_SILU) a *= sigmoid(a);
+      if (g.act == CNHWC_ACT_SILU) a *= sigmoid_for<DT>(a);
       o.e[v] = from_f<DT>(a);
     }
     store_pack<DT, V>(y + n * int64_t(g.c) + c0, o);
@@ -210,19 +226,18 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(
       for (int v = 0; v < V; ++v) win[k + 1][v] = to_f<DT>(p.e[v]);
     }
     const int64_t end = j0 + g.run < rows ? j0 + g.run : rows;
-    for (int64_t tb = j0 - (K - 1); tb < end; tb += kBatch) {
-      Pack<DT, V> px[kBatch], pg[kBatch];
+    const int64_t touched = end < int64_t(len) + K - 1 ? end : int64_t(len) + K - 1;  // rows past it are 0
+    Pack<DT, V> px[kBatch], pg[kBatch], nx[kBatch], ng[kBatch];
+    const int64_t first = j0 - (K - 1);
+    load_rows<DT, V, K>(px, xn, sn, g.xs[1], g.c, first, j0 < touched ? len : 0);
+    load_rows<DT, V, K>(pg, gn, nullptr, g.dys[1], g.c, first, j0 < touched ? len : 0);
+    for (int64_t tb = first; tb < touched; tb += kBatch) {
+      load_rows<DT, V, K>(nx, xn, sn, g.xs[1], g.c, tb + kBatch, tb + kBatch < touched ? len : 0);
+      load_rows<DT, V, K>(ng, gn, nullptr, g.dys[1], g.c, tb + kBatch, tb + kBatch < touched ? len : 0);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int64_t t = tb + i;
-        px[i] = load_row<DT, V, K>(xn, sn, g.xs[1], g.c, t, len);
-        pg[i] = t >= 0 && t < len ? load_pack<DT, V>(gn + t * g.dys[1]) : Pack<DT, V>{};
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int64_t t = tb + i;
-        if (t >= end) break;
-        const bool valid = t >= 0 && t < len, own = t >= j0;
+        const bool valid = t >= 0 && t < len, own = t >= j0 && t < touched;
         const int64_t fin = t - len;  // row of dfin that belongs to dX row t
         Pack<DT, V> pf{};
         if (own && dfin && fin >= 0 && fin < K - 1) pf = load_pack<DT, V>(dfin + so + fin * int64_t(g.c));
@@ -240,22 +255,24 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(
             float a = tap.b[v];
 #pragma unroll
             for (int k = 0; k < K; ++k) a = __builtin_fmaf(tap.w[v][k], win[k][v], a);
-            const float s = sigmoid(a);
+            const float s = sigmoid_for<DT>(a);
             d *= s * __builtin_fmaf(a, 1.0f - s, 1.0f);
           }
           dpre[K - 1][v] = d = valid ? d : 0.0f;
-          if (own) {
-            db[v] += d;
-            float r = to_f<DT>(pf.e[v]);
+          float r = to_f<DT>(pf.e[v]);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-              // past the valid rows X may hold anything: d is 0 there and so is the term
-              dw[v][k] = valid ? __builtin_fmaf(d, win[k][v], dw[v][k]) : dw[v][k];
-              r = __builtin_fmaf(tap.w[v][k], dpre[K - 1 - k][v], r);
-            }
-            o.e[v] = from_f<DT>(r);
+          for (int k = 0; k < K; ++k) r = __builtin_fmaf(tap.w[v][k], dpre[K - 1 - k][v], r);
+          o.e[v] = from_f<DT>(r);
+          // positions before the run are the neighbour's; past the valid ones X
+          // may hold anything
+          if (own && valid) {
+            db[v] += d;
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[v][k] = __builtin_fmaf(d, win[k][v], dw[v][k]);
           }
         }
+        px[i] = nx[i];
+        pg[i] = ng[i];
         if (!own) continue;
         if (t < K - 1) {
           if (dstate) store_pack<DT, V>(dstate + so + t * int64_t(g.c), o);
@@ -264,6 +281,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(
         }
       }
     }
+    for (int64_t t = j0 > touched ? j0 : touched; t < end; ++t)
+      store_pack<DT, V>(dxn + (t - (K - 1)) * int64_t(g.c), Pack<DT, V>{});
   }
   // the two runs of a wavefront, then the wavefronts through LDS in order
   __shared__ float sum[4][kLanes * V * (K + 1)];
@@ -306,10 +325,10 @@ ConvGeo geo_of(const cnhwc_causal_conv_desc_t& d, int ve) {
   return g;
 }
 
-// 16-byte vectors of rows at these strides.
-bool vectors(const cnhwc_causal_conv_desc_t& d, const int64_t (&s)[2], const void* p) {
-  const int64_t v = 16 / int64_t(dtype_size(d.dtype));
-  return aligned(p, 16) && d.c % v == 0 && (d.n == 1 || s[0] % v == 0) && (d.l == 1 || s[1] % v == 0);
+// Aligned vectors of rows at these strides.
+bool vectors(const cnhwc_causal_conv_desc_t& d, const int64_t (&s)[2], const void* p, int64_t bytes) {
+  const int64_t v = bytes / int64_t(dtype_size(d.dtype));
+  return aligned(p, bytes) && d.c % v == 0 && (d.n == 1 || s[0] % v == 0) && (d.l == 1 || s[1] % v == 0);
 }
 
 // Positions per thread: long runs load fewer rows twice, short ones fill the
@@ -440,7 +459,7 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_fwd(const cnhwc_causal_conv_desc_t* 
   bf.out(y, uint64_t(d.n) * d.l * d.c * es, es, true);
   bf.out(state_out, state_bytes(d), es, false);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
-  const bool vec = vectors(d, d.x_stride, x) && aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) &&
+  const bool vec = vectors(d, d.x_stride, x, 16) && aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) &&
                    aligned(y, 16) && aligned(state_out, 16);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   hipError_t e;
@@ -462,7 +481,7 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd_workspace(const cnhwc_causal_con
   if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
   // the vector and the element form alike: which one runs also depends on the pointers
   uint64_t most = 0;
-  for (int64_t ve : {int64_t(1), 16 / int64_t(dtype_size(desc->dtype))}) {
+  for (int64_t ve : {int64_t(1), 8 / int64_t(dtype_size(desc->dtype))}) {
     int32_t run;
     int64_t blocks;
     bwd_runs(*desc, ve, &run, &blocks);
@@ -500,8 +519,9 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd(const cnhwc_causal_conv_desc_t* 
   bf.out(dstate, state_bytes(d), es, false);
   bf.out(workspace, need, 16, true);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
-  const bool vec = d.k <= 4 && vectors(d, d.x_stride, x) && vectors(d, d.dy_stride, dy) && aligned(dstate_out, 16) &&
-                   aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) && aligned(dx, 16) && aligned(dstate, 16);
+  const bool vec = d.k <= 4 && vectors(d, d.x_stride, x, 8) && vectors(d, d.dy_stride, dy, 8) &&
+                   aligned(dstate_out, 8) && aligned(w, 8) && aligned(bias, 8) && aligned(state, 8) &&
+                   aligned(dx, 8) && aligned(dstate, 8);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   float* part = static_cast<float*>(workspace);
   hipError_t e;
@@ -509,9 +529,9 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd(const cnhwc_causal_conv_desc_t* 
     return conv_bwd_t<decltype(dt)::value, decltype(v)::value>(d, dy, dstate_out, x, w, bias, state, lengths, dx, dw,
                                                                dbias, dstate, part, s);
   };
-  if (d.dtype == CNHWC_F32) e = vec ? run(Int<CNHWC_F32>{}, Int<4>{}) : run(Int<CNHWC_F32>{}, Int<1>{});
-  else if (d.dtype == CNHWC_F16) e = vec ? run(Int<CNHWC_F16>{}, Int<8>{}) : run(Int<CNHWC_F16>{}, Int<1>{});
-  else e = vec ? run(Int<CNHWC_BF16>{}, Int<8>{}) : run(Int<CNHWC_BF16>{}, Int<1>{});
+  if (d.dtype == CNHWC_F32) e = vec ? run(Int<CNHWC_F32>{}, Int<2>{}) : run(Int<CNHWC_F32>{}, Int<1>{});
+  else if (d.dtype == CNHWC_F16) e = vec ? run(Int<CNHWC_F16>{}, Int<4>{}) : run(Int<CNHWC_F16>{}, Int<1>{});
+  else e = vec ? run(Int<CNHWC_BF16>{}, Int<4>{}) : run(Int<CNHWC_BF16>{}, Int<1>{});
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }
 
@@ -532,7 +552,7 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_step(const cnhwc_causal_conv_desc_t*
   bf.out(y, uint64_t(d.n) * d.c * es, es, true);
   bf.out(state_out, state_bytes(d), es, d.k > 1);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
-  const bool vec = vectors(d, d.x_stride, x) && aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) &&
+  const bool vec = vectors(d, d.x_stride, x, 16) && aligned(w, 16) && aligned(bias, 16) && aligned(state, 16) &&
                    aligned(y, 16) && aligned(state_out, 16);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   hipError_t e;

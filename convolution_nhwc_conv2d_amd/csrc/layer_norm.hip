@@ -65,6 +65,20 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(
   constexpr int kThreads = TPR > 256 ? TPR : 256;
   __shared__ float red[2][16];
   const int t = threadIdx.x % TPR;
+  // w and b stay in registers where they are few, else each row takes them from
+  // the cache again
+  constexpr bool kHold = NV * VE <= 16;
+  float wf[kHold ? NV : 1][VE], bf[kHold ? NV : 1][VE];
+  auto params = [&](int32_t c0, float (&wv)[VE], float (&bv)[VE]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < VE; ++e) wv[e] = 1.0f, bv[e] = 0.0f;
+    if (w && c0 < g.c) load_params<DT, VE>(w, c0, g.w_f32, wv);
+    if (b && c0 < g.c) load_params<DT, VE>(b, c0, g.w_f32, bv);
+  };
+  if constexpr (kHold) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) params((i * TPR + t) * VE, wf[i], bf[i]);
+  }
   // every thread of a workgroup walks the same number of rows (barriers inside)
   for (int64_t row0 = int64_t(blockIdx.x) * (kThreads / TPR); row0 < g.rows;
        row0 += int64_t(gridDim.x) * (kThreads / TPR)) {
@@ -98,23 +112,20 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(
     const float rstd = 1.0f / __builtin_sqrtf(var + g.eps);
     if (!live) continue;
     Elem<DT>* yr = y + row * g.c;
-    // wide tiles load w and b again for every row (from the cache): holding
-    // them over the loop would take more registers than there are
-    int32_t again = 0;
-    if constexpr (NV * VE > 16) asm volatile("" : "+v"(again));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int32_t c0 = (i * TPR + t) * VE;
       if (c0 >= g.c) continue;
+      if constexpr (!kHold) {
+        int32_t at = c0;
+        asm volatile("" : "+v"(at));  // not to be held over the rows
+        params(at, wf[0], bf[0]);
+      }
       Pack<DT, VE> o;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        float v = (to_f<DT>(p[i].e[e]) - mean) * rstd;
-        if (w) {
-          const int32_t c = c0 + e + again;
-          v = __builtin_fmaf(v, load_param<DT>(w, c, g.w_f32), b ? load_param<DT>(b, c, g.w_f32) : 0.0f);
-        }
-        o.e[e] = from_f<DT>(v);
+        const float v = (to_f<DT>(p[i].e[e]) - mean) * rstd;
+        o.e[e] = from_f<DT>(__builtin_fmaf(v, wf[kHold ? i : 0][e], bf[kHold ? i : 0][e]));
       }
       store_pack<DT, VE>(yr + c0, o);
     }
@@ -168,13 +179,18 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_kernel(
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   float wf[NV * VE], dw[NV * VE], db[NV * VE];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    const int32_t c0 = (i * TPR + t) * VE;
+    float wv[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) wv[e] = 1.0f;
+    if (w && c0 < g.c) load_params<DT, VE>(w, c0, g.w_f32, wv);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const int32_t c = (i * TPR + t) * VE + e;
-      wf[i * VE + e] = c < g.c ? (w ? load_param<DT>(w, c, g.w_f32) : 1.0f) : 0.0f;
+      wf[i * VE + e] = wv[e];
       dw[i * VE + e] = db[i * VE + e] = 0.0f;
     }
+  }
   const int64_t step = int64_t(gridDim.x) * kGroups;
   int phase = 0;
   // a workgroup-wide row takes part in barriers: its row index is uniform there
@@ -349,10 +365,8 @@ bool with_tile(int64_t vecs, F&& f) {
   if (vecs <= 32) { f(Tile<1, 32>{}); return true; }
   if (vecs <= 64) { f(Tile<1, 64>{}); return true; }
   if (vecs <= 128) { f(Tile<2, 64>{}); return true; }
-  if (vecs <= 256) { f(Tile<4, 64>{}); return true; }
-  if constexpr (VE * 8 <= REGS) {
-    if (vecs <= 512) { f(Tile<8, 64>{}); return true; }
-  }
+  if (vecs <= 256) { f(Tile<1, 256>{}); return true; }
+  if (vecs <= 512) { f(Tile<2, 256>{}); return true; }
   if (vecs <= 1024) { f(Tile<4, 256>{}); return true; }
   if constexpr (VE * 8 <= REGS) {
     if (vecs <= 2048) { f(Tile<8, 256>{}); return true; }
@@ -371,6 +385,10 @@ bool with_tile(int64_t vecs, F&& f) {
 
 // The forward pass keeps the row as it was loaded; the backward pass also w and
 // two sums for every channel, in 32 bits.
+// Most workgroups of the forward pass, a few for every place on the device, so
+// that w and b are taken up a few times only (32768 x 4096 bf16: 1024
+// workgroups 104 us, 8192 98, 65536 117; 65536 x 2048: 154, 98, 111).
+constexpr int64_t kFwdBlocks = 8192;
 constexpr int kFwdRegs = 64, kFwdWide = 64, kBwdRegs = 32, kBwdWide = 16;
 
 template <int DT, int VE>
@@ -380,7 +398,8 @@ hipError_t ln_fwd_t(const LnGeo& g, const void* x, const void* w, const void* b,
   const bool held = with_tile<VE, kFwdRegs, kFwdWide>(ceil_div(g.c, VE), [&](auto tile) {
     constexpr int NV = decltype(tile)::nv, TPR = decltype(tile)::tpr;
     constexpr int threads = TPR > 256 ? TPR : 256;
-    hipLaunchKernelGGL((ln_fwd_kernel<DT, VE, NV, TPR>), grid_of(ceil_div(g.rows, threads / TPR)),
+    const int64_t blocks = ceil_div(g.rows, threads / TPR);
+    hipLaunchKernelGGL((ln_fwd_kernel<DT, VE, NV, TPR>), dim3(unsigned(blocks < kFwdBlocks ? blocks : kFwdBlocks)),
                        dim3(threads), 0, st, static_cast<const E*>(x), w, b, static_cast<E*>(y), mean, rstd, g);
   });
   if (!held)
@@ -399,7 +418,7 @@ int64_t bwd_groups(const cnhwc_layer_norm_desc_t& d, bool vec) {
   auto pick = [&](auto tile) {
     constexpr int TPR = decltype(tile)::tpr;
     per = TPR > 256 ? 1 : 256 / TPR;
-    cap = TPR > 256 ? 256 : 512;
+    cap = TPR > 256 ? 256 : 1024;
   };
   if (ve == 8) with_tile<8, kBwdRegs, kBwdWide>(ceil_div(d.c, 8), pick);
   else if (ve == 4) with_tile<4, kBwdRegs, kBwdWide>(ceil_div(d.c, 4), pick);
@@ -468,7 +487,7 @@ extern "C" cnhwc_status_t cnhwc_layer_norm_fwd(const cnhwc_layer_norm_desc_t* de
   bf.out(rstd, rows * 4, 4, mean != nullptr);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   const LnGeo g = geo_of(d, false);
-  const bool vec = vectors(d, d.x_stride, x) && aligned(y, 16);
+  const bool vec = vectors(d, d.x_stride, x) && aligned(w, 16) && aligned(b, 16) && aligned(y, 16);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   hipError_t e;
   if (d.dtype == CNHWC_F32)
@@ -523,7 +542,7 @@ extern "C" cnhwc_status_t cnhwc_layer_norm_bwd(const cnhwc_layer_norm_desc_t* de
   }
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   const LnGeo g = geo_of(d, true);
-  const bool vec = vectors(d, d.x_stride, x) && vectors(d, d.dy_stride, dy) && aligned(dx, 16);
+  const bool vec = vectors(d, d.x_stride, x) && vectors(d, d.dy_stride, dy) && aligned(w, 16) && aligned(dx, 16);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   float* part = static_cast<float*>(workspace);
   hipError_t e;

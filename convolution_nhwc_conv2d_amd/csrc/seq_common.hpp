@@ -30,9 +30,11 @@ __device__ __forceinline__ Elem<DT> from_f(float v) {
   else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
 }
 
-// V consecutive elements; V * sizeof(element) is 16 bytes (aligned) or V is 1.
+// V consecutive elements: 16 or 8 aligned bytes, or V is 1.
 template <int DT, int V>
 struct Pack { Elem<DT> e[V]; };
+template <int DT, int V>
+using PackBits = std::conditional_t<V * sizeof(Elem<DT>) == 16, uint4, uint2>;
 
 template <int DT, int V>
 __device__ __forceinline__ Pack<DT, V> load_pack(const Elem<DT>* p) {
@@ -40,8 +42,7 @@ __device__ __forceinline__ Pack<DT, V> load_pack(const Elem<DT>* p) {
   if constexpr (V == 1) {
     r.e[0] = *p;
   } else {
-    static_assert(V * sizeof(Elem<DT>) == 16, "16-byte vectors");
-    r = __builtin_bit_cast(Pack<DT, V>, *reinterpret_cast<const uint4*>(p));
+    r = __builtin_bit_cast(Pack<DT, V>, *reinterpret_cast<const PackBits<DT, V>*>(p));
   }
   return r;
 }
@@ -51,8 +52,7 @@ __device__ __forceinline__ void store_pack(Elem<DT>* p, const Pack<DT, V>& v) {
   if constexpr (V == 1) {
     *p = v.e[0];
   } else {
-    static_assert(V * sizeof(Elem<DT>) == 16, "16-byte vectors");
-    *reinterpret_cast<uint4*>(p) = __builtin_bit_cast(uint4, v);
+    *reinterpret_cast<PackBits<DT, V>*>(p) = __builtin_bit_cast(PackBits<DT, V>, v);
   }
 }
 
@@ -61,6 +61,27 @@ template <int DT>
 __device__ __forceinline__ float load_param(const void* p, int64_t i, bool f32) {
   if constexpr (DT == CNHWC_F32) return static_cast<const float*>(p)[i];
   else return f32 ? static_cast<const float*>(p)[i] : to_f<DT>(static_cast<const uint16_t*>(p)[i]);
+}
+
+// V consecutive parameters; vectors of V * sizeof(element of DT) = 16 bytes (32
+// where they are fp32 beside a 16-bit DT), 16-byte aligned.
+template <int DT, int V>
+__device__ __forceinline__ void load_params(const void* p, int64_t i, bool f32, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = load_param<DT>(p, i, f32);
+  } else {
+    if (DT == CNHWC_F32 || f32) {
+#pragma unroll
+      for (int k = 0; k < V; k += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + k);
+        v[k] = f.x, v[k + 1] = f.y, v[k + 2] = f.z, v[k + 3] = f.w;
+      }
+    } else {
+      const Pack<DT, V> r = load_pack<DT, V>(static_cast<const Elem<DT>*>(p) + i);
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = to_f<DT>(r.e[k]);
+    }
+  }
 }
 
 template <int DT>
@@ -134,6 +155,15 @@ __device__ __forceinline__ float rcp_full(float v) {
 __device__ __forceinline__ float sigmoid(float x) {
   const float n = -x > 80.0f ? 80.0f : -x;
   return rcp_full(1.0f + exp_full(n));
+}
+
+// The same for a result that is rounded to DT: a 16-bit one takes the plain
+// product and the hardware's reciprocal, whose errors (2^-23 of the value, and
+// 2^-24 |x| of the exponential) are far below its rounding.
+template <int DT>
+__device__ __forceinline__ float sigmoid_for(float x) {
+  if constexpr (DT == CNHWC_F32) return sigmoid(x);
+  else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
 
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1], and its
