@@ -1010,13 +1010,18 @@ int32_t columns(const cnhwc_scan_desc_t& d) {
 // data, so there is one where 1024 wavefronts (one for each SIMD) come without
 // them: 32 sequences of 512 x 2048 channels take 233 us so, 273 us in two
 // chunks.  Otherwise enough of them for 4096 wavefronts (16384 x 2048 channels:
-// 292 us; 2048 wavefronts 316, 8192 322 us), of at least 32 positions.
+// 292 us; 2048 wavefronts 316, 8192 322 us).  With little to do the time is a
+// chunk's steps, one after the other, and the join's along the chunks, so
+// chunks have 16 positions at least and 32 in long sequences (2 x 984 x 311
+// channels: chunks of 16 take 29 us, of 32 36; 4 x 2048 x 64: 44 and 40), and up
+// to 64 positions are one chunk (2 x 40 x 128: 21 us, 31 in two).
 int32_t fwd_chunk(const cnhwc_scan_desc_t& d) {
   const int64_t one = d.n * columns(d) * kWaves;
   int64_t chunk = d.l;
-  if (one < 1024) {
+  if (one < 1024 && d.l > 64) {
+    const int64_t least = d.l < 1536 ? 16 : 32;
     chunk = ceil_div(d.l * one, 4096);
-    chunk = chunk < 32 ? 32 : chunk;
+    chunk = chunk < least ? least : chunk;
   }
   return int32_t(ceil_div(chunk, kTile) * kTile);
 }
