@@ -10,7 +10,7 @@
 // gradient of the state that the forward pass left is added to the last K-1.
 //
 // A few operations per element, so memory is the bound: a thread owns 16 bytes
-// of channels over a run of positions and slides a register window along it,
+// of channels (two channels in the backward pass) over a run of positions and slides a register window along it,
 // so each row is loaded once per run (plus the K-1 rows before it, which the
 // neighbouring run has just brought into the cache).  The weights stay in
 // registers.  The backward pass recomputes pre from x instead of reading a
@@ -340,9 +340,11 @@ int32_t pick_run(int64_t work, int64_t threads, int32_t most) {
 }
 // Measured forward: 4 x 4096 x 4096 bf16 with 512 threads 52 us, 2048 56, 4096 68.
 constexpr int64_t kFwdThreads = 512;
-// Backward: 5 x 2047 x 2048 f16 of several lengths with 512 threads 42 us, 1024
-// 35, 2048 37; 2 x 2048 x 2048 f32 32, 36, 38.
-constexpr int64_t kBwdThreads = 768;
+// Backward, with two channels to a thread: 5 x 2047 x 2048 f16 of several
+// lengths with 768 threads 38 us, 1536 33, 3072 35; 2 x 2048 x 2048 f32 30, 35,
+// 38.  (Four f16 channels to a thread, in more registers: 35 us at best.)
+constexpr int kBwdChannels = 2;
+int64_t bwd_threads(int32_t dtype, int64_t ve) { return dtype != CNHWC_F32 && ve == kBwdChannels ? 1536 : 768; }
 
 template <int N>
 using Int = std::integral_constant<int, N>;
@@ -395,7 +397,7 @@ hipError_t conv_step_t(const cnhwc_causal_conv_desc_t& d, const void* x, const v
 // Run length and workgroups per sequence of the backward pass, from the shape only.
 void bwd_runs(const cnhwc_causal_conv_desc_t& d, int64_t ve, int32_t* run, int64_t* blocks) {
   const int64_t rows = d.l + d.k - 1;
-  *run = pick_run(d.n * rows * ceil_div(d.c, ve), kBwdThreads, 64);
+  *run = pick_run(d.n * rows * ceil_div(d.c, ve), bwd_threads(d.dtype, ve), 64);
   *blocks = ceil_div(rows, int64_t(*run) * kRunsPerBlock);
 }
 
@@ -486,7 +488,7 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd_workspace(const cnhwc_causal_con
   if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
   // the vector and the element form alike: which one runs also depends on the pointers
   uint64_t most = 0;
-  for (int64_t ve : {int64_t(1), 8 / int64_t(dtype_size(desc->dtype))}) {
+  for (int64_t ve : {int64_t(1), int64_t(kBwdChannels)}) {
     int32_t run;
     int64_t blocks;
     bwd_runs(*desc, ve, &run, &blocks);
@@ -524,9 +526,10 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd(const cnhwc_causal_conv_desc_t* 
   bf.out(dstate, state_bytes(d), es, false);
   bf.out(workspace, need, 16, true);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
-  const bool vec = d.k <= 4 && vectors(d, d.x_stride, x, 8) && vectors(d, d.dy_stride, dy, 8) &&
-                   aligned(dstate_out, 8) && aligned(w, 8) && aligned(bias, 8) && aligned(state, 8) &&
-                   aligned(dx, 8) && aligned(dstate, 8);
+  const uint64_t bytes = kBwdChannels * es;
+  const bool vec = d.k <= 4 && vectors(d, d.x_stride, x, int64_t(bytes)) && vectors(d, d.dy_stride, dy, int64_t(bytes)) &&
+                   aligned(dstate_out, bytes) && aligned(w, bytes) && aligned(bias, bytes) && aligned(state, bytes) &&
+                   aligned(dx, bytes) && aligned(dstate, bytes);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   float* part = static_cast<float*>(workspace);
   hipError_t e;
@@ -534,9 +537,9 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd(const cnhwc_causal_conv_desc_t* 
     return conv_bwd_t<decltype(dt)::value, decltype(v)::value>(d, dy, dstate_out, x, w, bias, state, lengths, dx, dw,
                                                                dbias, dstate, part, s);
   };
-  if (d.dtype == CNHWC_F32) e = vec ? run(Int<CNHWC_F32>{}, Int<2>{}) : run(Int<CNHWC_F32>{}, Int<1>{});
-  else if (d.dtype == CNHWC_F16) e = vec ? run(Int<CNHWC_F16>{}, Int<4>{}) : run(Int<CNHWC_F16>{}, Int<1>{});
-  else e = vec ? run(Int<CNHWC_BF16>{}, Int<4>{}) : run(Int<CNHWC_BF16>{}, Int<1>{});
+  if (d.dtype == CNHWC_F32) e = vec ? run(Int<CNHWC_F32>{}, Int<kBwdChannels>{}) : run(Int<CNHWC_F32>{}, Int<1>{});
+  else if (d.dtype == CNHWC_F16) e = vec ? run(Int<CNHWC_F16>{}, Int<kBwdChannels>{}) : run(Int<CNHWC_F16>{}, Int<1>{});
+  else e = vec ? run(Int<CNHWC_BF16>{}, Int<kBwdChannels>{}) : run(Int<CNHWC_BF16>{}, Int<1>{});
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }
 

@@ -30,11 +30,12 @@ __device__ __forceinline__ Elem<DT> from_f(float v) {
   else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
 }
 
-// V consecutive elements: 16 or 8 aligned bytes, or V is 1.
+// V consecutive elements: 16, 8 or 4 aligned bytes, or V is 1.
 template <int DT, int V>
 struct Pack { Elem<DT> e[V]; };
 template <int DT, int V>
-using PackBits = std::conditional_t<V * sizeof(Elem<DT>) == 16, uint4, uint2>;
+using PackBits = std::conditional_t<V * sizeof(Elem<DT>) == 16, uint4,
+                                    std::conditional_t<V * sizeof(Elem<DT>) == 8, uint2, uint32_t>>;
 
 template <int DT, int V>
 __device__ __forceinline__ Pack<DT, V> load_pack(const Elem<DT>* p) {
@@ -179,9 +180,13 @@ __device__ __forceinline__ float softplus(float x, float& s) {
   s = x < 0.0f ? e * inv : inv;
   return (x > 0.0f ? x : 0.0f) + __builtin_fmaf(__builtin_amdgcn_logf(w), 0.693147181f, left * inv);
 }
+// The value alone: 1 / w scales only the correction there, the estimate is enough.
 __device__ __forceinline__ float softplus(float x) {
-  float s;
-  return softplus(x, s);
+  const float e = exp_full(-__builtin_fabsf(x));
+  const float w = 1.0f + e;
+  const float left = e - (w - 1.0f);
+  return (x > 0.0f ? x : 0.0f) +
+         __builtin_fmaf(__builtin_amdgcn_logf(w), 0.693147181f, left * __builtin_amdgcn_rcpf(w));
 }
 
 // Valid positions of sequence n.
