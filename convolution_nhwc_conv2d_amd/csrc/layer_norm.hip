@@ -58,6 +58,23 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[16], int slot) {
   }
 }
 
+// Two sums at once.
+template <int TPR>
+__device__ __forceinline__ void row_sums(float& v, float& w, float (*red)[2][16], int slot) {
+  v = group_sum<(TPR < 64 ? TPR : 64)>(v);
+  w = group_sum<(TPR < 64 ? TPR : 64)>(w);
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      red[slot][0][threadIdx.x >> 6] = v;
+      red[slot][1][threadIdx.x >> 6] = w;
+    }
+    __syncthreads();
+    v = red[slot][0][0], w = red[slot][1][0];
+#pragma unroll
+    for (int i = 1; i < TPR / 64; ++i) v += red[slot][0][i], w += red[slot][1][i];
+  }
+}
+
 template <int DT, int VE, int NV, int TPR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(
     const Elem<DT>* __restrict__ x, const void* __restrict__ w, const void* __restrict__ b,
@@ -175,7 +192,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_kernel(
     float* __restrict__ part, LnGeo g) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
   constexpr int kGroups = kThreads / TPR;
-  __shared__ float red[4][16];
+  __shared__ float red[2][2][16];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   float wf[NV * VE], dw[NV * VE], db[NV * VE];
 #pragma unroll
@@ -192,41 +209,61 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_kernel(
     }
   }
   const int64_t step = int64_t(gridDim.x) * kGroups;
-  int phase = 0;
-  // a workgroup-wide row takes part in barriers: its row index is uniform there
-  for (int64_t row = int64_t(blockIdx.x) * kGroups + grp; row < g.rows; row += step) {
-    const Elem<DT>* xr = x + row_offset(row, g.l, g.xs);
-    const Elem<DT>* gr = dy + row_offset(row, g.l, g.dys);
-    Pack<DT, VE> px[NV], pg[NV];
+  // small tiles keep g and xh, and the next row's loads are under way meanwhile
+  constexpr bool kAhead = NV * VE <= 8 && TPR <= 256;
+  Pack<DT, VE> px[NV], pg[NV];
+  float mu = 0.0f, rs = 0.0f;
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+    const bool ok = row < g.rows;
+    const Elem<DT>* xr = x + (ok ? row_offset(row, g.l, g.xs) : 0);
+    const Elem<DT>* gr = dy + (ok ? row_offset(row, g.l, g.dys) : 0);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int32_t c0 = (i * TPR + t) * VE;
-      if (c0 < g.c) {
-        px[i] = load_pack<DT, VE>(xr + c0);
-        pg[i] = load_pack<DT, VE>(gr + c0);
-      } else {
-        px[i] = pg[i] = Pack<DT, VE>{};
+      Pack<DT, VE> a{}, b{};
+      if (ok && c0 < g.c) {
+        a = load_pack<DT, VE>(xr + c0);
+        b = load_pack<DT, VE>(gr + c0);
       }
+      px[i] = a;
+      pg[i] = b;
     }
-    const float mu = mean[row], rs = rstd[row];
-    float s1 = 0.0f, s2 = 0.0f;
+    mu = ok ? mean[row] : 0.0f;
+    rs = ok ? rstd[row] : 0.0f;
+  };
+  int slot = 0;
+  // a workgroup-wide row takes part in barriers: its row index is uniform there
+  int64_t row = int64_t(blockIdx.x) * kGroups + grp;
+  if constexpr (kAhead) load(row);
+  for (; row < g.rows; row += step, slot ^= 1) {
+    if constexpr (!kAhead) load(row);
+    // g and xh of an element, from the row as it was loaded (0 past the row,
+    // whatever the statistics)
+    auto terms = [&](int i, int e, float& v, float& xh) __attribute__((always_inline)) {
+      v = to_f<DT>(pg[i].e[e]) * wf[i * VE + e];
+      xh = !kAhead || (i * TPR + t) * VE < g.c ? (to_f<DT>(px[i].e[e]) - mu) * rs : 0.0f;
+    };
+    float xh[kAhead ? NV * VE : 1], v[kAhead ? NV * VE : 1], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if ((i * TPR + t) * VE >= g.c) continue;
+      if (!kAhead && (i * TPR + t) * VE >= g.c) continue;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const float xh = (to_f<DT>(px[i].e[e]) - mu) * rs;
+        const int k = i * VE + e, h = kAhead ? k : 0;
+        terms(i, e, v[h], xh[h]);
         const float d = to_f<DT>(pg[i].e[e]);
-        const float v = d * wf[i * VE + e];
-        s1 += v;
-        s2 = __builtin_fmaf(v, xh, s2);
-        dw[i * VE + e] = __builtin_fmaf(d, xh, dw[i * VE + e]);
-        db[i * VE + e] += d;
+        s1 += v[h];
+        s2 = __builtin_fmaf(v[h], xh[h], s2);
+        dw[k] = __builtin_fmaf(d, xh[h], dw[k]);
+        db[k] += d;
       }
     }
-    s1 = row_sum<TPR>(s1, red, phase) * g.inv_c;
-    s2 = row_sum<TPR>(s2, red, phase + 1) * g.inv_c;
-    phase ^= 2;
+    const float r = rs;
+    if constexpr (kAhead) load(row + step);
+    row_sums<TPR>(s1, s2, red, slot);
+    if constexpr (!kAhead) asm volatile("" : "+v"(mu), "+v"(rs));  // made again, not held
+    s1 *= g.inv_c;
+    s2 *= g.inv_c;
     Elem<DT>* dr = dx + row * g.c;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -235,9 +272,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_kernel(
       Pack<DT, VE> o;
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const float xh = (to_f<DT>(px[i].e[e]) - mu) * rs;
-        const float v = to_f<DT>(pg[i].e[e]) * wf[i * VE + e];
-        o.e[e] = from_f<DT>(rs * (v - s1 - xh * s2));
+        const int h = kAhead ? i * VE + e : 0;
+        if constexpr (!kAhead) terms(i, e, v[0], xh[0]);
+        o.e[e] = from_f<DT>(r * (v[h] - s1 - xh[h] * s2));
       }
       store_pack<DT, VE>(dr + c0, o);
     }
