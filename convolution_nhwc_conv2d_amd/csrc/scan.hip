@@ -720,7 +720,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo
   // half tile's states and two sets of partial sums, up to 32 one set
   constexpr bool kSaveLow = NS <= 32;
   constexpr int kParts = NS <= 16 ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) float bc[kTile * 2 * NS];
+  __shared__ __attribute__((aligned(16))) float bc2[2][kTile * 2 * NS];
   __shared__ float part[kParts][kWaves][kTile][2 * NS];
   __shared__ float4 enter[kWaves][SPL][64];                // the state that enters the chunk
   __shared__ float4 low[kSaveLow ? kHalf - 1 : 1][kWaves][SPL][64];  // states 1, 2, 3 of a tile
@@ -758,9 +758,16 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo
   float dskip = 0.0f, dbias = 0.0f;
   const int64_t rows = (int64_t(gridDim.x) / (int64_t(g.col_blocks) * g.chunks)) * g.l;  // N * L
   const int64_t col = blockIdx.x % g.col_blocks;
-  for (int32_t k = (t_end - t_begin + kTile - 1) / kTile - 1; k >= 0; --k) {
+  const int32_t tiles = (t_end - t_begin + kTile - 1) / kTile;
+  st.stage(bn, cn, g, t_begin + (tiles - 1) * kTile, t_valid);
+  st.put(bc2[(tiles - 1) & 1]);
+  __syncthreads();
+  // One barrier to a tile: it stands behind the tile's partial sums and the next
+  // tile's b and c.
+  for (int32_t k = tiles - 1; k >= 0; --k) {
     const int32_t t0 = t_begin + k * kTile;
-    st.stage(bn, cn, g, t0, t_valid);
+    const float* bc = bc2[k & 1];
+    if (k > 0) st.stage(bn, cn, g, t0 - kTile, t_valid);
     float df[kTile], sg[kTile];
     Elem<DT> u_t[kTile];
     Two<DT> yz[kTile];  // dy and gate
@@ -795,9 +802,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo
         for (int i = 0; i < SPL; ++i)
           h0[j][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(quad_lane(sum, j) * a2[j][i]), h0[j][i], hk[j][i]);
     }
-    __syncthreads();
-    st.put(bc);
-    __syncthreads();
     if (g.softplus) {
 #pragma unroll
       for (int i = 0; i < kTile; ++i) df[i] = softplus(df[i], sg[i]);
@@ -910,10 +914,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo
     }
 #pragma unroll
     for (int i = kHalf - 1; i >= 0; --i) back(i, hs[i], hs[i + 1]);
+    if (k > 0) st.put(bc2[(k - 1) & 1]);
     __syncthreads();
-    // the workgroup's channels.  The next tile's barriers stand between these
-    // reads and the writes of the tile after it; with one buffer, its first one
-    // between these reads and its own writes.
+    // the workgroup's channels; with two buffers, the next tile's barrier stands
+    // between these reads and the writes of the tile after it
     for (int i = threadIdx.x; i < kTile * 2 * NS; i += 256) {
       const int t = i / (2 * NS), q = i % (2 * NS), which = q / NS, s = q % NS;
       if (t0 + t >= t_valid || s >= g.s) continue;
@@ -922,6 +926,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo
       for (int w = 1; w < kWaves; ++w) v += part[k % kParts][w][t][q];
       out.bc_part[((col * rows + n * g.l + t0 + t) * 2 + which) * g.s + s] = v;
     }
+    if constexpr (kParts == 1) __syncthreads();
   }
   float* pp = out.param_part + c_id * (ds + 2 * int64_t(g.d));
   store_states<SL, SPL>(da, pp, at, g);
