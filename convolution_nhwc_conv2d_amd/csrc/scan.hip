@@ -5,8 +5,10 @@
 //   y[t,d] = (sum_s c[t,s] h[t,d,s] + skip[d] u[t,d]) silu(gate[t,d])
 //
 // Every channel and state has its own decay, so no product over t or s has the
-// form of a matrix product: the work is vector instructions, and of those the
-// exponential (a quarter-rate instruction) costs as much as the other four.
+// form of a matrix product: the work is vector instructions.  Per position,
+// channel and state the forward pass needs four products and sums and one
+// exponential, which counts as two (measured: 4.4 cycles a wavefront for a
+// product and sum, 9.0 for an exponential).
 //
 // A wavefront holds 64 / SL groups of SL lanes; a group holds four channels and
 // SL * SPL states, each lane SPL states of all four channels.  So per position a
@@ -20,6 +22,11 @@
 // state and leaves the chunk's end state and sum of D; a second one, along the
 // chunks, turns these into the state that enters every chunk (a chunk scales
 // what enters it by exp(a sum D)); the last runs each chunk from there.
+//
+// Measured, 1 x 16384 x 2048 channels x 16 states, bf16: 279 us (7982 us in one
+// chunk), of them 124 the local chunks, 15 the join, 171 the outputs, when each
+// kernel is timed alone.  The vector pipes are busy 82 and 84% of the kernels'
+// cycles; the bytes that have to move (270 MB) would take 56 us.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -516,7 +523,14 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanIn<DT> in, ScanGeo g
 // The state at every tile of a chunk costs less to keep than to run again: the
 // chunk kernel leaves it (from its zero start) with the sum of D up to there,
 // in the order of its lanes, and the gradient kernel adds what the entering
-// state has become by then, one exponential per state and tile.
+// state has become by then, one exponential per state and tile.  (Tiles of four
+// positions instead of eight move twice the states: 789 us against 710.)
+//
+// Measured, 8 x 2048 x 2048 channels x 16 states, bf16: 701 us, of them 205 the
+// chunk kernel, 17 the join, 545 the gradient, 14 the two sums.  The gradient
+// kernel issues 394 vector instructions per position and wavefront (16 elements
+// a lane) and keeps the vector pipes busy 73% of its cycles, with two wavefronts
+// to a SIMD (registers); the bytes that have to move (472 MB) would take 98 us.
 
 template <int DT>
 struct ScanOut {
