@@ -346,8 +346,8 @@ int32_t pick_run(int64_t work, int64_t threads, int32_t most) {
 // Measured forward: 4 x 4096 x 4096 bf16 with 512 threads 52 us, 2048 56, 4096 68.
 constexpr int64_t kFwdThreads = 512;
 // Backward, with two channels to a thread: 5 x 2047 x 2048 f16 of several
-// lengths with 768 threads 38 us, 1536 33, 3072 35; 2 x 2048 x 2048 f32 30, 35,
-// 38.  (Four f16 channels to a thread, in more registers: 35 us at best.)
+// lengths with 768 threads 38 us, 1536 33, twice that 35; 2 x 2048 x 2048 f32
+// 30, 35, 38.  (Four f16 channels to a thread, in more registers: 35 us at best.)
 constexpr int kBwdChannels = 2;
 int64_t bwd_threads(int32_t dtype, int64_t ve) { return dtype != CNHWC_F32 && ve == kBwdChannels ? 1536 : 768; }
 
@@ -531,8 +531,8 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd(const cnhwc_causal_conv_desc_t* 
   bf.out(dstate, state_bytes(d), es, false);
   bf.out(workspace, need, 16, true);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
-  const uint64_t bytes = kBwdChannels * es;
-  const bool vec = d.k <= 4 && vectors(d, d.x_stride, x, int64_t(bytes)) && vectors(d, d.dy_stride, dy, int64_t(bytes)) &&
+  const int64_t bytes = kBwdChannels * int64_t(es);
+  const bool vec = d.k <= 4 && vectors(d, d.x_stride, x, bytes) && vectors(d, d.dy_stride, dy, bytes) &&
                    aligned(dstate_out, bytes) && aligned(w, bytes) && aligned(bias, bytes) && aligned(state, bytes) &&
                    aligned(dx, bytes) && aligned(dstate, bytes);
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);

@@ -1101,9 +1101,11 @@ cnhwc_status_t check_desc(const cnhwc_scan_desc_t* d, bool bwd) {
       !strides_ok(d->n, d->l, d->d, d->gate_stride) || (bwd && !strides_ok(d->n, d->l, d->d, d->dy_stride)))
     return CNHWC_ERR_INVALID_ARGUMENT;
   if (d->s > CNHWC_SCAN_MAX_STATE) return CNHWC_ERR_UNSUPPORTED;
-  // positions fit 32 bits with a chunk's overhang; grids and offsets stay in range
-  if (d->l > INT_MAX - 1024 || d->d > (1ll << 23) || !dense_ok(d->n, d->l, d->d * d->s) ||
-      d->n * ceil_div(d->l, 16) * ceil_div(d->d, 64) > (1ll << 23))
+  // positions fit 32 bits with a chunk's overhang; 64-bit offsets; the grids of
+  // the backward pass (chunks of 128 positions at these sizes) and of its sums
+  if (d->l > INT_MAX - 1024 || d->d > (1ll << 23) || d->d * (d->s + 2) > (1ll << 27) ||
+      !dense_ok(d->n, d->l, d->d * d->s) ||
+      d->n * ceil_div(d->l, 128) * ceil_div(d->d, 64) > (1ll << 23))
     return CNHWC_ERR_UNSUPPORTED;
   return CNHWC_OK;
 }
