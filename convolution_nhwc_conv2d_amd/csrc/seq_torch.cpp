@@ -10,6 +10,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -401,12 +402,13 @@ Tensor selective_scan_step(const Tensor& u, const Tensor& delta, const Tensor& a
 
 PYBIND11_MODULE(_seq, m) {
   m.def("set_error", [](py::object cls) { g_error = cls.release().ptr(); });
-  m.def("layer_norm", &layer_norm);
-  m.def("layer_norm_backward", &layer_norm_backward);
-  m.def("causal_conv1d", &causal_conv1d);
-  m.def("causal_conv1d_backward", &causal_conv1d_backward);
-  m.def("causal_conv1d_step", &causal_conv1d_step);
-  m.def("selective_scan", &selective_scan);
-  m.def("selective_scan_backward", &selective_scan_backward);
-  m.def("selective_scan_step", &selective_scan_step);
+  // torch's own errors (an allocation that fails) keep their Python types
+  m.def("layer_norm", torch::wrap_pybind_function(layer_norm));
+  m.def("layer_norm_backward", torch::wrap_pybind_function(layer_norm_backward));
+  m.def("causal_conv1d", torch::wrap_pybind_function(causal_conv1d));
+  m.def("causal_conv1d_backward", torch::wrap_pybind_function(causal_conv1d_backward));
+  m.def("causal_conv1d_step", torch::wrap_pybind_function(causal_conv1d_step));
+  m.def("selective_scan", torch::wrap_pybind_function(selective_scan));
+  m.def("selective_scan_backward", torch::wrap_pybind_function(selective_scan_backward));
+  m.def("selective_scan_step", torch::wrap_pybind_function(selective_scan_step));
 }
