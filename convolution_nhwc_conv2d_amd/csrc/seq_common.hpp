@@ -152,10 +152,14 @@ __device__ __forceinline__ float rcp_full(float v) {
   return __builtin_fmaf(r, __builtin_fmaf(-v, r, 1.0f), r);
 }
 
-// 1 / (1 + e^-x); the exponent is held at 80, where the result is 1.8e-35.
+// 1 / (1 + e^-x), from e = e^-|x| in (0, 1] (below 0: e / (1 + e)), so nothing
+// overflows and the result falls to 0 with e: silu and its slope, which multiply
+// it by x, are 0 for any finite x below -88.  (Held at a smallest value instead,
+// it gave silu(-1e35) = -1.8.)
 __device__ __forceinline__ float sigmoid(float x) {
-  const float n = -x > 80.0f ? 80.0f : -x;
-  return rcp_full(1.0f + exp_full(n));
+  const float e = exp_full(-__builtin_fabsf(x));
+  const float inv = rcp_full(1.0f + e);
+  return x < 0.0f ? e * inv : inv;
 }
 
 // The same for a result that is rounded to DT: a 16-bit one takes the plain

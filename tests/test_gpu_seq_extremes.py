@@ -1,0 +1,72 @@
+"""The sequence operators on values at the ends of their types."""
+import numpy as np
+import pytest
+import torch
+
+import seq_reference as R
+from gpu_util import bits
+
+pytestmark = pytest.mark.gpu
+
+cn = pytest.importorskip("convolution_nhwc_conv2d_amd")
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def _large(dt):
+    """100, 1e30 where the type holds it, and its largest value."""
+    return [100.0] + ([] if dt == "f16" else [1e30]) + [torch.finfo(DT[dt]).max]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_conv_silu_of_large_values(dt):
+    """One tap of 1: pre is x itself.  For x <= -100 silu and its slope are below
+    2^-126, so 0 to the type; for x >= 100 they are x and 1 to its last place."""
+    v = _large(dt)
+    x = torch.tensor([-t for t in v] + v, dtype=torch.float64).to(DT[dt]).cuda()
+    x = x.repeat(2, 5, 8)  # [2, 5, C]: vectors and, cut by one channel, single elements
+    for c in (x.shape[2], x.shape[2] - 1):
+        xc = x[..., :c].contiguous()
+        w = torch.zeros(c, 4, dtype=xc.dtype, device="cuda")
+        w[:, 3] = 1
+        low = (xc < 0).cpu()
+        tiny = R.TINY[xc.dtype]
+        y = cn.causal_conv1d(xc, w, activation="silu")
+        assert (R.f64(y)[low].abs() <= tiny).all() and torch.equal(y.cpu()[~low], xc.cpu()[~low])
+        state = torch.zeros(2, 3, c, dtype=xc.dtype, device="cuda")
+        assert torch.equal(bits(cn.causal_conv1d_step(xc[:, 0], state, w, activation="silu")), bits(y[:, 0]))
+        dy = torch.full_like(xc, 2.0)
+        r = cn.causal_conv1d_backward(dy, xc, w, torch.zeros(c, dtype=xc.dtype, device="cuda"), activation="silu")
+        assert (R.f64(r.x)[low].abs() <= tiny).all() and (R.f64(r.x)[~low] == 2.0).all()
+        assert torch.equal(R.f64(r.bias), (~low).double().sum((0, 1)) * 2.0)
+
+
+def _gated(dt, s):
+    """Channels with the large gates, half of them negative; products with the
+    positive ones stay inside the type."""
+    v = _large(dt)
+    gates = torch.tensor(([-t for t in v] + v) * 8, dtype=torch.float64)
+    d, n, l = len(gates), 2, 12
+    g = np.random.default_rng([1, s])
+    t = DT[dt]
+    r = lambda *sh, dtype=t, **kw: R.rand(g, *sh, **kw).to(dtype).cuda()
+    f = torch.float32
+    low = gates < 0
+    dy = R.rand(g, n, l, d) * torch.where(low, 4.0, 0.01)
+    return dict(u=r(n, l, d), delta=r(n, l, d), a=-r(d, s, dtype=f).abs() - 0.05, b=r(n, l, s),
+                c=r(n, l, s, scale=0.005), gate=gates.to(t).cuda().expand(n, l, d).contiguous(), dy=dy.to(t).cuda(),
+                low=low)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("s", [8, 16])
+def test_scan_gates_of_large_values(s, dt):
+    """The reference's magnitudes take silu of the gate, so a closed gate's bound is 2^-126."""
+    i = _gated(dt, s)
+    args = (i["u"], i["delta"], i["a"], i["b"], i["c"])
+    y, last = cn.selective_scan(*args, gate=i["gate"], softplus=True, return_state=True)
+    ref = [R.f64(t) for t in args] + [None, R.f64(i["gate"]), None, True, None, None]
+    R.check(y, R.scan(*ref)[0], R.scan(*ref, absolute=True)[0], 16 * 12 + 64, "y")
+    state = torch.zeros_like(last)
+    tok = [t[:, 0] if t.dim() == 3 else t for t in args]
+    assert torch.equal(bits(cn.selective_scan_step(*tok, state, gate=i["gate"][:, 0], softplus=True)), bits(y[:, 0]))
