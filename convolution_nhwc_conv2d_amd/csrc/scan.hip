@@ -862,7 +862,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo
     auto back = [&](int i, const float (&before)[4][SPL], const float (&after)[4][SPL]) __attribute__((always_inline)) {
       const float u = to_f<DT>(u_t[i]), yg = yz[i].first(), z = yz[i].second();
       const float sz = in.gate ? sigmoid_for<DT>(z) : 0.0f;
-      const float gy = in.gate ? yg * z * sz : yg;
+      const float gy = in.gate ? yg * (z * sz) : yg;  // yg * z alone can overflow where sz is 0
       float bf[SPL], cf[SPL], db[SPL], dc[SPL];
       const float dl = again(df[i]);
       const float dx = dl * u;

@@ -70,3 +70,27 @@ def test_scan_gates_of_large_values(s, dt):
     state = torch.zeros_like(last)
     tok = [t[:, 0] if t.dim() == 3 else t for t in args]
     assert torch.equal(bits(cn.selective_scan_step(*tok, state, gate=i["gate"][:, 0], softplus=True)), bits(y[:, 0]))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("s", [8, 16])
+def test_scan_gradient_of_large_gates(s, dt):
+    """Through a closed gate nothing comes back, whatever the gradient in front of
+    it; the reference's magnitude of dgate grows with the gate, so that one is
+    compared with 0 (|z silu'(z)| is below 2^-126 there) and with dy y."""
+    i = _gated(dt, s)
+    args = (i["u"], i["delta"], i["a"], i["b"], i["c"])
+    r = cn.selective_scan_backward(i["dy"], *args, gate=i["gate"], softplus=True)
+    ref = [R.f64(i["dy"])] + [R.f64(t) for t in args] + [None, R.f64(i["gate"]), None, True, None, None, None]
+    want, mag = R.scan_backward(*ref), R.scan_backward(*ref, absolute=True)
+    k = 32 * 12 + 128
+    for name in ("u", "delta", "a", "b", "c"):
+        R.check(getattr(r, name), want[name], mag[name], k + (2 * 12 if name == "a" else 0), "d" + name)
+    low = i["low"]
+    dgate = R.f64(r.gate)
+    assert (dgate[..., low].abs() <= R.TINY[DT[dt]]).all()
+    y = cn.selective_scan(*[t.float() for t in args], softplus=True)  # without the gate
+    dyy = R.f64(i["dy"]) * R.f64(y)
+    bound = (R.ROUND[DT[dt]] + 2 * k * R.EPS) * dyy.abs() + k * R.EPS * R.f64(i["dy"]).abs() * R.scan(
+        *ref[1:6], None, None, None, True, None, None, absolute=True)[0] + R.TINY[DT[dt]]
+    assert ((dgate - dyy).abs() <= bound)[..., ~low].all()
