@@ -29,6 +29,7 @@
 // cycles; the bytes that have to move (270 MB) would take 56 us.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <climits>
 
 #include "internal.hpp"
@@ -157,6 +158,20 @@ __device__ __forceinline__ void settle(float (&h)[4][SPL]) {
   for (int j = 0; j < 4; ++j) settle(h[j]);
 }
 
+// a log2(e), finite for a of minus infinity too: where D is 0, as past the
+// valid positions, the state stands still, and 0 times infinity is no number.
+__device__ __forceinline__ float rate(float a) {
+  const float r = a * kLog2e;
+  return r < -FLT_MAX ? -FLT_MAX : r;
+}
+template <int SPL>
+__device__ __forceinline__ void rates(float (&a)[4][SPL]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) a[j][i] = rate(a[j][i]);
+}
+
 template <int SPL>
 __device__ __forceinline__ void copy(const float (&from)[4][SPL], float (&to)[4][SPL]) {
 #pragma unroll
@@ -281,10 +296,11 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanIn<DT> in, ScanGeo g,
 
   float a2[4][SPL], h[4][SPL];
   load_states<SL, SPL>(a2, in.a, at, g);
+  rates(a2);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, h[j][i] = 0.0f;
+    for (int i = 0; i < SPL; ++i) h[j][i] = 0.0f;
   const int64_t ds = int64_t(g.d) * g.s;
   if constexpr (!LOCAL) {
     if (chunk > 0) get_lanes<SPL>(states, blockIdx.x, h);
@@ -391,7 +407,7 @@ struct Column {
     sum_step = int64_t(g.col_blocks) * kWaves * 64;
     live = d < g.d && s < g.s;
     user = (n * g.d + d) * g.s + s;
-    a2 = live ? a[d * g.s + s] * kLog2e : 0.0f;
+    a2 = live ? rate(a[d * g.s + s]) : 0.0f;
   }
 };
 
@@ -488,7 +504,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanIn<DT> in, ScanGeo g
       float v = 0.0f;
 #pragma unroll
       for (int k = 0; k < SPL; ++k) {
-        const float e = __builtin_amdgcn_exp2f(dl[q] * (a2[k] * kLog2e));
+        const float e = __builtin_amdgcn_exp2f(dl[q] * rate(a2[k]));
         h[q][k] = __builtin_fmaf(e, h[q][k], dx * bf[q][k]);
         v = __builtin_fmaf(h[q][k], cf[q][k], v);
       }
@@ -565,10 +581,11 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_local_kernel(ScanIn<DT> in, S
 
   float a2[4][SPL], h[4][SPL], p[4][SPL], r[4][SPL];
   load_states<SL, SPL>(a2, in.a, at, g);
+  rates(a2);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, h[j][i] = 0.0f, p[j][i] = 1.0f, r[j][i] = 0.0f;
+    for (int i = 0; i < SPL; ++i) h[j][i] = 0.0f, p[j][i] = 1.0f, r[j][i] = 0.0f;
   const float bias = in.delta_bias ? in.delta_bias[at.at] : 0.0f;
   const Elem<DT>* un = in.u + n * g.us[0];
   const Elem<DT>* dn = in.delta + n * g.ds[0];
@@ -753,11 +770,12 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanIn<DT> in, ScanGeo
 #pragma unroll
   for (int i = 0; i < SPL; ++i) enter[wave][i][lane] = states[lane_order<SPL>(blockIdx.x) + i * 64];
   load_states<SL, SPL>(a2, in.a, at, g);
+  rates(a2);
   get_lanes<SPL>(backs, blockIdx.x, carry);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) a2[j][i] *= kLog2e, da[j][i] = 0.0f;
+    for (int i = 0; i < SPL; ++i) da[j][i] = 0.0f;
   const float bias = in.delta_bias ? in.delta_bias[at.at] : 0.0f;
   const float skip = in.skip ? in.skip[at.at] : 0.0f;
   const Elem<DT>* un = in.u + n * g.us[0];

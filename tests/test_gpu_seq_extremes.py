@@ -94,3 +94,38 @@ def test_scan_gradient_of_large_gates(s, dt):
     bound = (R.ROUND[DT[dt]] + 2 * k * R.EPS) * dyy.abs() + k * R.EPS * R.f64(i["dy"]).abs() * R.scan(
         *ref[1:6], None, None, None, True, None, None, absolute=True)[0] + R.TINY[DT[dt]]
     assert ((dgate - dyy).abs() <= bound)[..., ~low].all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("s", [5, 16, 32])
+def test_scan_rates_without_end(s, dt):
+    """a of minus infinity (and of the lowest float): the state holds the newest
+    position alone, and past the lengths it stands still.  The reference of the
+    gradient takes -1e30, whose decay is the same 0 and whose products are finite."""
+    g = np.random.default_rng([2, s])
+    n, l, d = 3, 21, 40
+    t = DT[dt]
+    r = lambda *sh, dtype=t, **kw: R.rand(g, *sh, **kw).to(dtype).cuda()
+    f = torch.float32
+    i = dict(u=r(n, l, d), delta=r(n, l, d), a=-r(d, s, dtype=f).abs() - 0.05, b=r(n, l, s), c=r(n, l, s))
+    finite = i["a"].clone()
+    i["a"][::2, ::2], finite[::2, ::2] = -float("inf"), -1e30
+    i["a"][1::4, 1::2], finite[1::4, 1::2] = torch.finfo(f).min, -1e30
+    lengths = torch.tensor([21, 6, 0], dtype=torch.int32, device="cuda")
+    state, dy, dstate = r(n, d, s, dtype=f), r(n, l, d), r(n, d, s, dtype=f)
+    y, last = cn.selective_scan(*i.values(), softplus=True, state=state, lengths=lengths, return_state=True)
+    ref = [R.f64(v) for v in dict(i, a=finite).values()] + [None, None, None, True, R.f64(state), lengths]
+    for got, want, mag in zip((y, last), R.scan(*ref), R.scan(*ref, absolute=True)):
+        R.check(got, want, mag, 16 * l + 64, "forward")
+    assert torch.equal(last[2], state[2])
+    tok = [v[:, 0] if v.dim() == 3 else v for v in i.values()]
+    moved = state.clone()
+    y0 = cn.selective_scan_step(*tok, moved, softplus=True)
+    y1, s1 = cn.selective_scan(*[v[:, :1] if v.dim() == 3 else v for v in i.values()], softplus=True, state=state,
+                               return_state=True)
+    assert torch.equal(bits(y0), bits(y1[:, 0])) and torch.equal(bits(moved), bits(s1))
+    grads = cn.selective_scan_backward(dy, *i.values(), softplus=True, state=state, lengths=lengths, dstate=dstate)
+    args = [R.f64(dy)] + ref + [R.f64(dstate)]
+    want, mag = R.scan_backward(*args), R.scan_backward(*args, absolute=True)
+    for name in ("u", "delta", "a", "b", "c", "state"):
+        R.check(getattr(grads, name), want[name], mag[name], 32 * l + 128 + (n * l if name == "a" else 0), "d" + name)
