@@ -187,6 +187,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(
 // A workgroup: 32 channel vectors by 8 runs of positions of one sequence, over
 // the L + K - 1 rows j of dX.  part: per workgroup column of 32 vectors and per
 // (sequence, workgroup along it) one row [C*K | C] of dw and dbias sums.
+// first_block: the launch's first workgroup among all of the pass.
 constexpr int kLanes = 32, kRunsPerBlock = 8;
 
 template <int DT, int V, int K>
@@ -194,9 +195,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(
     const Elem<DT>* __restrict__ dy, const Elem<DT>* __restrict__ dfin, const Elem<DT>* __restrict__ x,
     const Elem<DT>* __restrict__ wp, const Elem<DT>* __restrict__ bp, const Elem<DT>* __restrict__ state,
     const int32_t* __restrict__ lengths, Elem<DT>* __restrict__ dx, Elem<DT>* __restrict__ dstate,
-    float* __restrict__ part, ConvGeo g, int64_t col_blocks) {
-  const int64_t row_id = blockIdx.x / col_blocks;
-  const int32_t vec = int32_t(blockIdx.x - row_id * col_blocks) * kLanes + int32_t(threadIdx.x & (kLanes - 1));
+    float* __restrict__ part, ConvGeo g, int64_t col_blocks, int64_t first_block) {
+  const int64_t block = first_block + blockIdx.x, row_id = block / col_blocks, col = block - row_id * col_blocks;
+  const int32_t vec = int32_t(col) * kLanes + int32_t(threadIdx.x & (kLanes - 1));
   const int64_t n = row_id / g.runs;
   const int64_t j0 = ((row_id - n * g.runs) * kRunsPerBlock + threadIdx.x / kLanes) * g.run;
   const int64_t rows = int64_t(g.l) + K - 1;
@@ -304,7 +305,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(
   }
   __syncthreads();
   float* pr = part + row_id * (int64_t(g.c) * (K + 1));
-  const int64_t cb = int64_t(blockIdx.x - row_id * col_blocks) * kLanes * V;
+  const int64_t cb = col * kLanes * V;
   for (int i = threadIdx.x; i < kLanes * V * (K + 1); i += 256) {
     const float r = sum[0][i] + sum[1][i] + sum[2][i] + sum[3][i];
     if (i < kLanes * V * K) {
@@ -406,6 +407,11 @@ void bwd_runs(const cnhwc_causal_conv_desc_t& d, int64_t ve, int32_t* run, int64
   *blocks = ceil_div(rows, int64_t(*run) * kRunsPerBlock);
 }
 
+// Workgroups of one launch: 2^31 threads, where a launch takes fewer than 2^32.
+// Every sequence has a workgroup of its own at least, so very many short ones
+// take several launches.
+constexpr int64_t kMostBlocks = 1ll << 23;
+
 template <int DT, int V>
 hipError_t conv_bwd_t(const cnhwc_causal_conv_desc_t& d, const void* dy, const void* dfin, const void* x,
                       const void* w, const void* b, const void* state, const int32_t* lengths, void* dx, void* dw,
@@ -414,14 +420,19 @@ hipError_t conv_bwd_t(const cnhwc_causal_conv_desc_t& d, const void* dy, const v
   ConvGeo g = geo_of(d, V);
   bwd_runs(d, V, &g.run, &g.runs);
   const int64_t cols = ceil_div(g.vecs, kLanes), parts = d.n * g.runs;
-  with_taps(d.k, [&](auto k) {
-    constexpr int K = decltype(k)::value;
-    if constexpr (V == 1 || K <= 4)  // more taps than four hold too many registers with vectors
-      hipLaunchKernelGGL((conv_bwd_kernel<DT, V, K>), dim3(unsigned(cols * parts)), dim3(256), 0, st,
-                         static_cast<const E*>(dy), static_cast<const E*>(dfin), static_cast<const E*>(x),
-                         static_cast<const E*>(w), static_cast<const E*>(b), static_cast<const E*>(state), lengths,
-                         static_cast<E*>(dx), static_cast<E*>(dstate), part, g, cols);
-  });
+  for (int64_t first = 0; first < cols * parts; first += kMostBlocks) {
+    const int64_t blocks = cols * parts - first < kMostBlocks ? cols * parts - first : kMostBlocks;
+    with_taps(d.k, [&](auto k) {
+      constexpr int K = decltype(k)::value;
+      if constexpr (V == 1 || K <= 4)  // more taps than four hold too many registers with vectors
+        hipLaunchKernelGGL((conv_bwd_kernel<DT, V, K>), dim3(unsigned(blocks)), dim3(256), 0, st,
+                           static_cast<const E*>(dy), static_cast<const E*>(dfin), static_cast<const E*>(x),
+                           static_cast<const E*>(w), static_cast<const E*>(b), static_cast<const E*>(state), lengths,
+                           static_cast<E*>(dx), static_cast<E*>(dstate), part, g, cols, first);
+    });
+    // the sums would read rows that a failed launch did not write
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
   sum_parts<DT>(part, parts, SumOut{{dw, db, nullptr}, {d.c * d.k, d.c, 0}}, false, st);
   return hipGetLastError();
 }
@@ -433,8 +444,8 @@ cnhwc_status_t check_desc(const cnhwc_causal_conv_desc_t* d, bool bwd) {
   if (!strides_ok(d->n, d->l, d->c, d->x_stride)) return CNHWC_ERR_INVALID_ARGUMENT;
   if (bwd && !strides_ok(d->n, d->l, d->c, d->dy_stride)) return CNHWC_ERR_INVALID_ARGUMENT;
   if (d->k > CNHWC_CAUSAL_CONV_MAX_K) return CNHWC_ERR_UNSUPPORTED;
-  // positions fit 32 bits with the run's overhang; the grids of the backward
-  // pass (at least 16384 elements a workgroup) and of its reduction stay in range
+  // positions fit 32 bits with the run's overhang, the workgroups of the backward
+  // pass and the elements 64, and the grid of its reduction stays in range
   if (d->l > INT_MAX - 1024 || d->c > (1ll << 23) || !dense_ok(d->n, d->l + d->k, d->c) ||
       d->n * (d->l + d->k) * d->c > (1ll << 37))
     return CNHWC_ERR_UNSUPPORTED;
