@@ -3,7 +3,9 @@
 // Forward, per row of C channels: mean = sum x / C, var = sum (x - mean)^2 / C,
 // y = (x - mean) rstd w + b.  The row stays in registers as it was loaded, so
 // the variance is the two-pass one (no cancellation) at the traffic of one
-// pass: x read once, y written once.
+// pass: x read once, y written once.  The mean of a row of one constant is that
+// constant: what the product with 1 / C has rounded is put back, and for fp32
+// rows what the sum has rounded too (mean_of, put_right below).
 //
 // Backward, with xh = (x - mean) rstd and g = dy w:
 //   dx = rstd (g - mean(g) - xh mean(g xh)),  dw = sum_rows dy xh,  db = sum_rows dy.
@@ -19,6 +21,8 @@
 // multiple of 16 bytes go element by element; rows wider than the largest
 // register tile are re-read from the cache.
 #include <hip/hip_runtime.h>
+
+#include <cfloat>
 
 #include "internal.hpp"
 #include "seq_common.hpp"
@@ -77,12 +81,37 @@ __device__ __forceinline__ void row_sums(float& v, float& w, float (*red)[2][16]
   }
 }
 
+__device__ __forceinline__ float if_finite(float v) { return __builtin_fabsf(v) <= FLT_MAX ? v : 0.0f; }
+
+// sum / C: the product with 1 / C, and what that leaves of the sum (exact).  A
+// row with an infinity keeps it as its mean.
+__device__ __forceinline__ float mean_of(float sum, const LnGeo& g) {
+  const float m = sum * g.inv_c;
+  return __builtin_fmaf(if_finite(__builtin_fmaf(-float(g.c), m, sum)), g.inv_c, m);
+}
+
+// The variance from the sum of (x - m)^2.  fp32: the sum of x - m beside it says
+// how far the rounded sum of the row has moved m, which matters where the row
+// hardly varies (3000.1 throughout: up to 80 units of the last place, 0.02 of a
+// distance whose scale is sqrt(eps)); m moves back, and m's own distance
+// leaves the variance.  Rows of 16-bit elements of one constant have an exact
+// sum up to thousands of channels, and the second sum costs 65536 x 512 f16 5% (23.2 to
+// 24.4 us; 25088 x 512 f32 16.2 with and without), so they go without.
+template <int DT>
+__device__ __forceinline__ float put_right(float left, float squares, float& m, const LnGeo& g) {
+  if constexpr (DT != CNHWC_F32) return squares * g.inv_c;
+  const float dm = if_finite(left * g.inv_c);
+  const float var = __builtin_fmaf(-dm, dm, squares * g.inv_c);
+  m += dm;
+  return var < 0.0f ? 0.0f : var;  // a NaN stays
+}
+
 template <int DT, int VE, int NV, int TPR>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(
     const Elem<DT>* __restrict__ x, const void* __restrict__ w, const void* __restrict__ b,
     Elem<DT>* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, LnGeo g) {
   constexpr int kThreads = TPR > 256 ? TPR : 256;
-  __shared__ float red[2][16];
+  __shared__ float red[2][2][16];
   const int t = threadIdx.x % TPR;
   // w and b stay in registers where they are few, else each row takes them from
   // the cache again
@@ -116,8 +145,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VE; ++e) s += to_f<DT>(p[i].e[e]);
-    const float mean = row_sum<TPR>(s, red, 0) * g.inv_c;
-    float q = 0.0f;
+    float mean = mean_of(row_sum<TPR>(s, red[0], 0), g);
+    float q = 0.0f, left = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((i * TPR + t) * VE >= g.c) continue;
@@ -125,9 +154,12 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(
       for (int e = 0; e < VE; ++e) {
         const float d = to_f<DT>(p[i].e[e]) - mean;
         q = __builtin_fmaf(d, d, q);
+        if constexpr (DT == CNHWC_F32) left += d;
       }
     }
-    const float var = row_sum<TPR>(q, red, 1) * g.inv_c;
+    if constexpr (DT == CNHWC_F32) row_sums<TPR>(left, q, red, 1);
+    else q = row_sum<TPR>(q, red[1], 0);
+    const float var = put_right<DT>(left, q, mean, g);
     const float rstd = 1.0f / __builtin_sqrtf(var + g.eps);
     if (!live) continue;
     Elem<DT>* yr = y + row * g.c;
@@ -160,17 +192,20 @@ template <int DT>
 __global__ __launch_bounds__(1024) void ln_fwd_wide_kernel(
     const Elem<DT>* __restrict__ x, const void* __restrict__ w, const void* __restrict__ b,
     Elem<DT>* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, LnGeo g) {
-  __shared__ float red[2][16];
+  __shared__ float red[2][2][16];
   for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
     const Elem<DT>* xr = x + row_offset(row, g.l, g.xs);
-    float s = 0.0f, q = 0.0f;
+    float s = 0.0f, q = 0.0f, left = 0.0f;
     for (int64_t c = threadIdx.x; c < g.c; c += 1024) s += to_f<DT>(xr[c]);
-    const float mean = row_sum<1024>(s, red, 0) * g.inv_c;
+    float mean = mean_of(row_sum<1024>(s, red[0], 0), g);
     for (int64_t c = threadIdx.x; c < g.c; c += 1024) {
       const float d = to_f<DT>(xr[c]) - mean;
       q = __builtin_fmaf(d, d, q);
+      if constexpr (DT == CNHWC_F32) left += d;
     }
-    const float rstd = 1.0f / __builtin_sqrtf(row_sum<1024>(q, red, 1) * g.inv_c + g.eps);
+    if constexpr (DT == CNHWC_F32) row_sums<1024>(left, q, red, 1);
+    else q = row_sum<1024>(q, red[1], 0);
+    const float rstd = 1.0f / __builtin_sqrtf(put_right<DT>(left, q, mean, g) + g.eps);
     Elem<DT>* yr = y + row * g.c;
     for (int64_t c = threadIdx.x; c < g.c; c += 1024) {
       float v = (to_f<DT>(xr[c]) - mean) * rstd;

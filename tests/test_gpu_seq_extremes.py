@@ -129,3 +129,32 @@ def test_scan_rates_without_end(s, dt):
     want, mag = R.scan_backward(*args), R.scan_backward(*args, absolute=True)
     for name in ("u", "delta", "a", "b", "c", "state"):
         R.check(getattr(grads, name), want[name], mag[name], 32 * l + 128 + (n * l if name == "a" else 0), "d" + name)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_norm_of_constant_rows(dt):
+    """A constant row has that constant as its mean and no variance, whatever its
+    width: y is the bias, and rstd 1 / sqrt(eps).  In 16 bits the sums of these
+    rows are exact.  In 32 the sum's rounding, up to some 80 units of the mean's
+    last place, is exactly what is left of each element, and so is taken out;
+    what stays in the variance of it is 2^-16 of its square."""
+    eps = 1e-5
+    for c in [32, 33, 96, 100, 480, 513, 1000, 1056, 1999, 2048, 2560, 4097, 5000, 7168, 8192, 9001, 17000, 33000, 66000]:
+        v = torch.tensor([3000.0, 7.25, 3000.1, -0.1, 1e-3, 12345.678, 0.0])
+        x = v[:, None].expand(len(v), c).to(DT[dt]).cuda().contiguous()
+        g = np.random.default_rng([4, c])
+        w, b = (R.rand(g, c).to(DT[dt]).cuda() for _ in range(2))
+        y, mean, rstd = cn.layer_norm(x, w, b, eps, return_stats=True)
+        assert torch.equal(mean, x[:, 0].float()), c
+        assert torch.equal(y, b.expand(len(v), c)), c
+        left = 2.0 ** -16 * (80 * R.EPS * x[:, 0].double().cpu()) ** 2
+        assert ((R.f64(rstd) - eps ** -0.5).abs() <= eps ** -0.5 * (left / eps + 8 * R.EPS)).all(), c
+        assert torch.equal(cn.layer_norm(x, eps=eps), torch.zeros_like(x)), c
+
+
+def test_norm_mean_of_infinity():
+    """The mean of a row with an infinity is that infinity."""
+    x = torch.ones(2, 300, device="cuda")
+    x[0, 7], x[1, 9] = float("inf"), -float("inf")
+    _, mean, _ = cn.layer_norm(x, return_stats=True)
+    assert mean.tolist() == [float("inf"), -float("inf")]
