@@ -474,8 +474,19 @@ def direct_flops(x_shape, w_shape, plan):
     return 2 * x_shape[0] * plan.out_d * plan.out_h * plan.out_w * o * k
 
 
-from .sequence import (  # noqa: E402,F401  (uses the loaded library and the helpers above)
-    SEQ_EXPORTED, ConvGrads, ScanGrads, causal_conv1d, causal_conv1d_backward,
-    causal_conv1d_backward_workspace_bytes, causal_conv1d_step, layer_norm, layer_norm_backward,
-    layer_norm_backward_workspace_bytes, selective_scan, selective_scan_backward, selective_scan_step,
-    selective_scan_workspace_bytes)
+try:
+    from .sequence import (  # noqa: E402,F401  (uses the loaded library and the helpers above)
+        SEQ_EXPORTED, ConvGrads, ScanGrads, causal_conv1d, causal_conv1d_backward,
+        causal_conv1d_backward_workspace_bytes, causal_conv1d_step, layer_norm, layer_norm_backward,
+        layer_norm_backward_workspace_bytes, selective_scan, selective_scan_backward, selective_scan_step,
+        selective_scan_workspace_bytes)
+except ImportError as _e:
+    # The convolutions and the planner need libcnhwc.so alone; whoever asks for a
+    # sequence operator is told what is missing.
+    _no_sequence = str(_e)
+
+    def __getattr__(name):
+        if name in ("sequence", "SEQ_EXPORTED", "ConvGrads", "ScanGrads") or name.startswith(
+                ("layer_norm", "causal_conv1d", "selective_scan")):
+            raise ImportError(_no_sequence)
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
