@@ -18,10 +18,14 @@
 // workgroup through LDS, and leaves one row of partial sums per workgroup to a
 // second kernel, which adds them in a fixed order.
 //
-// Measured: 4 x 4096 x 4096 bf16 forward 52 us, 5.2 TB/s; backward 108 us,
-// 3.7 TB/s (a copy: 4.8 to 5.0); backward of five f16 sequences of 2047 x 2048
-// with 4260 valid positions 33 us, bound by the few wavefronts that the valid
-// positions give (1.1 a SIMD) and what each does one after the other.
+// Measured, bf16: 4 x 4096 x 4096 forward 59 us, 4.6 TB/s (52 us where the inputs
+// come back every third call and are partly in the cache); backward 114 us, 3.5
+// TB/s (a copy: 4.8 to 5.0), the vector pipes busy 71% of it.  Backward of five
+// f16 sequences of 2047 x 2048 with 4260 valid positions 33 us: the runs that
+// hold valid rows are 2.4 wavefronts a SIMD, each 28 rows one after the other
+// and three of its neighbour's; the pipes are busy 38%.  In both every row asks
+// whether it is valid, its own run's, a state's: the batch of four rows goes
+// through as several short pieces.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -346,11 +350,19 @@ int32_t pick_run(int64_t work, int64_t threads, int32_t most) {
 }
 // Measured forward: 4 x 4096 x 4096 bf16 with 512 threads 52 us, 2048 56, 4096 68.
 constexpr int64_t kFwdThreads = 512;
-// Backward, with two channels to a thread: 5 x 2047 x 2048 f16 of several
-// lengths with 768 threads 38 us, 1536 33, twice that 35; 2 x 2048 x 2048 f32
-// 30, 35, 38.  (Four f16 channels to a thread, in more registers: 35 us at best.)
+// Backward, with two channels to a thread.  What decides is how many of the
+// rows are there: batches with lengths leave runs without work, so they are
+// cut twice as fine.  Microseconds with 768 / 1536 threads: several sequences of
+// several lengths, 5 x 2047 x 2048 f16 38.7 / 32.9, f32 62.1 / 49.0, 6 x 8000 x
+// 512 f32 66.5 / 48.5, bf16 34.0 / 29.0 (against it: 8 x 2047 x 2048 f32 86 to 89 / 94);
+// without lengths 2 x 2048 x 2048 f16 24.2 / 27.5, f32 30.1 / 34.9, 3 x 1000 x
+// 2048 f32 23.5 / 29.0, bf16 18.2 / 22.2, 4 x 4096 x 4096 bf16 and f32 the same
+// (against it: 8 x 2047 x 2048 f32 142 / 112); one sequence with its length 1 x
+// 4000 x 2048 bf16 23.0 / 25.8, f32 38.1 / 36.2.  (Four f16 channels to a
+// thread, in more registers: the first case 35 at best.  Batches of eight rows: 51.
+// Occupancy bounds of 3 and 4 wavefronts: 90 and 195, registers spilled.)
 constexpr int kBwdChannels = 2;
-int64_t bwd_threads(int32_t dtype, int64_t ve) { return dtype != CNHWC_F32 && ve == kBwdChannels ? 1536 : 768; }
+int64_t bwd_threads(int64_t n, bool lengths) { return lengths && n > 1 ? 1536 : 768; }
 
 template <int N>
 using Int = std::integral_constant<int, N>;
@@ -400,10 +412,10 @@ hipError_t conv_step_t(const cnhwc_causal_conv_desc_t& d, const void* x, const v
   return hipGetLastError();
 }
 
-// Run length and workgroups per sequence of the backward pass, from the shape only.
-void bwd_runs(const cnhwc_causal_conv_desc_t& d, int64_t ve, int32_t* run, int64_t* blocks) {
+// Run length and workgroups per sequence of the backward pass.
+void bwd_runs(const cnhwc_causal_conv_desc_t& d, int64_t ve, bool lengths, int32_t* run, int64_t* blocks) {
   const int64_t rows = d.l + d.k - 1;
-  *run = pick_run(d.n * rows * ceil_div(d.c, ve), bwd_threads(d.dtype, ve), 64);
+  *run = pick_run(d.n * rows * ceil_div(d.c, ve), bwd_threads(d.n, lengths), 64);
   *blocks = ceil_div(rows, int64_t(*run) * kRunsPerBlock);
 }
 
@@ -418,7 +430,7 @@ hipError_t conv_bwd_t(const cnhwc_causal_conv_desc_t& d, const void* dy, const v
                       void* db, void* dstate, float* part, hipStream_t st) {
   using E = Elem<DT>;
   ConvGeo g = geo_of(d, V);
-  bwd_runs(d, V, &g.run, &g.runs);
+  bwd_runs(d, V, lengths != nullptr, &g.run, &g.runs);
   const int64_t cols = ceil_div(g.vecs, kLanes), parts = d.n * g.runs;
   for (int64_t first = 0; first < cols * parts; first += kMostBlocks) {
     const int64_t blocks = cols * parts - first < kMostBlocks ? cols * parts - first : kMostBlocks;
@@ -502,15 +514,17 @@ extern "C" cnhwc_status_t cnhwc_causal_conv_bwd_workspace(const cnhwc_causal_con
   const cnhwc_status_t st = check_desc(desc, true);
   if (st != CNHWC_OK) return st;
   if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
-  // the vector and the element form alike: which one runs also depends on the pointers
+  // the vector and the element form alike, with and without lengths: which one
+  // runs depends on the pointers
   uint64_t most = 0;
-  for (int64_t ve : {int64_t(1), int64_t(kBwdChannels)}) {
-    int32_t run;
-    int64_t blocks;
-    bwd_runs(*desc, ve, &run, &blocks);
-    const uint64_t b = uint64_t(desc->n) * blocks * (uint64_t(desc->c) * (desc->k + 1)) * 4;
-    most = b > most ? b : most;
-  }
+  for (int64_t ve : {int64_t(1), int64_t(kBwdChannels)})
+    for (bool lengths : {false, true}) {
+      int32_t run;
+      int64_t blocks;
+      bwd_runs(*desc, ve, lengths, &run, &blocks);
+      const uint64_t b = uint64_t(desc->n) * blocks * (uint64_t(desc->c) * (desc->k + 1)) * 4;
+      most = b > most ? b : most;
+    }
   *bytes = most;
   return CNHWC_OK;
 }

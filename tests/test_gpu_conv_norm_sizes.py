@@ -3,8 +3,8 @@ run, against 64-bit references on the GPU.
 
 The convolution gives a thread more than four positions from 655360 vectors on
 (of 16 bytes, or single elements; 32 positions at most), its gradient from
-983040 pairs or single elements, 1966080 16-bit pairs (64 rows at most).  Layer
-norm goes round its row loop again beyond 8192 workgroups.  Bounds as for the small sizes.
+983040 pairs or single elements, 1966080 in batches with lengths (64 rows at
+most).  Layer norm goes round its row loop again beyond 8192 workgroups.  Bounds as for the small sizes.
 """
 import pytest
 import torch
@@ -48,7 +48,8 @@ def test_conv_forward(dt, n, l, c, k, lengths, wide):
     assert torch.equal(last.double(), rl)
 
 
-GRAD = [  # runs of 8 to 64 rows; pairs, strided pairs and single elements
+GRAD = [  # runs of 4 to 64 rows; pairs, strided pairs and single elements
+    ("f32", 3, 4200, 512, 4, [4200, 0, 4197], False), ("f16", 2, 4203, 512, 4, [17, 4201], True),
     ("f32", 3, 4200, 256, 4, [4200, 0, 4197], False), ("f32", 2, 7001, 384, 3, None, True),
     ("f16", 3, 4011, 300, 7, [4011, 2, 4001], False), ("bf16", 4, 8300, 1024, 4, None, True),
     ("bf16", 6, 8300, 1024, 4, [8300, 8299, 64, 65, 1, 7777], False), ("f32", 3, 8204, 511, 4, [8200, 127, 8204], False),
