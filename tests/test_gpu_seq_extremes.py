@@ -73,6 +73,28 @@ def test_scan_gates_of_large_values(s, dt):
 
 
 @pytest.mark.parametrize("dt", list(DT))
+def test_nan_passes_silu(dt):
+    """A gate or a pre-activation that is no number leaves none, in its own place alone."""
+    i = _gated(dt, 8)
+    gate = torch.ones_like(i["gate"])
+    gate[0, 5, 3] = float("nan")
+    args = (i["u"], i["delta"], i["a"], i["b"], i["c"])
+    y = cn.selective_scan(*args, gate=gate, softplus=True)
+    hit = torch.isnan(gate)
+    assert torch.equal(torch.isnan(y), hit)
+    r = cn.selective_scan_backward(i["dy"], *args, gate=gate, softplus=True)
+    assert torch.equal(torch.isnan(r.gate), hit)
+    assert torch.isnan(r.c[0, 5]).all() and not torch.isnan(r.c[0, 4]).any() and torch.isnan(r.u[0, 5, 3])
+    x = torch.ones(2, 9, 16, dtype=DT[dt], device="cuda")
+    x[1, 4, 6] = float("nan")
+    w = torch.ones(16, 2, dtype=DT[dt], device="cuda")
+    y = cn.causal_conv1d(x, w, activation="silu")
+    assert torch.equal(torch.isnan(y).nonzero(), torch.tensor([[1, 4, 6], [1, 5, 6]], device="cuda"))
+    r = cn.causal_conv1d_backward(torch.ones_like(x), x, w, activation="silu")
+    assert torch.isnan(r.x[1, 3:6, 6]).all() and int(torch.isnan(r.x).sum()) == 3 and int(torch.isnan(r.w).sum()) == 2
+
+
+@pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("s", [8, 16])
 def test_scan_gradient_of_large_gates(s, dt):
     """Through a closed gate nothing comes back, whatever the gradient in front of
