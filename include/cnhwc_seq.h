@@ -113,7 +113,10 @@ cnhwc_status_t cnhwc_causal_conv_step(const cnhwc_causal_conv_desc_t* desc, cons
  *   D[t,d] = softplus(delta[t,d] + delta_bias[d])     (softplus == 0: the sum)
  *   h[t,d,s] = exp(D[t,d] a[d,s]) h[t-1,d,s] + D[t,d] u[t,d] b[t,s]
  *   y[t,d] = (sum_s c[t,s] h[t,d,s] + skip[d] u[t,d]) * silu(gate[t,d])
- * b and c are shared by all channels.  The state h is fp32 [N,D,S]. */
+ * b and c are shared by all channels.  The state h is fp32 [N,D,S].  The decays of
+ * up to a chunk of positions are joined in one exponential of the sum of D a, which
+ * does not overflow where D a <= 0; states that grow by e^88 and more do not fit
+ * fp32, and may come out as NaN. */
 #define CNHWC_SCAN_MAX_STATE 64
 
 typedef struct {
