@@ -20,10 +20,10 @@
 //
 // Measured, bf16: 4 x 4096 x 4096 forward 59 us, 4.6 TB/s (52 us where the inputs
 // come back every third call and are partly in the cache); backward 114 us, 3.5
-// TB/s (a copy: 4.8 to 5.0), the vector pipes busy 71% of it.  Backward of five
+// TB/s (a copy: 4.8 to 5.0), the vector pipes busy 70% of it.  Backward of five
 // f16 sequences of 2047 x 2048 with 4260 valid positions 33 us: the runs that
 // hold valid rows are 2.4 wavefronts a SIMD, each 28 rows one after the other
-// and three of its neighbour's; the pipes are busy 38%.  In both every row asks
+// and three of its neighbour's; the pipes are busy 37%.  In both every row asks
 // whether it is valid, its own run's, a state's: the batch of four rows goes
 // through as several short pieces.
 #include <hip/hip_runtime.h>

@@ -14,7 +14,7 @@
 // row of partial sums, and a second kernel adds those rows in a fixed order.
 //
 // Both are bound by memory: 32768 x 4096 bf16 forward 99 us, 5.4 TB/s; backward
-// of 65536 x 2048 bf16 164 us, 4.9 TB/s, of 16384 x 2048 55 us, 3.7 TB/s (52 where the
+// of 65536 x 2048 bf16 157 us, 5.1 TB/s, of 16384 x 2048 55 us, 3.7 TB/s (52 where the
 // inputs come back every third call; a copy reaches 4.8 to 5.0 TB/s on this card).
 // A row is held by TPR threads, NV vectors each: few threads for narrow rows
 // (several rows to a wavefront), one wavefront up to 64 * NV vectors, a workgroup

@@ -25,8 +25,8 @@
 //
 // Measured, 1 x 16384 x 2048 channels x 16 states, bf16: 279 us (7982 us in one
 // chunk), of them 111 the local chunks, 13 the join, 155 the outputs (each of
-// them launched by itself, again and again).  The vector pipes are busy 82 and
-// 84% of the kernels' cycles; the bytes that have to move (270 MB) would take 56 us.
+// them launched by itself, again and again).  The vector pipes are busy 81 and
+// 83% of the kernels' cycles; the bytes that have to move (270 MB) would take 56 us.
 // Positions past a sequence's length go through all of it: 6 sequences of 1023
 // x 1000 x 16 fp32 of which 2449 of 6138 positions are valid take 72 us (24, 8, 39).
 #include <hip/hip_runtime.h>
@@ -547,8 +547,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanIn<DT> in, ScanGeo g
 // Measured, 8 x 2048 x 2048 channels x 16 states, bf16: 700 us, of them 179 the
 // chunk kernel, 14 the join, 489 the gradient (each launched by itself, again
 // and again), the rest the two sums.  The gradient
-// kernel issues 394 vector instructions per position and wavefront (16 elements
-// a lane) and keeps the vector pipes busy 73% of its cycles, with two wavefronts
+// kernel issues 384 vector instructions per position and wavefront (16 elements
+// a lane) and keeps the vector pipes busy 74% of its cycles, with two wavefronts
 // to a SIMD (registers); the bytes that have to move (472 MB) would take 98 us.
 
 template <int DT>
