@@ -205,7 +205,8 @@ def selective_scan(u, delta, a, b, c, *, skip=None, gate=None, delta_bias=None, 
 
     u, delta, gate, y [N,L,D] and b, c [N,L,S] in one dtype; a [D,S], skip,
     delta_bias [D] and the states [N,D,S] in float32; S <= 64.  Absent skip,
-    delta_bias and state count as 0, an absent gate leaves its factor out.
+    delta_bias and state count as 0, an absent gate leaves its factor out.  States
+    that grow (D a > 0) by e^88 within a chunk of positions do not fit float32.
     With return_state: (y, the state after the last valid position)."""
     return _seq.selective_scan(u, delta, a, b, c, skip, gate, delta_bias, softplus, state, lengths, return_state, out,
                                workspace)
