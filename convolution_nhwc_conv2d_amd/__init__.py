@@ -9,8 +9,9 @@ this import fails, and every library error raises :class:`CnhwcError`.
     conv3d(x, w, stride, padding, dilation, *, algo, inner_algo, ws_limit, ...)
     plan2d(...) / plan3d(...) -> Plan      (algorithm selection only; no GPU needed)
 
-The sequence operators (layer norm, the short causal convolution, the selective
-state space scan, forward and backward) are in ``sequence.py`` and re-exported here.
+The sequence operators (layer norm, root-mean-square norm, the short causal
+convolution, the selective state space scan, rotary positions and linear
+attention, forward and backward) are in ``sequence.py`` and re-exported here.
 
 Layouts: x [N,H,W,C] / [N,D,H,W,C]; w [O,KH,KW,C] / [O,KD,KH,KW,C];
 y [N,OH,OW,O] / [N,OD,OH,OW,O]; dtype float32, float16 or bfloat16 (x, w, y
@@ -476,17 +477,19 @@ def direct_flops(x_shape, w_shape, plan):
 
 try:
     from .sequence import (  # noqa: E402,F401  (uses the loaded library and the helpers above)
-        SEQ_EXPORTED, ConvGrads, ScanGrads, causal_conv1d, causal_conv1d_backward,
+        SEQ_EXPORTED, ConvGrads, LinearAttentionGrads, ScanGrads, causal_conv1d, causal_conv1d_backward,
         causal_conv1d_backward_workspace_bytes, causal_conv1d_step, layer_norm, layer_norm_backward,
-        layer_norm_backward_workspace_bytes, selective_scan, selective_scan_backward, selective_scan_step,
-        selective_scan_workspace_bytes)
+        layer_norm_backward_workspace_bytes, linear_attention, linear_attention_backward, linear_attention_step,
+        linear_attention_workspace_bytes, rms_norm, rms_norm_backward, rms_norm_backward_workspace_bytes,
+        rms_norm_quantized, rotary, rotary_backward, rotary_frequencies, selective_scan, selective_scan_backward,
+        selective_scan_step, selective_scan_workspace_bytes)
 except ImportError as _e:
     # The convolutions and the planner need libcnhwc.so alone; whoever asks for a
     # sequence operator is told what is missing.
     _no_sequence = str(_e)
 
     def __getattr__(name):
-        if name in ("sequence", "SEQ_EXPORTED", "ConvGrads", "ScanGrads") or name.startswith(
-                ("layer_norm", "causal_conv1d", "selective_scan")):
+        if name in ("sequence", "SEQ_EXPORTED", "ConvGrads", "LinearAttentionGrads", "ScanGrads") or name.startswith(
+                ("layer_norm", "causal_conv1d", "selective_scan", "rms_norm", "rotary", "linear_attention")):
             raise ImportError(_no_sequence)
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

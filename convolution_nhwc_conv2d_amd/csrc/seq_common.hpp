@@ -1,6 +1,5 @@
-// Device helpers shared by the sequence kernels (layer norm, causal
-// convolution, selective scan): element types, vector loads and stores, sums
-// across lanes, and the scalar functions.
+// Device helpers shared by the sequence kernels: element types, vector loads and
+// stores, sums across lanes, and the scalar functions.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <cstdint>
@@ -129,6 +128,29 @@ __device__ __forceinline__ float group_sum(float v) {
   if constexpr (G >= 16) v += dpp<kRowMirror>(v);
   if constexpr (G >= 32) v = add_row_pairs(v);
   if constexpr (G >= 64) v = add_halves(v);
+  return v;
+}
+
+__device__ __forceinline__ float max_row_pairs(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __builtin_fmaxf(__builtin_bit_cast(float, uint32_t(r[0])), __builtin_bit_cast(float, uint32_t(r[1])));
+}
+__device__ __forceinline__ float max_halves(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_fmaxf(__builtin_bit_cast(float, uint32_t(r[0])), __builtin_bit_cast(float, uint32_t(r[1])));
+}
+
+// The largest over groups of G consecutive lanes, in each of them; NaN is passed over.
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  if constexpr (G >= 2) v = __builtin_fmaxf(v, dpp<kQuadXor1>(v));
+  if constexpr (G >= 4) v = __builtin_fmaxf(v, dpp<kQuadXor2>(v));
+  if constexpr (G >= 8) v = __builtin_fmaxf(v, dpp<kHalfMirror>(v));
+  if constexpr (G >= 16) v = __builtin_fmaxf(v, dpp<kRowMirror>(v));
+  if constexpr (G >= 32) v = max_row_pairs(v);
+  if constexpr (G >= 64) v = max_halves(v);
   return v;
 }
 

@@ -16,6 +16,8 @@
 #include <optional>
 #include <string>
 #include <tuple>
+#include <utility>
+#include <vector>
 
 #include "cnhwc_seq.h"
 
@@ -398,6 +400,251 @@ Tensor selective_scan_step(const Tensor& u, const Tensor& delta, const Tensor& a
   return y;
 }
 
+// ---------------------------------------------------------------- root-mean-square norm
+
+cnhwc_rms_norm_desc_t rms_desc(const Tensor& x, const Rows& r, const Opt& more, const char* name, at::ScalarType wd,
+                               double eps, int32_t group) {
+  const int32_t code = dtype_code(x, "x");
+  cnhwc_rms_norm_desc_t d{code, wd == at::kFloat ? int32_t(CNHWC_F32) : code, r.n, r.l, r.c,
+                          {r.stride[0], r.stride[1]}, {0, 0}, {0, 0}, float(eps), group};
+  if (more) {
+    const Rows m = rows_of(like(*more, name, x, x.scalar_type(), x.sizes(), false), name);
+    d.residual_stride[0] = m.stride[0];
+    d.residual_stride[1] = m.stride[1];
+  }
+  return d;
+}
+
+// What the two forms of the norm have besides y: the sum with a residual, rstd where wanted.
+std::pair<Opt, Opt> rms_outputs(const Tensor& x, const Opt& residual, const Opt& sum_out, bool stats) {
+  if (sum_out && !residual) throw py::value_error("sum_out needs residual");
+  like(sum_out, "sum_out", x, x.scalar_type(), x.sizes());
+  Opt sum = sum_out, rstd;
+  if (residual && !sum) sum = dense_like(x);
+  if (stats) rstd = at::empty(x.sizes().slice(0, x.dim() - 1), x.options().dtype(at::kFloat));
+  return {sum, rstd};
+}
+
+py::object some(std::initializer_list<const Opt*> all) {
+  py::list l;
+  for (const Opt* t : all)
+    if (*t) l.append(py::cast(**t));
+  return l.size() == 1 ? py::object(l[0]) : py::object(py::tuple(l));
+}
+
+py::object rms_norm(const Tensor& x, const Opt& weight, double eps, const Opt& residual, bool stats, const Opt& out,
+                    const Opt& sum_out) {
+  dtype_code(x, "x");
+  const Rows r = rows_of(x, "x");
+  const at::ScalarType wd = norm_params(weight, Opt(), x);
+  const cnhwc_rms_norm_desc_t d = rms_desc(x, r, residual, "residual", wd, eps, 0);
+  const Opt y = output(out, x);
+  const auto [sum, rstd] = rms_outputs(x, residual, sum_out, stats);
+  if (x.numel() > 0)
+    launch(x, "cnhwc_rms_norm_fwd", [&, sum = sum, rstd = rstd](void* s) {
+      return cnhwc_rms_norm_fwd(&d, ptr(x), ptr(residual), ptr(weight), ptr(y), ptr(sum), ptr<float>(rstd), s);
+    });
+  return some({&y, &sum, &rstd});
+}
+
+py::object rms_norm_quantized(const Tensor& x, const Opt& weight, double eps, std::optional<int64_t> group,
+                              const Opt& residual, bool stats, const Opt& out, const Opt& scale_out,
+                              const Opt& sum_out) {
+  dtype_code(x, "x");
+  const Rows r = rows_of(x, "x");
+  const at::ScalarType wd = norm_params(weight, Opt(), x);
+  if (group && (*group < 1 || *group > INT32_MAX || r.c % *group != 0))
+    throw py::value_error("group must divide x's channels");
+  const cnhwc_rms_norm_desc_t d = rms_desc(x, r, residual, "residual", wd, eps, group ? int32_t(*group) : 0);
+  std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end() - 1);
+  if (group) shape.push_back(r.c / *group);
+  like(out, "out", x, at::kFloat8_e4m3fn, x.sizes());
+  like(scale_out, "scale_out", x, at::kFloat, shape);
+  const Opt q = out ? out : Opt(at::empty(x.sizes(), x.options().dtype(at::kFloat8_e4m3fn)));
+  const Opt scale = scale_out ? scale_out : Opt(at::empty(shape, x.options().dtype(at::kFloat)));
+  const auto [sum, rstd] = rms_outputs(x, residual, sum_out, stats);
+  if (x.numel() > 0)
+    launch(x, "cnhwc_rms_norm_fwd_q8", [&, sum = sum, rstd = rstd](void* s) {
+      return cnhwc_rms_norm_fwd_q8(&d, ptr(x), ptr(residual), ptr(weight), ptr(q), ptr<float>(scale), ptr(sum),
+                                   ptr<float>(rstd), s);
+    });
+  return some({&q, &scale, &sum, &rstd});
+}
+
+std::tuple<Tensor, Opt> rms_norm_backward(const Tensor& dy, const Tensor& x, const Tensor& rstd, const Opt& weight,
+                                          const Opt& dsum, const Opt& given) {
+  dtype_code(x, "x");
+  const Rows r = rows_of(x, "x");
+  const Rows g = rows_of(like(dy, "dy", x, x.scalar_type(), x.sizes(), false), "dy");
+  like(rstd, "rstd", x, at::kFloat, x.sizes().slice(0, x.dim() - 1));
+  const at::ScalarType wd = norm_params(weight, Opt(), x);
+  cnhwc_rms_norm_desc_t d = rms_desc(x, r, dsum, "dsum", wd, 0.0, 0);
+  d.dy_stride[0] = g.stride[0];
+  d.dy_stride[1] = g.stride[1];
+  const Tensor dx = dense_like(x);
+  const Opt dw = dense_like(weight);
+  if (x.numel() == 0) {
+    if (dw) dw->zero_();
+    return {dx, dw};
+  }
+  uint64_t need = 0;
+  raise_status(cnhwc_rms_norm_bwd_workspace(&d, dw.has_value(), &need), "cnhwc_rms_norm_bwd_workspace");
+  const Tensor ws = workspace(given, need, x);
+  launch(x, "cnhwc_rms_norm_bwd", [&](void* s) {
+    return cnhwc_rms_norm_bwd(&d, ptr(dy), ptr(dsum), ptr(x), ptr<float>(rstd), ptr(weight), ptr(dx), ptr(dw),
+                              ptr(ws), bytes_of(ws), s);
+  });
+  return {dx, dw};
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+Tensor rotary(const Tensor& x, const Tensor& freqs, const Opt& positions, int64_t offset, bool interleaved,
+              double scale, bool inverse, const Opt& out) {
+  cnhwc_rotary_desc_t d{};
+  d.dtype = dtype_code(x, "x");
+  const bool token = x.dim() == 3;
+  if (!token && x.dim() != 4) throw py::value_error("x must be [N,L,H,D], or [N,H,D] for a token of each sequence");
+  const int64_t n = x.size(0), l = token ? 1 : x.size(1), wide = x.size(-1);
+  like(x, "x", x, x.scalar_type(), x.sizes(), false);
+  if (freqs.dim() != 1 || freqs.size(0) * 2 > wide) throw py::value_error("freqs must be [R/2] with R <= D");
+  like(freqs, "freqs", x, at::kDouble, freqs.sizes());
+  if (wide > INT32_MAX) throw py::value_error("D must be below 2^31");
+  if (positions) {
+    if (token) {
+      like(positions, "positions", x, at::kInt, {n}, false);
+      d.position_stride[0] = positions->stride(0);
+    } else {
+      like(positions, "positions", x, at::kInt, positions->dim() == 1 ? at::IntArrayRef{l} : at::IntArrayRef{n, l},
+           false);
+      d.position_stride[0] = positions->dim() == 1 ? 0 : positions->stride(0);
+      d.position_stride[1] = positions->stride(-1);
+    }
+  }
+  if (out) like(*out, "out", x, x.scalar_type(), x.sizes(), false);
+  const Tensor y = out ? *out : dense_like(x);
+  d.interleaved = interleaved;
+  d.inverse = inverse;
+  d.n = n, d.l = l, d.h = x.size(-2);
+  d.d = int32_t(wide), d.r = int32_t(freqs.size(0) * 2);
+  auto strides = [&](const Tensor& t, int64_t (&to)[3]) {
+    to[0] = t.stride(0);
+    to[1] = token ? 0 : t.stride(1);
+    to[2] = t.stride(-2);
+  };
+  strides(x, d.x_stride);
+  strides(y, d.out_stride);
+  d.offset = offset;
+  d.scale = float(scale);
+  if (x.numel() > 0)
+    launch(x, "cnhwc_rotary", [&](void* s) {
+      return cnhwc_rotary(&d, ptr(x), d.r ? ptr<double>(freqs) : nullptr, ptr<int32_t>(positions), ptr(y), s);
+    });
+  return y;
+}
+
+// ---------------------------------------------------------------- linear attention
+
+struct Attention {
+  cnhwc_linear_attention_desc_t d{};
+  cnhwc_linear_attention_inputs_t in{};
+};
+
+Attention attention_check(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& log_decay, double scale,
+                          const Opt& state, const Opt& lengths, int64_t dims) {
+  Attention r;
+  cnhwc_linear_attention_desc_t& d = r.d;
+  d.dtype = dtype_code(q, "q");
+  if (q.dim() != dims) throw py::value_error(dims == 4 ? "q must be [N,L,H,DK]" : "q must be [N,H,DK]");
+  if (v.dim() != dims) throw py::value_error(dims == 4 ? "v must be [N,L,H,DV]" : "v must be [N,H,DV]");
+  const at::ScalarType dt = q.scalar_type();
+  std::vector<int64_t> wide(q.sizes().begin(), q.sizes().end());
+  const int64_t n = wide[0], l = dims == 4 ? wide[1] : 1, h = q.size(-2), dk = q.size(-1), dv = v.size(-1);
+  wide.back() = dv;
+  if (dk < 1 || dv < 1) throw py::value_error("q, k and v need channels");
+  like(q, "q", q, dt, q.sizes(), false);
+  like(k, "k", q, dt, q.sizes(), false);
+  like(v, "v", q, dt, wide, false);
+  like(log_decay, "log_decay", q, at::kFloat, {h});
+  like(state, "state", q, at::kFloat, {n, h, dk, dv});
+  like(lengths, "lengths", q, at::kInt, {n});
+  d.n = n, d.l = l, d.h = h;
+  d.dk = int32_t(dk < INT32_MAX ? dk : INT32_MAX);
+  d.dv = int32_t(dv < INT32_MAX ? dv : INT32_MAX);
+  d.scale = float(scale);
+  auto strides = [&](const Tensor& t, int64_t (&to)[3]) {
+    to[0] = t.stride(0);
+    to[1] = dims == 4 ? t.stride(1) : 0;
+    to[2] = t.stride(-2);
+  };
+  strides(q, d.q_stride);
+  strides(k, d.k_stride);
+  strides(v, d.v_stride);
+  r.in = {ptr(q), ptr(k), ptr(v), ptr<float>(log_decay), ptr<float>(state), ptr<int32_t>(lengths)};
+  return r;
+}
+
+py::object linear_attention(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& log_decay, double scale,
+                            const Opt& state, const Opt& lengths, bool return_state, const Opt& out,
+                            const Opt& given) {
+  const Attention r = attention_check(q, k, v, log_decay, scale, state, lengths, 4);
+  const Tensor y = output(out, v);
+  Opt last;
+  if (return_state) last = at::empty({r.d.n, r.d.h, int64_t(r.d.dk), int64_t(r.d.dv)}, log_decay.options());
+  if (v.numel() > 0) {
+    uint64_t need = 0;
+    raise_status(cnhwc_linear_attention_fwd_workspace(&r.d, &need), "cnhwc_linear_attention_fwd_workspace");
+    const Tensor ws = workspace(given, need, q);
+    launch(q, "cnhwc_linear_attention_fwd", [&](void* s) {
+      return cnhwc_linear_attention_fwd(&r.d, &r.in, ptr(y), ptr<float>(last), ptr(ws), bytes_of(ws), s);
+    });
+  } else if (last) {
+    if (state) last->copy_(*state);
+    else last->zero_();
+  }
+  return last ? py::cast(std::make_tuple(y, *last)) : py::cast(y);
+}
+
+std::tuple<Tensor, Tensor, Tensor, Opt, Opt> linear_attention_backward(
+    const Tensor& dy, const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& log_decay, double scale,
+    const Opt& state, const Opt& lengths, const Opt& dlast, bool decay_grad, const Opt& given) {
+  Attention r = attention_check(q, k, v, log_decay, scale, state, lengths, 4);
+  like(dy, "dy", q, q.scalar_type(), v.sizes(), false);
+  like(dlast, "dstate", q, at::kFloat, {r.d.n, r.d.h, int64_t(r.d.dk), int64_t(r.d.dv)});
+  r.d.dy_stride[0] = dy.stride(0);
+  r.d.dy_stride[1] = dy.stride(1);
+  r.d.dy_stride[2] = dy.stride(2);
+  const Tensor dq = dense_like(q), dk = dense_like(k), dv = dense_like(v);
+  const Opt dg = decay_grad ? Opt(dense_like(log_decay)) : Opt(), ds = dense_like(state);
+  if (v.numel() == 0) {
+    if (dg) dg->zero_();
+    if (ds) dlast ? ds->copy_(*dlast) : ds->zero_();
+    return {dq, dk, dv, dg, ds};
+  }
+  uint64_t need = 0;
+  raise_status(cnhwc_linear_attention_bwd_workspace(&r.d, decay_grad, &need), "cnhwc_linear_attention_bwd_workspace");
+  const Tensor ws = workspace(given, need, q);
+  const cnhwc_linear_attention_grads_t g{ptr(dq), ptr(dk), ptr(dv), ptr<float>(dg), ptr<float>(ds)};
+  launch(q, "cnhwc_linear_attention_bwd", [&](void* s) {
+    return cnhwc_linear_attention_bwd(&r.d, &r.in, ptr(dy), ptr<float>(dlast), &g, ptr(ws), bytes_of(ws), s);
+  });
+  return {dq, dk, dv, dg, ds};
+}
+
+Tensor linear_attention_step(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& log_decay,
+                             const Opt& state, double scale, const Opt& state_out, const Opt& out) {
+  const Attention r = attention_check(q, k, v, log_decay, scale, state, Opt(), 3);
+  if (!state) throw py::value_error("state is required");
+  like(state_out, "state_out", q, at::kFloat, state->sizes());
+  const Tensor y = output(out, v);
+  if (v.numel() > 0)
+    launch(q, "cnhwc_linear_attention_step", [&](void* s) {
+      return cnhwc_linear_attention_step(&r.d, &r.in, ptr(y), state_out ? ptr<float>(state_out) : ptr<float>(state),
+                                         s);
+    });
+  return y;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_seq, m) {
@@ -411,4 +658,11 @@ PYBIND11_MODULE(_seq, m) {
   m.def("selective_scan", torch::wrap_pybind_function(selective_scan));
   m.def("selective_scan_backward", torch::wrap_pybind_function(selective_scan_backward));
   m.def("selective_scan_step", torch::wrap_pybind_function(selective_scan_step));
+  m.def("rms_norm", torch::wrap_pybind_function(rms_norm));
+  m.def("rms_norm_quantized", torch::wrap_pybind_function(rms_norm_quantized));
+  m.def("rms_norm_backward", torch::wrap_pybind_function(rms_norm_backward));
+  m.def("rotary", torch::wrap_pybind_function(rotary));
+  m.def("linear_attention", torch::wrap_pybind_function(linear_attention));
+  m.def("linear_attention_backward", torch::wrap_pybind_function(linear_attention_backward));
+  m.def("linear_attention_step", torch::wrap_pybind_function(linear_attention_step));
 }

@@ -1,14 +1,21 @@
-"""Sequence operators: layer norm, the short causal convolution and the
-selective state space scan -- the binding of ``include/cnhwc_seq.h``.
+"""Sequence operators: layer norm, the short causal convolution, the selective
+state space scan, root-mean-square norm, rotary positions and linear attention
+-- the binding of ``include/cnhwc_seq.h``.
 
     layer_norm(x, weight, bias, eps)            layer_norm_backward(dy, x, mean, rstd, weight)
+    rms_norm(x, weight, eps, residual=...)      rms_norm_backward(dy, x, rstd, weight)
+    rms_norm_quantized(x, weight, eps, ...)
+    rotary_frequencies(dim, base)
+    rotary(x, freqs)                            rotary_backward(dy, freqs)
+    linear_attention(q, k, v, log_decay)        linear_attention_backward(dy, q, k, v, log_decay)
+                                                linear_attention_step(q, k, v, log_decay, state)
     causal_conv1d(x, w, bias)                   causal_conv1d_backward(dy, x, w, bias)
                                                 causal_conv1d_step(x, state, w, bias)
     selective_scan(u, delta, a, b, c)           selective_scan_backward(dy, u, delta, a, b, c)
                                                 selective_scan_step(u, delta, a, b, c, state)
 
-Layouts: sequences are channels-last [N, L, C] as for conv1d; a single token is
-[N, C].  Inputs need a channel stride of 1 and may otherwise be strided, so the
+Layouts: sequences are channels-last [N, L, C] as for conv1d, with heads [N, L, H, D];
+a single token is [N, C] or [N, H, D].  Inputs need a channel stride of 1 and may otherwise be strided, so the
 parts of a projection's rows (``xz[..., :c]``) go in without a copy; parameters,
 states, outputs and gradients are dense.  Activations are float32, float16 or
 bfloat16; statistics, states and sums are held in float32.
@@ -29,6 +36,7 @@ Python.
 """
 import collections
 import ctypes
+import math
 
 import torch  # noqa: F401  (before the extension, which uses its libraries)
 
@@ -47,6 +55,7 @@ _P = ctypes.POINTER
 
 CAUSAL_CONV_MAX_K = 8
 SCAN_MAX_STATE = 64
+LINEAR_ATTENTION_MAX_DIM = 256
 
 ACTIVATIONS = {None: 0, "silu": 1}
 
@@ -75,6 +84,31 @@ class ScanGradPointers(ctypes.Structure):
     _fields_ = [(f, _vp) for f in ("u", "delta", "a", "b", "c", "skip", "gate", "delta_bias", "state")]
 
 
+class RmsNormDesc(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("w_dtype", _i32), ("n", _i64), ("l", _i64), ("c", _i64), ("x_stride", _i64 * 2),
+                ("residual_stride", _i64 * 2), ("dy_stride", _i64 * 2), ("eps", _f32), ("group", _i32)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("interleaved", _i32), ("n", _i64), ("l", _i64), ("h", _i64), ("d", _i32),
+                ("r", _i32), ("x_stride", _i64 * 3), ("out_stride", _i64 * 3), ("position_stride", _i64 * 2),
+                ("offset", _i64), ("scale", _f32), ("inverse", _i32), ("reserved", _i64)]
+
+
+class LinearAttentionDesc(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("reserved", _i32), ("n", _i64), ("l", _i64), ("h", _i64), ("dk", _i32), ("dv", _i32),
+                ("q_stride", _i64 * 3), ("k_stride", _i64 * 3), ("v_stride", _i64 * 3), ("dy_stride", _i64 * 3),
+                ("scale", _f32), ("reserved2", _i32)]
+
+
+class LinearAttentionInputs(ctypes.Structure):
+    _fields_ = [(f, _vp) for f in ("q", "k", "v", "log_decay", "state", "lengths")]
+
+
+class LinearAttentionGradPointers(ctypes.Structure):
+    _fields_ = [(f, _vp) for f in ("q", "k", "v", "log_decay", "state")]
+
+
 SEQ_EXPORTED = {
     "cnhwc_layer_norm_fwd": [_P(LayerNormDesc)] + [_vp] * 7,
     "cnhwc_layer_norm_bwd_workspace": [_P(LayerNormDesc), _i32, _P(_u64)],
@@ -88,6 +122,17 @@ SEQ_EXPORTED = {
     "cnhwc_scan_bwd_workspace": [_P(ScanDesc), _P(_u64)],
     "cnhwc_scan_bwd": [_P(ScanDesc), _P(ScanInputs), _vp, _vp, _P(ScanGradPointers), _vp, _u64, _vp],
     "cnhwc_scan_step": [_P(ScanDesc), _P(ScanInputs), _vp, _vp, _vp],
+    "cnhwc_rms_norm_fwd": [_P(RmsNormDesc)] + [_vp] * 7,
+    "cnhwc_rms_norm_fwd_q8": [_P(RmsNormDesc)] + [_vp] * 8,
+    "cnhwc_rms_norm_bwd_workspace": [_P(RmsNormDesc), _i32, _P(_u64)],
+    "cnhwc_rms_norm_bwd": [_P(RmsNormDesc)] + [_vp] * 8 + [_u64, _vp],
+    "cnhwc_rotary": [_P(RotaryDesc)] + [_vp] * 5,
+    "cnhwc_linear_attention_fwd_workspace": [_P(LinearAttentionDesc), _P(_u64)],
+    "cnhwc_linear_attention_fwd": [_P(LinearAttentionDesc), _P(LinearAttentionInputs), _vp, _vp, _vp, _u64, _vp],
+    "cnhwc_linear_attention_bwd_workspace": [_P(LinearAttentionDesc), _i32, _P(_u64)],
+    "cnhwc_linear_attention_bwd": [_P(LinearAttentionDesc), _P(LinearAttentionInputs), _vp, _vp,
+                                   _P(LinearAttentionGradPointers), _vp, _u64, _vp],
+    "cnhwc_linear_attention_step": [_P(LinearAttentionDesc), _P(LinearAttentionInputs), _vp, _vp, _vp],
 }
 for _name, _args in SEQ_EXPORTED.items():
     _fn = getattr(lib, _name)
@@ -95,6 +140,7 @@ for _name, _args in SEQ_EXPORTED.items():
 
 ConvGrads = collections.namedtuple("ConvGrads", "x w bias state")
 ScanGrads = collections.namedtuple("ScanGrads", "u delta a b c skip gate delta_bias state")
+LinearAttentionGrads = collections.namedtuple("LinearAttentionGrads", "q k v log_decay state")
 
 
 # ------------------------------------------------------------------ descriptors
@@ -116,6 +162,18 @@ def _scan_desc(dtype, softplus, n, l, d, s, us, ds, bs, cs, gs, ys):
     r.u_stride[:], r.delta_stride[:], r.b_stride[:], r.c_stride[:] = us, ds, bs, cs
     r.gate_stride[:], r.dy_stride[:] = gs, ys
     return r
+
+
+def _rms_desc(dtype, w_dtype, n, l, c, xs, rs, gs, eps, group):
+    d = RmsNormDesc(dtype=dtype, w_dtype=w_dtype, n=n, l=l, c=c, eps=eps, group=group)
+    d.x_stride[:], d.residual_stride[:], d.dy_stride[:] = xs, rs, gs
+    return d
+
+
+def _attention_desc(dtype, n, l, h, dk, dv, qs, ks, vs, gs, scale=1.0):
+    d = LinearAttentionDesc(dtype=dtype, n=n, l=l, h=h, dk=dk, dv=dv, scale=scale)
+    d.q_stride[:], d.k_stride[:], d.v_stride[:], d.dy_stride[:] = qs, ks, vs, gs
+    return d
 
 
 def _bytes(name, desc, *args):
@@ -238,3 +296,139 @@ def selective_scan_step(u, delta, a, b, c, state, *, skip=None, gate=None, delta
     """selective_scan of one new token per sequence: u, delta, gate, y [N,D], b, c
     [N,S].  The state [N,D,S] moves on by the token, in place or into state_out."""
     return _seq.selective_scan_step(u, delta, a, b, c, state, skip, gate, delta_bias, softplus, state_out, out)
+
+
+# ------------------------------------------------------------------ root-mean-square norm
+
+def rms_norm(x, weight=None, eps=1e-6, *, residual=None, return_stats=False, out=None, sum_out=None):
+    """y[..., C] = z * rstd * weight over the channels of each row, z = x + residual
+    and rstd = 1 / sqrt(mean z^2 + eps).  weight [C] has x's dtype or float32.
+
+    With residual: (y, z), z rounded to x's dtype and y taken from z before that;
+    sum_out, where z goes, may be residual itself (dense, updated in place).  With
+    return_stats rstd [...], float32, comes last: what rms_norm_backward takes."""
+    return _seq.rms_norm(x, weight, eps, residual, return_stats, out, sum_out)
+
+
+def rms_norm_quantized(x, weight=None, eps=1e-6, *, group=None, residual=None, return_stats=False, out=None,
+                       scale_out=None, sum_out=None):
+    """rms_norm with y in 8 bits: (q, scale), with residual (q, scale, z), and rstd last
+    with return_stats.  y = q * scale, q [..., C] float8_e4m3fn, scale float32: one for
+    each row [...], or for each group of 32, 64 or 128 channels [..., C / group]; the
+    largest |y| there over 448, at least 2^-100."""
+    return _seq.rms_norm_quantized(x, weight, eps, group, residual, return_stats, out, scale_out, sum_out)
+
+
+def rms_norm_backward(dy, x, rstd, weight=None, *, dsum=None, workspace=None):
+    """(dx, dweight) of rms_norm from dy and the rstd of the forward pass.  x is what was
+    normalised (with a residual: the returned z), and dx its gradient, which is that
+    of x and of residual alike; dsum is the gradient that reaches z past the norm.
+    dweight [C] has weight's dtype (None without weight)."""
+    return _seq.rms_norm_backward(dy, x, rstd, weight, dsum, workspace)
+
+
+def rms_norm_backward_workspace_bytes(x, weight=None):
+    """Bytes of the workspace that rms_norm_backward needs for x [..., C] and weight."""
+    if x.numel() == 0:
+        return 0
+    c, code = x.shape[-1], _DTYPE_CODE[x.dtype]
+    desc = _rms_desc(code, code if weight is None else _DTYPE_CODE[weight.dtype], 1, x.numel() // c, c, (0, c), (0, c),
+                     (0, c), 0.0, 0)
+    return _bytes("cnhwc_rms_norm_bwd_workspace", desc, int(weight is not None))
+
+
+# ------------------------------------------------------------------ rotary positions
+
+def rotary_frequencies(dim, base=10000.0, *, scaling=None, factor=1.0, original_length=None, fast=32.0, slow=1.0,
+                       device="cuda"):
+    """The frequencies of rotary positions, radians a position: base^(-2i / dim) for
+    i < dim / 2, float64 [dim / 2].  For contexts longer than a model was trained on:
+
+    scaling "linear": divided by factor (positions interpolated);
+    scaling "ntk": base times factor^(dim / (dim - 2)), which divides the lowest by factor
+    and leaves the highest;
+    scaling "yarn": those that turn less than ``slow`` times over original_length are
+    divided by factor, those that turn more than ``fast`` times are left, with a ramp
+    over the turns between (YaRN, arXiv 2309.00071; it also multiplies q and k by
+    0.1 ln(factor) + 1, which is rotary's ``scale``)."""
+    if dim < 0 or dim % 2:
+        raise ValueError("dim must be even")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    if scaling == "ntk" and dim > 2:
+        base = base * factor ** (dim / (dim - 2))
+    f = torch.tensor(base, dtype=torch.float64) ** (torch.arange(0, dim, 2, dtype=torch.float64) / -max(dim, 1))
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if not original_length or not fast > slow:
+            raise ValueError("yarn needs original_length, and fast above slow")
+        turns = f * (original_length / (2 * math.pi))
+        kept = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        f = f * kept + f / factor * (1 - kept)
+    return f.to(device)
+
+
+def rotary(x, freqs, *, positions=None, offset=0, interleaved=False, scale=1.0, out=None):
+    """Turns the first R channels of every head of x [N,L,H,D] (a token of each
+    sequence: [N,H,D]) in pairs by position * freqs[i], freqs float64 [R/2], R <= D;
+    the other channels go through.  A pair is the channels i and i + R/2, or 2i and
+    2i + 1 with interleaved; scale multiplies what was turned.
+
+    The position is offset + positions (int32, [N,L] or [L], of tokens [N]), or
+    offset + t without positions.  Angles are taken in float64, so far positions keep
+    their digits.  out has a channel stride of 1 and may be x itself."""
+    return _seq.rotary(x, freqs, positions, offset, interleaved, scale, False, out)
+
+
+def rotary_backward(dy, freqs, *, positions=None, offset=0, interleaved=False, scale=1.0, out=None):
+    """dx of rotary from dy: the same turn backwards."""
+    return _seq.rotary(dy, freqs, positions, offset, interleaved, scale, True, out)
+
+
+# ------------------------------------------------------------------ linear attention
+
+def linear_attention(q, k, v, log_decay, *, scale=1.0, state=None, lengths=None, return_state=False, out=None,
+                     workspace=None):
+    """Causal linear attention with a decay for each head:
+
+        S[n,t,h] = exp(log_decay[h]) S[n,t-1,h] + k[n,t,h]^T v[n,t,h]
+        y[n,t,h] = scale q[n,t,h] S[n,t,h]
+
+    q, k [N,L,H,DK] and v, y [N,L,H,DV] in one dtype; log_decay [H] (at most 0; minus
+    infinity forgets at once) and the states [N,H,DK,DV] in float32; DK, DV <= 256.
+    An absent state counts as 0.  Heads may be expanded (a stride of 0).  With
+    return_state: (y, the state after the last valid position)."""
+    return _seq.linear_attention(q, k, v, log_decay, scale, state, lengths, return_state, out, workspace)
+
+
+def linear_attention_backward(dy, q, k, v, log_decay, *, scale=1.0, state=None, lengths=None, dstate=None,
+                              decay_grad=False, workspace=None):
+    """LinearAttentionGrads(q, k, v, log_decay, state) of linear_attention from dy
+    [N,L,H,DV] and, if given, dstate [N,H,DK,DV], the gradient of the returned state.
+    log_decay's is None unless decay_grad asks for it, the state's None without state.
+    Expanded heads get the gradients of each head.  Nothing needs to be kept from
+    the forward pass but its inputs."""
+    return LinearAttentionGrads(*_seq.linear_attention_backward(dy, q, k, v, log_decay, scale, state, lengths, dstate,
+                                                                decay_grad, workspace))
+
+
+def linear_attention_workspace_bytes(q, v, backward=False, decay_grad=False):
+    """Bytes of the workspace that linear_attention (or its backward) needs for q [N,L,H,DK] and v [N,L,H,DV]."""
+    if v.numel() == 0:
+        return 0
+    n, l, h, dk = q.shape
+    dv = v.shape[-1]
+    a, b = (l * h * dk, h * dk, dk), (l * h * dv, h * dv, dv)
+    desc = _attention_desc(_DTYPE_CODE[q.dtype], n, l, h, dk, dv, a, a, b, b)
+    if backward:
+        return _bytes("cnhwc_linear_attention_bwd_workspace", desc, int(decay_grad))
+    return _bytes("cnhwc_linear_attention_fwd_workspace", desc)
+
+
+def linear_attention_step(q, k, v, log_decay, state, *, scale=1.0, state_out=None, out=None):
+    """linear_attention of one new token per sequence: q, k [N,H,DK], v, y [N,H,DV].  The
+    state [N,H,DK,DV] moves on by the token, in place or into state_out."""
+    return _seq.linear_attention_step(q, k, v, log_decay, state, scale, state_out, out)

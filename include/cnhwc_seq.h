@@ -1,11 +1,13 @@
 /*
  * cnhwc_seq.h -- C ABI of the sequence operators of the channels-last library
- * for AMD MI355X (gfx950): layer norm over channels, the short causal
- * (depthwise) convolution, and the selective state space scan, each forward
- * and backward, and the last two also for single tokens.
+ * for AMD MI355X (gfx950): layer norm and root-mean-square norm over channels,
+ * the short causal (depthwise) convolution, the selective state space scan,
+ * rotary positions and linear attention with a decay for each head, each forward
+ * and backward; the convolution, the scan and linear attention also for single tokens.
  *
- * Together with the pointwise conv1d of cnhwc.h they make up a sequence block:
- * norm, projection, causal convolution, scan with its gate, projection.
+ * Together with the pointwise conv1d of cnhwc.h they make up sequence blocks:
+ * norm, projection, causal convolution, scan with its gate, projection; or norm,
+ * projection, rotary positions of q and k, linear attention, projection.
  *
  * Layouts.  Sequences are [N,L,C] with the channels innermost (stride 1).
  * Input tensors carry the element strides of N and L in the descriptor, so a
@@ -27,7 +29,7 @@
  * queued, and results depend on the arguments alone, with the same bits on
  * every call (no atomics).  Tensor pointers are aligned to their element, the
  * workspace and fp32 tensors to 16 bytes.  Outputs overlap nothing, except
- * where a step's state_out is its state.
+ * where they are named as updated in place (a step's state_out on its state).
  */
 #ifndef CNHWC_SEQ_H_
 #define CNHWC_SEQ_H_
@@ -174,6 +176,129 @@ cnhwc_status_t cnhwc_scan_bwd(const cnhwc_scan_desc_t* desc, const cnhwc_scan_in
  * state_out may be in->state itself (updated in place). */
 cnhwc_status_t cnhwc_scan_step(const cnhwc_scan_desc_t* desc, const cnhwc_scan_inputs_t* in, void* y,
                                float* state_out, void* hip_stream);
+
+/* ------------------------------------------------------------ root-mean-square norm
+ * z = x + residual (x alone without one), rstd = 1 / sqrt(mean z^2 + eps) over the C
+ * channels of each of the N*L rows, y = z rstd w.  sum receives z in the
+ * activations' dtype; y comes from z before that rounding.
+ *
+ * The 8-bit form stores q in e4m3 (OCP: 448 the largest value) and scale, fp32, so
+ * that y = q * scale: scale = max |y| / 448 over the row [N*L], or over each group of
+ * `group` channels [N*L, C / group], and at least 2^-100.  NaN stays NaN and counts
+ * for no maximum; where |y| is infinite the whole row or group is NaN. */
+typedef struct {
+  int32_t dtype;              /* cnhwc_dtype_t of x, residual, sum, y, dy, dsum, dx */
+  int32_t w_dtype;            /* of w, dw: dtype or CNHWC_F32 */
+  int64_t n, l, c;            /* each in [1, 2^31) */
+  int64_t x_stride[2];        /* elements: sequence, position */
+  int64_t residual_stride[2]; /* of residual; in the backward pass of dsum */
+  int64_t dy_stride[2];       /* backward only */
+  float eps;                  /* >= 0 */
+  int32_t group;              /* 8-bit form: channels to a scale, 32, 64 or 128, dividing C; 0: the row.
+                                 0 elsewhere */
+} cnhwc_rms_norm_desc_t;
+
+/* residual, w [C], sum and rstd (fp32 [N*L]) may be NULL; sum needs residual, and
+ * may be residual itself where that is dense (updated in place). */
+cnhwc_status_t cnhwc_rms_norm_fwd(const cnhwc_rms_norm_desc_t* desc, const void* x, const void* residual,
+                                  const void* w, void* y, void* sum, float* rstd, void* hip_stream);
+
+/* q: one byte an element. */
+cnhwc_status_t cnhwc_rms_norm_fwd_q8(const cnhwc_rms_norm_desc_t* desc, const void* x, const void* residual,
+                                     const void* w, void* q, float* scale, void* sum, float* rstd,
+                                     void* hip_stream);
+
+/* Bytes of workspace of the backward pass (0 without the parameter's gradient). */
+cnhwc_status_t cnhwc_rms_norm_bwd_workspace(const cnhwc_rms_norm_desc_t* desc, int32_t param_grads,
+                                            uint64_t* bytes);
+
+/* dx [N,L,C], the gradient of z and so of x and of residual, and dw [C] (with w, or
+ * NULL), from dy and dsum (what reaches z past the norm; NULL: 0); x is z. */
+cnhwc_status_t cnhwc_rms_norm_bwd(const cnhwc_rms_norm_desc_t* desc, const void* dy, const void* dsum,
+                                  const void* x, const float* rstd, const void* w, void* dx, void* dw,
+                                  void* workspace, uint64_t workspace_bytes, void* hip_stream);
+
+/* ------------------------------------------------------------ rotary positions
+ * The first R channels of each head of x [N,L,H,D] turn in R/2 pairs, by the angle
+ * position * freqs[i] and times scale; the channels from R on are copied.  The
+ * pair i: channels i and i + R/2, or 2i and 2i + 1 (interleaved).  The position is
+ * offset + positions[n,t], or offset + t without positions.  inverse turns back
+ * (still times scale): the gradient. */
+typedef struct {
+  int32_t dtype;              /* of x and out */
+  int32_t interleaved;        /* 0 or 1 */
+  int64_t n, l, h;            /* each in [1, 2^31) */
+  int32_t d, r;               /* d >= 1; r even, in [0, d] */
+  int64_t x_stride[3], out_stride[3]; /* elements: sequence, position, head */
+  int64_t position_stride[2];
+  int64_t offset;             /* within 2^40 of 0 */
+  float scale;
+  int32_t inverse;            /* 0 or 1 */
+  int64_t reserved;           /* 0 */
+} cnhwc_rotary_desc_t;
+
+/* freqs: fp64 [R/2], radians a position; positions: int32 or NULL.  out has
+ * strides of its own and may be x itself, with the same ones. */
+cnhwc_status_t cnhwc_rotary(const cnhwc_rotary_desc_t* desc, const void* x, const double* freqs,
+                            const int32_t* positions, void* out, void* hip_stream);
+
+/* ------------------------------------------------------------ linear attention
+ *   S[t] = exp(log_decay[h]) S[t-1] + k[t]^T v[t],   y[t] = scale q[t] S[t]
+ * for each head; the state S is fp32 [N,H,DK,DV].  Decays are meant (log_decay <= 0,
+ * minus infinity included); a state that grows past fp32 is not represented.
+ * Heads may be shared through strides of 0; gradients are those of each head. */
+#define CNHWC_LINEAR_ATTENTION_MAX_DIM 256
+
+typedef struct {
+  int32_t dtype;          /* of q, k, v, y, dy and their gradients */
+  int32_t reserved;       /* 0 */
+  int64_t n, l, h;        /* each in [1, 2^31) */
+  int32_t dk, dv;         /* in [1, CNHWC_LINEAR_ATTENTION_MAX_DIM]; more is UNSUPPORTED */
+  int64_t q_stride[3], k_stride[3], v_stride[3];  /* elements: sequence, position, head */
+  int64_t dy_stride[3];   /* backward only */
+  float scale;
+  int32_t reserved2;      /* 0 */
+} cnhwc_linear_attention_desc_t;
+
+typedef struct {
+  const void* q;            /* [N,L,H,DK] */
+  const void* k;            /* [N,L,H,DK] */
+  const void* v;            /* [N,L,H,DV] */
+  const float* log_decay;   /* [H] */
+  const float* state;       /* [N,H,DK,DV] or NULL (0) */
+  const int32_t* lengths;   /* [N] or NULL */
+} cnhwc_linear_attention_inputs_t;
+
+typedef struct {
+  void* q;                  /* [N,L,H,DK] */
+  void* k;                  /* [N,L,H,DK] */
+  void* v;                  /* [N,L,H,DV] */
+  float* log_decay;         /* [H] or NULL (not wanted) */
+  float* state;             /* [N,H,DK,DV] or NULL */
+} cnhwc_linear_attention_grads_t;
+
+cnhwc_status_t cnhwc_linear_attention_fwd_workspace(const cnhwc_linear_attention_desc_t* desc, uint64_t* bytes);
+
+/* y [N,L,H,DV]; state_out [N,H,DK,DV] may be NULL. */
+cnhwc_status_t cnhwc_linear_attention_fwd(const cnhwc_linear_attention_desc_t* desc,
+                                          const cnhwc_linear_attention_inputs_t* in, void* y, float* state_out,
+                                          void* workspace, uint64_t workspace_bytes, void* hip_stream);
+
+cnhwc_status_t cnhwc_linear_attention_bwd_workspace(const cnhwc_linear_attention_desc_t* desc,
+                                                    int32_t decay_grad, uint64_t* bytes);
+
+/* Gradients from dy [N,L,H,DV] and dstate_out (the gradient of the final state;
+ * NULL: 0).  Nothing has to be kept from the forward pass. */
+cnhwc_status_t cnhwc_linear_attention_bwd(const cnhwc_linear_attention_desc_t* desc,
+                                          const cnhwc_linear_attention_inputs_t* in, const void* dy,
+                                          const float* dstate_out, const cnhwc_linear_attention_grads_t* grads,
+                                          void* workspace, uint64_t workspace_bytes, void* hip_stream);
+
+/* One position (l == 1; in->state is required, in->lengths must be NULL).
+ * state_out may be in->state itself (updated in place). */
+cnhwc_status_t cnhwc_linear_attention_step(const cnhwc_linear_attention_desc_t* desc,
+                                           const cnhwc_linear_attention_inputs_t* in, void* y,
+                                           float* state_out, void* hip_stream);
 
 #ifdef __cplusplus
 }
