@@ -9,10 +9,8 @@
 // where the backward ones meet G before a position's decay: G[t] = exp(g) G[t+1] ...
 #include <hip/hip_runtime.h>
 
-#include <cfloat>
-#include <type_traits>
-
 #include "internal.hpp"
+#include "linear_attention.hpp"
 #include "seq_common.hpp"
 #include "seq_host.hpp"
 
@@ -20,113 +18,72 @@ namespace cnhwc {
 namespace seq {
 namespace {
 
-// One pass: y = scale q S with S from k and v.  The backward pass puts other
-// tensors into these places.
-template <int DT>
-struct Pass {
-  const Elem<DT>* q;
-  const Elem<DT>* k;
-  const Elem<DT>* v;
-  Elem<DT>* y;             // dense [N,L,H,DV]
-  const float* state;      // element (i, j) of [DK,DV] at i * state_k + j * state_v
-  float* state_out;
-  int64_t qs[3], ks[3], vs[3];  // element strides: sequence, position, head
-  int64_t state_k, state_v;
-  int32_t dk, dv;
-  bool back;               // positions from the end, the state decays after its use
-  float scale_k, scale_y;  // of what enters the state, of what leaves it
-};
-
-struct LaGeo {
-  int32_t l, h;
-  const float* log_decay;
-  const int32_t* lengths;
-};
-
-// log_decay, finite for minus infinity too (0 times it is 0).
-__device__ __forceinline__ float rate(float g) { return g < -FLT_MAX ? -FLT_MAX : g; }
-
-// x -> exp(g) x without losing what a slow decay is about: exp(g) - 1 keeps its
-// digits where exp(g), rounded, would be off by 2^-25 at every position, 10^-4
-// after 4096 of them.
-struct Decay {
-  float m;     // exp(g) - 1, or exp(g)
-  float keep;  // 1, or 0
-  __device__ __forceinline__ explicit Decay(float g) {
-    const bool slow = __builtin_fabsf(g) < 0.5f;
-    m = slow ? expm1f(g) : exp_full(g);
-    keep = slow ? 1.0f : 0.0f;
-  }
-  __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(m, x, keep * x); }
-};
-
 // ---------------------------------------------------------------- position by position
 
-// A workgroup holds 64 columns of one head's state: 16 lanes by four columns, 16
-// row groups, rows r, r + 16, ... of NI.
-template <int DT, int NI>
+// A token of every sequence: a workgroup holds 64 columns of one head's state, 16 lanes by
+// four columns, 16 row groups, rows r, r + 16, ... of NI.  The state is the traffic,
+// read once and written once.
+template <int DT, int NI, bool VEC>
 __global__ __launch_bounds__(256) void la_step_kernel(Pass<DT> p, LaGeo g) {
-  __shared__ float part[2][4][64];
+  __shared__ float part[4][64];
   const int64_t nh = blockIdx.x;
   const int64_t n = nh / g.h, hd = nh - n * g.h;
   const int j0 = int(blockIdx.y) * 64 + int(threadIdx.x & 15) * 4, r0 = threadIdx.x >> 4;
   const int64_t base = nh * p.dk * p.dv;
   float s[NI][4];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NI; ++i) {
+    const int r = r0 + 16 * i;
+    if constexpr (VEC) {
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (r < p.dk && j0 < p.dv) f = *reinterpret_cast<const float4*>(p.state + base + r * p.dv + j0);
+      s[i][0] = f.x, s[i][1] = f.y, s[i][2] = f.z, s[i][3] = f.w;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = r0 + 16 * i, j = j0 + e;
-      s[i][e] = p.state && r < p.dk && j < p.dv ? p.state[base + r * p.state_k + j * p.state_v] : 0.0f;
+      for (int e = 0; e < 4; ++e) s[i][e] = r < p.dk && j0 + e < p.dv ? p.state[base + r * p.dv + j0 + e] : 0.0f;
     }
-  const Decay decay(rate(g.log_decay[hd]));
-  const int32_t len = valid_len(g.lengths, n, g.l);
+  }
   const Elem<DT>* qn = p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* kn = p.k + n * p.ks[0] + hd * p.ks[2];
   const Elem<DT>* vn = p.v + n * p.vs[0] + hd * p.vs[2];
-  for (int32_t i = 0; i < g.l; ++i) {
-    const int32_t t = p.back ? g.l - 1 - i : i;
-    Elem<DT>* y = p.y + ((n * g.l + t) * g.h + hd) * p.dv;
-    if (t >= len) {  // uniform over the workgroup
-      if (threadIdx.x < 64 && blockIdx.y * 64 + threadIdx.x < p.dv) y[blockIdx.y * 64 + threadIdx.x] = Elem<DT>(0);
-      continue;
-    }
-    float v[4], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float v[4], k[NI], q[NI], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = j0 + e < p.dv ? to_f<DT>(vn[t * p.vs[1] + j0 + e]) : 0.0f;
+  for (int e = 0; e < 4; ++e) v[e] = j0 + e < p.dv ? to_f<DT>(vn[j0 + e]) : 0.0f;
 #pragma unroll
-    for (int a = 0; a < NI; ++a) {
-      const int r = r0 + 16 * a;
-      const float k = r < p.dk ? to_f<DT>(kn[t * p.ks[1] + r]) * p.scale_k : 0.0f;
-      const float q = r < p.dk ? to_f<DT>(qn[t * p.qs[1] + r]) : 0.0f;
+  for (int i = 0; i < NI; ++i) {
+    const int r = r0 + 16 * i;
+    k[i] = r < p.dk ? to_f<DT>(kn[r]) : 0.0f;
+    q[i] = r < p.dk ? to_f<DT>(qn[r]) : 0.0f;
+  }
+  const Decay decay(rate(g.log_decay[hd]));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[a][e] = __builtin_fmaf(k, v[e], p.back ? s[a][e] : decay(s[a][e]));
-        acc[e] = __builtin_fmaf(q, s[a][e], acc[e]);
-        if (p.back) s[a][e] = decay(s[a][e]);
-      }
-    }
+  for (int i = 0; i < NI; ++i) {
+    const int r = r0 + 16 * i;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      acc[e] = add_halves(add_row_pairs(acc[e]));
-      if ((threadIdx.x & 48) == 0) part[i & 1][threadIdx.x >> 6][(threadIdx.x & 15) * 4 + e] = acc[e];
+      s[i][e] = __builtin_fmaf(k[i], v[e], decay(s[i][e]));
+      acc[e] = __builtin_fmaf(q[i], s[i][e], acc[e]);
     }
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      const int j = int(blockIdx.y) * 64 + threadIdx.x;
-      const float (&w)[4][64] = part[i & 1];
-      const float sum = (w[0][threadIdx.x] + w[1][threadIdx.x]) + (w[2][threadIdx.x] + w[3][threadIdx.x]);
-      if (j < p.dv) y[j] = from_f<DT>(sum * p.scale_y);
+    float* to = p.state_out + base + r * p.dv + j0;
+    if constexpr (VEC) {
+      if (r < p.dk && j0 < p.dv) *reinterpret_cast<float4*>(to) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r < p.dk && j0 + e < p.dv) to[e] = s[i][e];
     }
   }
-  if (!p.state_out) return;
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = r0 + 16 * i, j = j0 + e;
-      if (r < p.dk && j < p.dv) p.state_out[base + r * p.state_k + j * p.state_v] = s[i][e];
-    }
+  for (int e = 0; e < 4; ++e) {
+    acc[e] = add_halves(add_row_pairs(acc[e]));
+    if ((threadIdx.x & 48) == 0) part[threadIdx.x >> 6][(threadIdx.x & 15) * 4 + e] = acc[e];
+  }
+  __syncthreads();
+  const int j = int(blockIdx.y) * 64 + threadIdx.x;
+  if (threadIdx.x < 64 && j < p.dv) {
+    const float sum = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+    p.y[nh * p.dv + j] = from_f<DT>(sum * p.scale_y);
+  }
 }
 
 // The gradient of log_decay: with T[t] = exp(g) (T[t-1] + S[t-1]), the state's
@@ -210,11 +167,89 @@ void with_rows(int32_t dk, F&& f) {  // rows of 16 that a thread holds one of
 }
 
 template <int DT>
-void launch_steps(const Pass<DT>& p, const LaGeo& g, int64_t nh, hipStream_t st) {
+void launch_step(const Pass<DT>& p, const LaGeo& g, int64_t nh, hipStream_t st) {
+  const dim3 grid(unsigned(nh), unsigned((p.dv + 63) / 64));
   with_rows(p.dk, [&](auto ni) {
-    hipLaunchKernelGGL((la_step_kernel<DT, decltype(ni)::value>), dim3(unsigned(nh), unsigned((p.dv + 63) / 64)),
-                       dim3(256), 0, st, p, g);
+    constexpr int NI = decltype(ni)::value;
+    if (p.dv % 4 == 0) hipLaunchKernelGGL((la_step_kernel<DT, NI, true>), grid, dim3(256), 0, st, p, g);
+    else hipLaunchKernelGGL((la_step_kernel<DT, NI, false>), grid, dim3(256), 0, st, p, g);
   });
+}
+
+// The form of a pass: 16-row tiles of a state, 64-column parts of a workgroup (1 or 2).
+template <typename F>
+void with_shape(int32_t dk, int32_t dv, F&& f) {
+  auto wide = [&](auto dkt) {
+    if (dv <= 64) f(dkt, std::integral_constant<int, 1>{});
+    else f(dkt, std::integral_constant<int, 2>{});
+  };
+  if (dk <= 32) wide(std::integral_constant<int, 2>{});
+  else if (dk <= 64) wide(std::integral_constant<int, 4>{});
+  else if (dk <= 128) wide(std::integral_constant<int, 8>{});
+  else wide(std::integral_constant<int, 16>{});
+}
+
+// How a pass is cut: its chunk, the workgroups along a state's columns, the runs of
+// chunks, and the bytes of the states between them.  A function of the sizes alone.
+struct Cut {
+  int32_t chunk, parts, chunks, run, runs;
+  int32_t per;     // float4 of a head's state in lane order
+  uint64_t bytes;
+};
+template <int DT>
+Cut cut_of(const Desc& d, int32_t dk, int32_t dv, int64_t passes) {
+  Cut c{};
+  with_shape(dk, dv, [&](auto dkt, auto nt) {
+    constexpr int DKT = decltype(dkt)::value, NT = decltype(nt)::value;
+    using Sh = ChunkShape<DT, DKT, NT>;
+    c.chunk = Sh::kChunk;
+    c.parts = (dv + 64 * NT - 1) / (64 * NT);
+    c.per = c.parts * 4 * DKT * NT * 64;
+    c.chunks = int32_t((d.l + c.chunk - 1) / c.chunk);
+    const int64_t all = d.n * d.h * c.parts * passes, room = 256 * Sh::kOccupancy;
+    int64_t runs = all * 2 > room ? 1 : room / all;
+    if (runs > c.chunks / 4) runs = c.chunks / 4;
+    if (runs < 1) runs = 1;
+    c.run = int32_t((c.chunks + runs - 1) / runs);
+    c.runs = (c.chunks + c.run - 1) / c.run;
+  });
+  c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16;
+  return c;
+}
+
+bool whole(const void* p, const int64_t (&s)[3], int32_t c, int64_t piece, uint64_t es) {
+  return aligned(p, piece * es) && c % piece == 0 && s[0] % piece == 0 && s[1] % piece == 0 && s[2] % piece == 0;
+}
+
+// One or several passes of the same form.
+template <int DT>
+hipError_t launch_passes(Passes<DT>& ps, int count, LaGeo g, const Cut& c, int64_t heads, char* workspace,
+                         hipStream_t st) {
+  const uint64_t es = sizeof(Elem<DT>);
+  constexpr int kPiece = Mma<DT>::kPiece;
+  g.chunks = c.chunks, g.run = c.run, g.runs = c.runs;
+  for (int i = 0; i < count; ++i) {
+    Pass<DT>& p = ps.p[i];
+    p.vec_q = whole(p.q, p.qs, p.dk, kPiece, es);
+    p.vec_k = whole(p.k, p.ks, p.dk, kPiece, es);
+    p.vec_v = whole(p.v, p.vs, p.dv, kPiece, es);
+    p.vec_y = aligned(p.y, 4 * es) && p.dv % 4 == 0;
+    p.kept = reinterpret_cast<float4*>(workspace + i * c.bytes);
+  }
+  with_shape(ps.p[0].dk, ps.p[0].dv, [&](auto dkt, auto nt) {
+    constexpr int DKT = decltype(dkt)::value, NT = decltype(nt)::value;
+    const int64_t blocks = heads * c.parts;
+    if (c.runs > 1) {
+      hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, NT, true>), dim3(unsigned(blocks * (c.runs - 1)), count), dim3(256),
+                         0, st, ps, g);
+      const int64_t total = heads * c.per;
+      hipLaunchKernelGGL((la_join_kernel<DT>), dim3(grid_of(ceil_div(total, int64_t(256))).x, count), dim3(256), 0, st,
+                         ps, g, heads, c.per, c.chunk);
+    }
+    hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, NT, false>), dim3(unsigned(blocks * c.runs), count), dim3(256), 0, st,
+                       ps, g);
+  });
+  return hipGetLastError();
 }
 
 template <int DT>
@@ -275,33 +310,79 @@ bool inputs_ok(const Desc& d, const cnhwc_linear_attention_inputs_t* in, Buffers
 }
 
 LaGeo geo_of(const Desc& d, const cnhwc_linear_attention_inputs_t& in) {
-  return {int32_t(d.l), int32_t(d.h), in.log_decay, in.lengths};
+  return {int32_t(d.l), int32_t(d.h), in.log_decay, in.lengths, 0, 0, 0};
 }
 
 template <int DT>
 hipError_t forward_t(const Desc& d, const cnhwc_linear_attention_inputs_t& in, void* y, float* state_out,
-                     hipStream_t st) {
+                     char* workspace, hipStream_t st) {
+  Passes<DT> ps{};
+  ps.p[0] = pass_of<DT>(in.q, d.q_stride, in.k, d.k_stride, in.v, d.v_stride, y, d.dk, d.dv, d.scale, false);
+  ps.p[0].state = in.state, ps.p[0].state_out = state_out;
+  return launch_passes(ps, 1, geo_of(d, in), cut_of<DT>(d, d.dk, d.dv, 1), d.n * d.h, workspace, st);
+}
+
+template <int DT>
+hipError_t step_t(const Desc& d, const cnhwc_linear_attention_inputs_t& in, void* y, float* state_out,
+                  hipStream_t st) {
   Pass<DT> p = pass_of<DT>(in.q, d.q_stride, in.k, d.k_stride, in.v, d.v_stride, y, d.dk, d.dv, d.scale, false);
   p.state = in.state, p.state_out = state_out;
-  launch_steps(p, geo_of(d, in), d.n * d.h, st);
+  launch_step(p, geo_of(d, in), d.n * d.h, st);
   return hipGetLastError();
+}
+
+// The cuts of the backward passes: of v's, whose state is [DK,DV], and of q's and k's,
+// whose state is [DV,DK].  Where the two have one form all three go in one launch.
+template <int DT>
+bool one_form(const Desc& d) {
+  int a = 0, b = 0;
+  with_shape(d.dk, d.dv, [&](auto dkt, auto nt) { a = dkt.value * 4 + nt.value; });
+  with_shape(d.dv, d.dk, [&](auto dkt, auto nt) { b = dkt.value * 4 + nt.value; });
+  return a == b && (d.dk + 127) / 128 == (d.dv + 127) / 128;
+}
+template <int DT>
+void backward_cuts(const Desc& d, Cut& v, Cut& qk) {
+  if (one_form<DT>(d)) {
+    v = qk = cut_of<DT>(d, d.dk, d.dv, 3);
+  } else {
+    v = cut_of<DT>(d, d.dk, d.dv, 1);
+    qk = cut_of<DT>(d, d.dv, d.dk, 2);
+  }
+}
+uint64_t backward_bytes(const Desc& d, bool decay_grad) {
+  Cut v, qk;
+  if (d.dtype == CNHWC_F32) backward_cuts<CNHWC_F32>(d, v, qk);
+  else if (d.dtype == CNHWC_F16) backward_cuts<CNHWC_F16>(d, v, qk);
+  else backward_cuts<CNHWC_BF16>(d, v, qk);
+  const uint64_t part = decay_grad ? uint64_t(d.n) * d.h * ((d.dv + 63) / 64) * 4 : 0;
+  return v.bytes + 2 * qk.bytes + (part + 15) / 16 * 16;
 }
 
 template <int DT>
 hipError_t backward_t(const Desc& d, const cnhwc_linear_attention_inputs_t& in, const void* dy,
-                      const float* dstate_out, const cnhwc_linear_attention_grads_t& gr, float* part,
+                      const float* dstate_out, const cnhwc_linear_attention_grads_t& gr, char* workspace,
                       hipStream_t st) {
   const LaGeo g = geo_of(d, in);
   const int64_t nh = d.n * d.h;
   Pass<DT> q = pass_of<DT>(dy, d.dy_stride, in.v, d.v_stride, in.k, d.k_stride, gr.q, d.dv, d.dk, d.scale, false);
   q.state = in.state, q.state_k = 1, q.state_v = d.dv;  // S^T
-  launch_steps(q, g, nh, st);
   Pass<DT> v = pass_of<DT>(in.k, d.k_stride, in.q, d.q_stride, dy, d.dy_stride, gr.v, d.dk, d.dv, d.scale, true);
   v.state = dstate_out, v.state_out = gr.state;
-  launch_steps(v, g, nh, st);
   Pass<DT> k = pass_of<DT>(in.v, d.v_stride, dy, d.dy_stride, in.q, d.q_stride, gr.k, d.dv, d.dk, d.scale, true);
   k.state = dstate_out, k.state_k = 1, k.state_v = d.dv;
-  launch_steps(k, g, nh, st);
+  Cut cv, cqk;
+  backward_cuts<DT>(d, cv, cqk);
+  hipError_t e;
+  if (one_form<DT>(d)) {
+    Passes<DT> ps{{q, k, v}};
+    e = launch_passes(ps, 3, g, cv, nh, workspace, st);
+  } else {
+    Passes<DT> ps{{q, k}}, pv{{v}};
+    e = launch_passes(ps, 2, g, cqk, nh, workspace, st);
+    if (e == hipSuccess) e = launch_passes(pv, 1, g, cv, nh, workspace + 2 * cqk.bytes, st);
+  }
+  if (e != hipSuccess) return e;
+  float* part = reinterpret_cast<float*>(workspace + cv.bytes + 2 * cqk.bytes);
   if (gr.log_decay) {
     Pass<DT> s = pass_of<DT>(in.q, d.q_stride, in.k, d.k_stride, in.v, d.v_stride, nullptr, d.dk, d.dv, d.scale, false);
     s.state = in.state;
@@ -328,7 +409,10 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_fwd_workspace(const Desc* desc,
   const cnhwc_status_t st = check_desc(desc, false);
   if (st != CNHWC_OK) return st;
   if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
-  *bytes = 0;
+  const Desc& d = *desc;
+  *bytes = d.dtype == CNHWC_F32   ? cut_of<CNHWC_F32>(d, d.dk, d.dv, 1).bytes
+           : d.dtype == CNHWC_F16 ? cut_of<CNHWC_F16>(d, d.dk, d.dv, 1).bytes
+                                  : cut_of<CNHWC_BF16>(d, d.dk, d.dv, 1).bytes;
   return CNHWC_OK;
 }
 
@@ -350,9 +434,10 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_fwd(const Desc* desc, const cnh
   }
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
-  const hipError_t e = d.dtype == CNHWC_F32   ? forward_t<CNHWC_F32>(d, *in, y, state_out, s)
-                       : d.dtype == CNHWC_F16 ? forward_t<CNHWC_F16>(d, *in, y, state_out, s)
-                                              : forward_t<CNHWC_BF16>(d, *in, y, state_out, s);
+  char* ws = static_cast<char*>(workspace);
+  const hipError_t e = d.dtype == CNHWC_F32   ? forward_t<CNHWC_F32>(d, *in, y, state_out, ws, s)
+                       : d.dtype == CNHWC_F16 ? forward_t<CNHWC_F16>(d, *in, y, state_out, ws, s)
+                                              : forward_t<CNHWC_BF16>(d, *in, y, state_out, ws, s);
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }
 
@@ -361,7 +446,7 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_bwd_workspace(const Desc* desc,
   const cnhwc_status_t st = check_desc(desc, true);
   if (st != CNHWC_OK) return st;
   if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
-  *bytes = decay_grad ? uint64_t(desc->n) * desc->h * ((desc->dv + 63) / 64) * 4 : 0;
+  *bytes = backward_bytes(*desc, decay_grad != 0);
   return CNHWC_OK;
 }
 
@@ -391,10 +476,10 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_bwd(const Desc* desc, const cnh
   }
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
-  float* part = static_cast<float*>(workspace);
-  const hipError_t e = d.dtype == CNHWC_F32   ? backward_t<CNHWC_F32>(d, *in, dy, dstate_out, *grads, part, s)
-                       : d.dtype == CNHWC_F16 ? backward_t<CNHWC_F16>(d, *in, dy, dstate_out, *grads, part, s)
-                                              : backward_t<CNHWC_BF16>(d, *in, dy, dstate_out, *grads, part, s);
+  char* ws = static_cast<char*>(workspace);
+  const hipError_t e = d.dtype == CNHWC_F32   ? backward_t<CNHWC_F32>(d, *in, dy, dstate_out, *grads, ws, s)
+                       : d.dtype == CNHWC_F16 ? backward_t<CNHWC_F16>(d, *in, dy, dstate_out, *grads, ws, s)
+                                              : backward_t<CNHWC_BF16>(d, *in, dy, dstate_out, *grads, ws, s);
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }
 
@@ -411,8 +496,8 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_step(const Desc* desc, const cn
   bf.out(state_out, uint64_t(d.n) * d.h * d.dk * d.dv * 4, 16, true);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
-  const hipError_t e = d.dtype == CNHWC_F32   ? forward_t<CNHWC_F32>(d, *in, y, state_out, s)
-                       : d.dtype == CNHWC_F16 ? forward_t<CNHWC_F16>(d, *in, y, state_out, s)
-                                              : forward_t<CNHWC_BF16>(d, *in, y, state_out, s);
+  const hipError_t e = d.dtype == CNHWC_F32   ? step_t<CNHWC_F32>(d, *in, y, state_out, s)
+                       : d.dtype == CNHWC_F16 ? step_t<CNHWC_F16>(d, *in, y, state_out, s)
+                                              : step_t<CNHWC_BF16>(d, *in, y, state_out, s);
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }

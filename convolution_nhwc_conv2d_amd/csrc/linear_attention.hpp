@@ -1,0 +1,555 @@
+// Linear attention's passes in chunks of positions, as matrix products.
+//
+// A pass is y = scale q S with S from k and v (the gradients are passes with other
+// tensors in these places).  In a chunk of C positions that starts from the state S,
+//   y[u] = e^(g (u+1)) q[u] S + sum_{s <= u} e^(g (u-s)) (q[u] . k[s]) v[s]
+//   S'   = e^(g C) S + sum_t k[t]^T (e^(g (C-1-t)) v[t])
+// which is four matrix products: q k^T under its decays, that times v, q S, and k^T
+// times the decayed v.  A pass from the end has u and s the other way round.
+//
+// A workgroup owns one head's state, or 64 NT columns of it, for a run of chunks.  The
+// four wavefronts have 16 NT columns each, in fp32 accumulators: a lane holds
+// four consecutive rows of one column, which is just what the next product takes
+// as its left operand (S^T), so the state never leaves the registers.  y is computed
+// transposed for the same reason, and a lane then stores consecutive channels.
+// Only the products of q and k go through LDS, since every wavefront needs all of them.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+#include <type_traits>
+
+#include "device_common.hpp"
+#include "seq_common.hpp"
+
+namespace cnhwc {
+namespace seq {
+
+// One pass: y = scale q S with S from k and v.  The backward pass puts other
+// tensors into these places.
+template <int DT>
+struct Pass {
+  const Elem<DT>* q;
+  const Elem<DT>* k;
+  const Elem<DT>* v;
+  Elem<DT>* y;             // dense [N,L,H,DV]
+  const float* state;      // element (i, j) of [DK,DV] at i * state_k + j * state_v
+  float* state_out;
+  int64_t qs[3], ks[3], vs[3];  // element strides: sequence, position, head
+  int64_t state_k, state_v;
+  int32_t dk, dv;
+  bool back;               // positions from the end, the state decays after its use
+  float scale_k, scale_y;  // of what enters the state, of what leaves it
+  bool vec_q, vec_k, vec_v, vec_y;  // whole vectors to load and store
+  float4* kept;            // the states that enter all runs of chunks but the first, in lane order
+};
+
+struct LaGeo {
+  int32_t l, h;
+  const float* log_decay;
+  const int32_t* lengths;
+  int32_t chunks, run, runs;  // chunks of a sequence, of a run, runs of a sequence
+};
+
+// log_decay, finite for minus infinity too (0 times it is 0).
+__device__ __forceinline__ float rate(float g) { return g < -FLT_MAX ? -FLT_MAX : g; }
+
+// x -> exp(g) x without losing what a slow decay is about: exp(g) - 1 keeps its
+// digits where exp(g), rounded, would be off by 2^-25 at every position, 10^-4
+// after 4096 of them.
+struct Decay {
+  float m;     // exp(g) - 1, or exp(g)
+  float keep;  // 1, or 0
+  __device__ __forceinline__ explicit Decay(float g) {
+    const bool slow = __builtin_fabsf(g) < 0.5f;
+    m = slow ? expm1f(g) : exp_full(g);
+    keep = slow ? 1.0f : 0.0f;
+  }
+  __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(m, x, keep * x); }
+};
+
+// What the matrix products are made of.  bf16: operands as they are, 32 deep; an
+// fp32 operand is one to three bf16 terms (8 digits each).  Otherwise fp32, 16 deep
+// in four instructions.  The depth runs over the lanes' four groups g in an order
+// that the accumulators have (16 i + 4 g + r): a lane's elements are rows
+// 4 g ... 4 g + 3 of one 16-row tile (fp32), or of two (bf16).
+template <int DT>
+struct Mma {
+  using T = float;
+  using Frag = float4;
+  static constexpr int kDeep = 16, kPiece = 4, kTerms = 1;
+  static __device__ __forceinline__ void mul(const Frag& a, const Frag& b, v4f& c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b.x, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b.y, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.z, b.z, c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b.w, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<CNHWC_BF16> {
+  using T = uint16_t;
+  using Frag = uint4;
+  static constexpr int kDeep = 32, kPiece = 8, kTerms = 3;
+  static __device__ __forceinline__ void mul(const Frag& a, const Frag& b, v4f& c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  }
+};
+
+// Two floats as bf16, the first in the lower half; and back.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return uint32_t(from_f<CNHWC_BF16>(a)) | uint32_t(from_f<CNHWC_BF16>(b)) << 16;
+}
+__device__ __forceinline__ float low2(uint32_t v) { return __builtin_bit_cast(float, v << 16); }
+__device__ __forceinline__ float high2(uint32_t v) { return __builtin_bit_cast(float, v & 0xffff0000u); }
+
+// An operand of kPiece floats as TERMS operands that add up to it.
+template <int DT, int TERMS, int P>
+__device__ __forceinline__ void split(const float (&x)[P], typename Mma<DT>::Frag (&f)[TERMS]) {
+  if constexpr (P == 4) {
+    f[0] = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = x[i];
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      uint32_t p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = pack2(v[2 * i], v[2 * i + 1]);
+        if (t + 1 < TERMS) v[2 * i] -= low2(p[i]), v[2 * i + 1] -= high2(p[i]);
+      }
+      f[t] = make_uint4(p[0], p[1], p[2], p[3]);
+    }
+  }
+}
+
+// A tile of CH positions by COLS channels on its way from memory into LDS: rows of
+// COLS elements and 16 bytes more, so that the 16 rows that are read together lie in
+// different banks.  bf16 rows whose channels are a product's depth have each 32
+// of them in the order of the lanes (element 16 i + 4 g + r at 8 g + 4 i + r).
+template <int DT, int COLS, int CH>
+struct Rows2D {
+  using M = Mma<DT>;
+  using T = typename M::T;
+  static constexpr int kPiece = M::kPiece, kPer = COLS / kPiece, kCount = CH * kPer / 256;
+  static constexpr int kStride = COLS * int(sizeof(T)) + 16, kBytes = CH * kStride;
+  static_assert(kCount * 256 == CH * kPer, "whole pieces for every thread");
+  Pack<DT, kPiece> v[kCount];
+
+  // rows past `valid` and channels past `cols` are 0 and not read
+  __device__ __forceinline__ void load(const Elem<DT>* __restrict__ base, int64_t stride, int32_t cols, int32_t valid,
+                                       bool vec) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const int id = int(threadIdx.x) + 256 * i, row = id / kPer, col = id % kPer * kPiece;
+      Pack<DT, kPiece> x{};
+      if (row < valid && col < cols) {
+        const Elem<DT>* p = base + row * stride + col;
+        if (vec) {
+          x = load_pack<DT, kPiece>(p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPiece; ++e)
+            if (col + e < cols) x.e[e] = p[e];
+        }
+      }
+      v[i] = x;
+    }
+  }
+
+  template <bool DEPTH>
+  __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      const int id = int(threadIdx.x) + 256 * i, row = id / kPer, col = id % kPer * kPiece;
+      char* p = lds + row * kStride;
+      if constexpr (kPiece == 4) {
+        *reinterpret_cast<float4*>(p + col * 4) =
+            make_float4(to_f<DT>(v[i].e[0]), to_f<DT>(v[i].e[1]), to_f<DT>(v[i].e[2]), to_f<DT>(v[i].e[3]));
+      } else {
+        const uint4 x = __builtin_bit_cast(uint4, v[i]);
+        if constexpr (DEPTH) {
+          char* o = p + (col & ~31) * 2 + (col & 8) * 4 + (col & 16) / 2;
+          *reinterpret_cast<uint2*>(o) = make_uint2(x.x, x.y);
+          *reinterpret_cast<uint2*>(o + 16) = make_uint2(x.z, x.w);
+        } else {
+          *reinterpret_cast<uint4*>(p + col * 2) = x;
+        }
+      }
+    }
+  }
+
+  // The operand whose rows (or columns) are this tile's rows 16 i + (lane & 15), depth block kb.
+  static __device__ __forceinline__ typename M::Frag along(const char* lds, int i, int kb) {
+    const int lane = threadIdx.x & 63;
+    return *reinterpret_cast<const typename M::Frag*>(lds + (16 * i + (lane & 15)) * kStride + kb * 64 + (lane >> 4) * 16);
+  }
+
+  // The operand whose rows (or columns) are this tile's channels 16 j + (lane & 15) and
+  // whose depth is its positions, block kb.  bf16: the LDS read that transposes.
+  template <bool DEPTH>
+  static __device__ __forceinline__ typename M::Frag across(const char* lds, int j, int kb) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    if constexpr (kPiece == 4) {
+      const float* p = reinterpret_cast<const float*>(lds + (16 * kb + 4 * g) * kStride) + 16 * j + c;
+      constexpr int s = kStride / 4;
+      return make_float4(p[0], p[s], p[2 * s], p[3 * s]);
+    } else {
+      typedef short v4s __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4s lds_v4s;
+      const int col = DEPTH ? (j >> 1) * 32 + (c & 3) * 8 + (j & 1) * 4 : 16 * j + (c & 3) * 4;
+      const char* p = lds + (32 * kb + 4 * g + (c >> 2)) * kStride + col * 2;
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 16 * kStride));
+      const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
+      return make_uint4(x.x, x.y, y.x, y.y);
+    }
+  }
+};
+
+// The chunk of a pass's kernels, LDS and occupancy.
+template <int DT, int DKT, int NT>
+struct ChunkShape {
+  using M = Mma<DT>;
+  static constexpr int kChunk = sizeof(typename M::T) == 4 && DKT == 16 ? 32 : 64;
+  static constexpr int kTiles = kChunk / 16;                  // of 16 positions
+  static constexpr int kDepth = DKT * 16 / M::kDeep;          // blocks of a state's rows
+  static constexpr int kBlocks = kChunk / M::kDeep;           // blocks of positions
+  static constexpr int kPerBlock = M::kDeep / 16;             // 16-row tiles of a block
+  using KTile = Rows2D<DT, DKT * 16, kChunk>;                 // q and k
+  using VTile = Rows2D<DT, NT * 64, kChunk>;
+  using PTile = Rows2D<DT, kChunk, kChunk>;
+  static constexpr int kLds = 2 * KTile::kBytes + VTile::kBytes + PTile::kBytes;
+  static constexpr int kOccupancy = kLds <= 80 * 1024 && DKT <= 8 ? 2 : 1;
+};
+
+template <int DT>
+struct Passes {
+  Pass<DT> p[3];
+};
+
+// LOCAL: the state that a run of chunks leaves from a zero state (the first run: from
+// the initial one), for all runs but the last.  Otherwise y and the final state.
+template <int DT, int DKT, int NT, bool LOCAL>
+__global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la_chunk_kernel(Passes<DT> passes,
+                                                                                            LaGeo g) {
+  using Sh = ChunkShape<DT, DKT, NT>;
+  using M = typename Sh::M;
+  using Frag = typename M::Frag;
+  using KTile = typename Sh::KTile;
+  using VTile = typename Sh::VTile;
+  using PTile = typename Sh::PTile;
+  constexpr int CH = Sh::kChunk, MT = Sh::kTiles, PE = M::kPiece, PB = Sh::kPerBlock;
+  __shared__ __attribute__((aligned(16))) char lds[LOCAL ? KTile::kBytes + VTile::kBytes : Sh::kLds];
+  char* const lds_k = lds;
+  char* const lds_v = lds + KTile::kBytes;
+  char* const lds_q = lds_v + VTile::kBytes;
+  char* const lds_p = lds_q + KTile::kBytes;
+
+  const Pass<DT>& p = passes.p[blockIdx.y];
+  const int lane = threadIdx.x & 63, c = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t parts = (p.dv + 64 * NT - 1) / (64 * NT);  // workgroups along the state's columns
+  const int32_t part = int32_t(blockIdx.x % unsigned(parts));
+  const int64_t row = blockIdx.x / unsigned(parts);
+  const int32_t runs = LOCAL ? g.runs - 1 : g.runs;
+  const int64_t nh = row / runs;
+  const int32_t run = int32_t(row - nh * runs);  // in the order that the pass goes through them
+  const int64_t n = nh / g.h, hd = nh - n * g.h;
+  const int32_t len = valid_len(g.lengths, n, g.l);
+  const float gd = rate(g.log_decay[hd]);
+  const bool back = p.back;
+
+  const int32_t at = back ? g.runs - 1 - run : run;
+  const int32_t chunk_lo = at * g.run;
+  const int32_t chunk_hi = chunk_lo + g.run < g.chunks ? chunk_lo + g.run : g.chunks;
+  const int32_t count = chunk_hi - chunk_lo;
+  const int32_t col0 = part * 64 * NT;                // first column of the workgroup, and
+  const int32_t j0 = col0 + wave * 16 * NT;           // of the wavefront
+
+  // ---- the state: rows 16 a + 4 g + r, column j0 + 16 b + c
+  v4f s[DKT][NT];
+  float4* const kept = p.kept + ((nh * (g.runs - 1) * parts + part) * 4 + wave) * (DKT * NT * 64) + lane;
+  const int64_t kept_step = int64_t(parts) * 4 * (DKT * NT * 64);  // to the next run's
+  if (!LOCAL && run > 0) {
+#pragma unroll
+    for (int a = 0; a < DKT; ++a)
+#pragma unroll
+      for (int b = 0; b < NT; ++b) s[a][b] = __builtin_bit_cast(v4f, kept[(run - 1) * kept_step + (a * NT + b) * 64]);
+  } else {
+    const float* st = p.state && run == 0 ? p.state + nh * p.dk * p.dv : nullptr;
+#pragma unroll
+    for (int a = 0; a < DKT; ++a)
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int32_t i = 16 * a + 4 * g4 + r, j = j0 + 16 * b + c;
+          s[a][b][r] = st && i < p.dk && j < p.dv ? st[i * p.state_k + j * p.state_v] : 0.0f;
+        }
+  }
+
+  // ---- decays within a chunk
+  float between[LOCAL ? 1 : MT][4];  // of the wavefront's tile of q.k: positions 16 i + 4 g + r, for 16 wave + c
+  if constexpr (!LOCAL) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int far = 16 * wave + c - (16 * i + 4 * g4 + r), d = back ? -far : far;
+        between[i][r] = d >= 0 ? exp_full(gd * float(d)) * p.scale_k : 0.0f;
+      }
+  }
+  int32_t known = -1;  // the number of valid positions that these are for:
+  float from_start[LOCAL ? 1 : MT];           // from the entering state to position 16 m + c
+  float to_end[Sh::kBlocks][PE];              // from a position to the end, times scale_k
+  Decay whole(0.0f);
+  auto decays = [&](int32_t valid) {
+    known = valid;
+#pragma unroll
+    for (int kb = 0; kb < Sh::kBlocks; ++kb)
+#pragma unroll
+      for (int e = 0; e < PE; ++e) {
+        const int t = kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4;
+        const int d = back ? t + 1 : valid - 1 - t;
+        to_end[kb][e] = exp_full(gd * float(d < 0 ? 0 : d)) * p.scale_k;
+      }
+    if constexpr (!LOCAL) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int d = back ? valid - 1 - (16 * m + c) : 16 * m + c + 1;
+        from_start[m] = exp_full(gd * float(d < 0 ? 0 : d));
+      }
+    }
+    whole = Decay(gd * float(valid));
+  };
+
+  const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
+  const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
+  const Elem<DT>* const vn = p.v + n * p.vs[0] + hd * p.vs[2] + col0;
+  auto chunk_at = [&](int32_t i) { return back ? chunk_hi - 1 - i : chunk_lo + i; };
+  auto valid_at = [&](int32_t i) {
+    const int32_t v = len - chunk_at(i) * CH;
+    return v < 0 ? 0 : v > CH ? CH : v;
+  };
+  KTile tk, tq;
+  VTile tv;
+  auto fetch = [&](int32_t i) {
+    const int32_t valid = valid_at(i);
+    const int64_t t0 = int64_t(chunk_at(i)) * CH;
+    tk.load(kn + t0 * p.ks[1], p.ks[1], p.dk, valid, p.vec_k);
+    tv.load(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid, p.vec_v);
+    if constexpr (!LOCAL) tq.load(qn + t0 * p.qs[1], p.qs[1], p.dk, valid, p.vec_q);
+  };
+  if (count > 0) fetch(0);
+
+  for (int32_t step = 0; step < count; ++step) {
+    const int32_t valid = valid_at(step);
+    const int32_t t0 = chunk_at(step) * CH;
+    if (valid == 0) {  // all of it past the sequence's end: the state stands still
+      if constexpr (!LOCAL) {
+        const int32_t rows = g.l - t0 < CH ? g.l - t0 : CH, wide = p.dv - col0 < 64 * NT ? p.dv - col0 : 64 * NT;
+        for (int32_t e = threadIdx.x; e < rows * wide; e += 256)
+          p.y[((n * g.l + t0 + e / wide) * g.h + hd) * p.dv + col0 + e % wide] = Elem<DT>(0);
+      }
+      if (step + 1 < count) fetch(step + 1);
+      continue;
+    }
+    if (valid != known) decays(valid);
+    __syncthreads();  // the chunk before has been read
+    tk.template store<true>(lds_k);
+    tv.template store<false>(lds_v);
+    if constexpr (!LOCAL) tq.template store<true>(lds_q);
+    __syncthreads();
+    if (step + 1 < count) fetch(step + 1);
+
+    v4f o[LOCAL ? 1 : MT][NT];
+    if constexpr (!LOCAL) {
+      // ---- (q k^T)^T under its decays: this wavefront's 16 columns of q, to LDS as rows
+      if (wave < MT) {
+#pragma unroll
+        for (int b = 0; b < Sh::kBlocks; ++b) {
+          const bool any = back ? b >= wave / PB : b <= wave / PB;
+          if (!any) continue;
+          float x[PE];
+#pragma unroll
+          for (int i = 0; i < PB; ++i) {
+            const int tile = b * PB + i;
+            v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (back ? tile >= wave : tile <= wave) {
+#pragma unroll
+              for (int kb = 0; kb < Sh::kDepth; ++kb)
+                M::mul(KTile::along(lds_k, tile, kb), KTile::along(lds_q, wave, kb), acc);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[4 * i + r] = acc[r] * between[tile][r];
+          }
+          Frag f[1];
+          split<DT>(x, f);
+          *reinterpret_cast<Frag*>(lds_p + (16 * wave + c) * PTile::kStride + b * 64 + g4 * 16) = f[0];
+        }
+      }
+      // ---- S^T q^T, decayed from the chunk's start
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) o[m][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = 0; kb < Sh::kDepth; ++kb) {
+        Frag st[NT][1];
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+          float x[PE];
+#pragma unroll
+          for (int e = 0; e < PE; ++e) x[e] = s[kb * PB + e / 4][b][e % 4];
+          split<DT>(x, st[b]);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const Frag f = KTile::along(lds_q, m, kb);
+#pragma unroll
+          for (int b = 0; b < NT; ++b) M::mul(st[b][0], f, o[m][b]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) o[m][b] *= from_start[m];
+      __syncthreads();  // the products of q and k are there
+    }
+
+    Frag vf[Sh::kBlocks][NT];
+#pragma unroll
+    for (int kb = 0; kb < Sh::kBlocks; ++kb)
+#pragma unroll
+      for (int b = 0; b < NT; ++b) vf[kb][b] = VTile::template across<false>(lds_v, wave * NT + b, kb);
+
+    if constexpr (!LOCAL) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int kb = 0; kb < Sh::kBlocks; ++kb) {
+          if (back ? kb < m / PB : kb > m / PB) continue;
+          const Frag f = PTile::along(lds_p, m, kb);
+#pragma unroll
+          for (int b = 0; b < NT; ++b) M::mul(vf[kb][b], f, o[m][b]);
+        }
+      // ---- y: a lane has channels j0 + 16 b + 4 g ... of position 16 m + c
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int32_t t = t0 + 16 * m + c;
+        if (t >= g.l) continue;
+        Elem<DT>* y = p.y + ((n * g.l + t) * g.h + hd) * p.dv;
+        const bool live = t < len;
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+          const int32_t j = j0 + 16 * b + 4 * g4;
+          Pack<DT, 4> out;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) out.e[r] = from_f<DT>(live ? o[m][b][r] * p.scale_y : 0.0f);
+          if (p.vec_y) {
+            if (j < p.dv) store_pack<DT, 4>(y + j, out);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (j + r < p.dv) y[j + r] = out.e[r];
+          }
+        }
+      }
+    }
+
+    // ---- S <- decay S + k^T (decayed v)
+#pragma unroll
+    for (int a = 0; a < DKT; ++a)
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[a][b][r] = whole(s[a][b][r]);
+#pragma unroll
+    for (int kb = 0; kb < Sh::kBlocks; ++kb) {
+      Frag vt[NT][M::kTerms];
+#pragma unroll
+      for (int b = 0; b < NT; ++b) {
+        float x[PE];
+        if constexpr (PE == 4) {
+          const float4 f = vf[kb][b];
+          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        } else {
+          const uint4 f = vf[kb][b];
+          const uint32_t u[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < PE; ++e) x[e] *= to_end[kb][e];
+        split<DT>(x, vt[b]);
+      }
+#pragma unroll
+      for (int a = 0; a < DKT; ++a) {
+        const Frag f = KTile::template across<true>(lds_k, a, kb);
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int t = 0; t < M::kTerms; ++t) M::mul(f, vt[b][t], s[a][b]);
+      }
+    }
+  }
+
+  if constexpr (LOCAL) {
+#pragma unroll
+    for (int a = 0; a < DKT; ++a)
+#pragma unroll
+      for (int b = 0; b < NT; ++b) kept[run * kept_step + (a * NT + b) * 64] = __builtin_bit_cast(float4, s[a][b]);
+  } else if (p.state_out && run == g.runs - 1) {
+    float* st = p.state_out + nh * p.dk * p.dv;
+#pragma unroll
+    for (int a = 0; a < DKT; ++a)
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int32_t i = 16 * a + 4 * g4 + r, j = j0 + 16 * b + c;
+          if (i < p.dk && j < p.dv) st[i * p.state_k + j * p.state_v] = s[a][b][r];
+        }
+  }
+}
+
+// Along the runs, in place: what each leaves from a zero state -> the state that
+// enters the next one.  `per` float4 of every head and run.
+template <int DT>
+__global__ __launch_bounds__(256) void la_join_kernel(Passes<DT> passes, LaGeo g, int64_t heads, int32_t per,
+                                                      int32_t chunk) {
+  const Pass<DT>& p = passes.p[blockIdx.y];
+  const int32_t slots = g.runs - 1;
+  const int64_t total = heads * per;
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+    const int64_t nh = id / per;
+    const int64_t n = nh / g.h, hd = nh - n * g.h;
+    const int32_t len = valid_len(g.lengths, n, g.l);
+    const float gd = rate(g.log_decay[hd]);
+    float4* at = p.kept + nh * slots * per + (id - nh * per);
+    constexpr int kAhead = 8;
+    float4 h = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int32_t k0 = 0; k0 < slots; k0 += kAhead) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (k0 + i < slots) v[i] = at[int64_t(k0 + i) * per];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (k0 + i >= slots) break;
+        const int32_t run = p.back ? g.runs - 1 - (k0 + i) : k0 + i;
+        const int32_t lo = run * g.run * chunk, hi = (run + 1 == g.runs ? g.chunks : (run + 1) * g.run) * chunk;
+        const int32_t valid = (hi < len ? hi : len) - lo;
+        const Decay d(gd * float(valid < 0 ? 0 : valid));
+        h.x = d(h.x) + v[i].x, h.y = d(h.y) + v[i].y, h.z = d(h.z) + v[i].z, h.w = d(h.w) + v[i].w;
+        at[int64_t(k0 + i) * per] = h;
+      }
+    }
+  }
+}
+
+}  // namespace seq
+}  // namespace cnhwc
