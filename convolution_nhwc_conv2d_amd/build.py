@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libcnhwc.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["select.cpp", "api.cpp", "gemm.hip", "gemm_lds.hip", "wino_gemm.hip", "winograd.hip", "winograd_h.hip",
            "unfold.hip", "noalloc.hip", "gemm_patch.hip", "layer_norm.hip", "causal_conv.hip", "scan.hip",
-           "rms_norm.hip", "rotary.hip", "linear_attention.hip"]
+           "rms_norm.hip", "rotary.hip", "linear_attention.hip", "linear_attention_f32.hip", "linear_attention_f16.hip",
+           "linear_attention_bf16.hip"]
 EXT = os.path.join(PKG, "_seq.so")
 EXT_SOURCE = "seq_torch.cpp"
 TORCH = importlib.util.find_spec("torch").submodule_search_locations[0]

@@ -10,7 +10,7 @@
 #include <hip/hip_runtime.h>
 
 #include "internal.hpp"
-#include "linear_attention.hpp"
+#include "linear_attention_host.hpp"
 #include "seq_common.hpp"
 #include "seq_host.hpp"
 
@@ -174,82 +174,6 @@ void launch_step(const Pass<DT>& p, const LaGeo& g, int64_t nh, hipStream_t st) 
     if (p.dv % 4 == 0) hipLaunchKernelGGL((la_step_kernel<DT, NI, true>), grid, dim3(256), 0, st, p, g);
     else hipLaunchKernelGGL((la_step_kernel<DT, NI, false>), grid, dim3(256), 0, st, p, g);
   });
-}
-
-// The form of a pass: 16-row tiles of a state, 64-column parts of a workgroup (1 or 2).
-template <typename F>
-void with_shape(int32_t dk, int32_t dv, F&& f) {
-  auto wide = [&](auto dkt) {
-    if (dv <= 64) f(dkt, std::integral_constant<int, 1>{});
-    else f(dkt, std::integral_constant<int, 2>{});
-  };
-  if (dk <= 32) wide(std::integral_constant<int, 2>{});
-  else if (dk <= 64) wide(std::integral_constant<int, 4>{});
-  else if (dk <= 128) wide(std::integral_constant<int, 8>{});
-  else wide(std::integral_constant<int, 16>{});
-}
-
-// How a pass is cut: its chunk, the workgroups along a state's columns, the runs of
-// chunks, and the bytes of the states between them.  A function of the sizes alone.
-struct Cut {
-  int32_t chunk, parts, chunks, run, runs;
-  int32_t per;     // float4 of a head's state in lane order
-  uint64_t bytes;
-};
-template <int DT>
-Cut cut_of(const Desc& d, int32_t dk, int32_t dv, int64_t passes) {
-  Cut c{};
-  with_shape(dk, dv, [&](auto dkt, auto nt) {
-    constexpr int DKT = decltype(dkt)::value, NT = decltype(nt)::value;
-    using Sh = ChunkShape<DT, DKT, NT>;
-    c.chunk = Sh::kChunk;
-    c.parts = (dv + 64 * NT - 1) / (64 * NT);
-    c.per = c.parts * 4 * DKT * NT * 64;
-    c.chunks = int32_t((d.l + c.chunk - 1) / c.chunk);
-    const int64_t all = d.n * d.h * c.parts * passes, room = 256 * Sh::kOccupancy;
-    int64_t runs = all * 2 > room ? 1 : room / all;
-    if (runs > c.chunks / 4) runs = c.chunks / 4;
-    if (runs < 1) runs = 1;
-    c.run = int32_t((c.chunks + runs - 1) / runs);
-    c.runs = (c.chunks + c.run - 1) / c.run;
-  });
-  c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16;
-  return c;
-}
-
-bool whole(const void* p, const int64_t (&s)[3], int32_t c, int64_t piece, uint64_t es) {
-  return aligned(p, piece * es) && c % piece == 0 && s[0] % piece == 0 && s[1] % piece == 0 && s[2] % piece == 0;
-}
-
-// One or several passes of the same form.
-template <int DT>
-hipError_t launch_passes(Passes<DT>& ps, int count, LaGeo g, const Cut& c, int64_t heads, char* workspace,
-                         hipStream_t st) {
-  const uint64_t es = sizeof(Elem<DT>);
-  constexpr int kPiece = Mma<DT>::kPiece;
-  g.chunks = c.chunks, g.run = c.run, g.runs = c.runs;
-  for (int i = 0; i < count; ++i) {
-    Pass<DT>& p = ps.p[i];
-    p.vec_q = whole(p.q, p.qs, p.dk, kPiece, es);
-    p.vec_k = whole(p.k, p.ks, p.dk, kPiece, es);
-    p.vec_v = whole(p.v, p.vs, p.dv, kPiece, es);
-    p.vec_y = aligned(p.y, 4 * es) && p.dv % 4 == 0;
-    p.kept = reinterpret_cast<float4*>(workspace + i * c.bytes);
-  }
-  with_shape(ps.p[0].dk, ps.p[0].dv, [&](auto dkt, auto nt) {
-    constexpr int DKT = decltype(dkt)::value, NT = decltype(nt)::value;
-    const int64_t blocks = heads * c.parts;
-    if (c.runs > 1) {
-      hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, NT, true>), dim3(unsigned(blocks * (c.runs - 1)), count), dim3(256),
-                         0, st, ps, g);
-      const int64_t total = heads * c.per;
-      hipLaunchKernelGGL((la_join_kernel<DT>), dim3(grid_of(ceil_div(total, int64_t(256))).x, count), dim3(256), 0, st,
-                         ps, g, heads, c.per, c.chunk);
-    }
-    hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, NT, false>), dim3(unsigned(blocks * c.runs), count), dim3(256), 0, st,
-                       ps, g);
-  });
-  return hipGetLastError();
 }
 
 template <int DT>

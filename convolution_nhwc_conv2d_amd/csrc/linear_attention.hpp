@@ -41,7 +41,6 @@ struct Pass {
   int32_t dk, dv;
   bool back;               // positions from the end, the state decays after its use
   float scale_k, scale_y;  // of what enters the state, of what leaves it
-  bool vec_q, vec_k, vec_v, vec_y;  // whole vectors to load and store
   float4* kept;            // the states that enter all runs of chunks but the first, in lane order
 };
 
@@ -139,15 +138,16 @@ struct Rows2D {
   Pack<DT, kPiece> v[kCount];
 
   // rows past `valid` and channels past `cols` are 0 and not read
-  __device__ __forceinline__ void load(const Elem<DT>* __restrict__ base, int64_t stride, int32_t cols, int32_t valid,
-                                       bool vec) {
+  template <bool VEC>
+  __device__ __forceinline__ void load(const Elem<DT>* __restrict__ base, int64_t stride, int32_t cols,
+                                       int32_t valid) {
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
       const int id = int(threadIdx.x) + 256 * i, row = id / kPer, col = id % kPer * kPiece;
       Pack<DT, kPiece> x{};
       if (row < valid && col < cols) {
         const Elem<DT>* p = base + row * stride + col;
-        if (vec) {
+        if constexpr (VEC) {
           x = load_pack<DT, kPiece>(p);
         } else {
 #pragma unroll
@@ -232,7 +232,7 @@ struct Passes {
 
 // LOCAL: the state that a run of chunks leaves from a zero state (the first run: from
 // the initial one), for all runs but the last.  Otherwise y and the final state.
-template <int DT, int DKT, int NT, bool LOCAL>
+template <int DT, int DKT, int NT, bool LOCAL, bool VEC>
 __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la_chunk_kernel(Passes<DT> passes,
                                                                                             LaGeo g) {
   using Sh = ChunkShape<DT, DKT, NT>;
@@ -243,6 +243,7 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
   using PTile = typename Sh::PTile;
   constexpr int CH = Sh::kChunk, MT = Sh::kTiles, PE = M::kPiece, PB = Sh::kPerBlock;
   __shared__ __attribute__((aligned(16))) char lds[LOCAL ? KTile::kBytes + VTile::kBytes : Sh::kLds];
+  __shared__ float power[CH + 1], power_k[CH + 1];
   char* const lds_k = lds;
   char* const lds_v = lds + KTile::kBytes;
   char* const lds_q = lds_v + VTile::kBytes;
@@ -263,8 +264,10 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
   const bool back = p.back;
 
   const int32_t at = back ? g.runs - 1 - run : run;
-  const int32_t chunk_lo = at * g.run;
-  const int32_t chunk_hi = chunk_lo + g.run < g.chunks ? chunk_lo + g.run : g.chunks;
+  // the run's chunks with valid positions; past them the state stands still
+  const int32_t chunk_lo = at * g.run, all_hi = chunk_lo + g.run < g.chunks ? chunk_lo + g.run : g.chunks;
+  const int32_t used = (len + CH - 1) / CH;
+  const int32_t chunk_hi = used < chunk_lo ? chunk_lo : used < all_hi ? used : all_hi;
   const int32_t count = chunk_hi - chunk_lo;
   const int32_t col0 = part * 64 * NT;                // first column of the workgroup, and
   const int32_t j0 = col0 + wave * 16 * NT;           // of the wavefront
@@ -291,40 +294,14 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
         }
   }
 
-  // ---- decays within a chunk
-  float between[LOCAL ? 1 : MT][4];  // of the wavefront's tile of q.k: positions 16 i + 4 g + r, for 16 wave + c
-  if constexpr (!LOCAL) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int far = 16 * wave + c - (16 * i + 4 * g4 + r), d = back ? -far : far;
-        between[i][r] = d >= 0 ? exp_full(gd * float(d)) * p.scale_k : 0.0f;
-      }
+  // ---- decays over up to a chunk: exp(g d), and times scale_k.  Held in registers
+  // (36 of them) they would cost the second workgroup of a compute unit its place.
+  if (threadIdx.x <= CH) {
+    const float d = exp_full(gd * float(int(threadIdx.x)));
+    power[threadIdx.x] = d;
+    power_k[threadIdx.x] = d * p.scale_k;
   }
-  int32_t known = -1;  // the number of valid positions that these are for:
-  float from_start[LOCAL ? 1 : MT];           // from the entering state to position 16 m + c
-  float to_end[Sh::kBlocks][PE];              // from a position to the end, times scale_k
-  Decay whole(0.0f);
-  auto decays = [&](int32_t valid) {
-    known = valid;
-#pragma unroll
-    for (int kb = 0; kb < Sh::kBlocks; ++kb)
-#pragma unroll
-      for (int e = 0; e < PE; ++e) {
-        const int t = kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4;
-        const int d = back ? t + 1 : valid - 1 - t;
-        to_end[kb][e] = exp_full(gd * float(d < 0 ? 0 : d)) * p.scale_k;
-      }
-    if constexpr (!LOCAL) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int d = back ? valid - 1 - (16 * m + c) : 16 * m + c + 1;
-        from_start[m] = exp_full(gd * float(d < 0 ? 0 : d));
-      }
-    }
-    whole = Decay(gd * float(valid));
-  };
+  const Decay full(gd * float(CH));
 
   const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
@@ -332,32 +309,28 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
   auto chunk_at = [&](int32_t i) { return back ? chunk_hi - 1 - i : chunk_lo + i; };
   auto valid_at = [&](int32_t i) {
     const int32_t v = len - chunk_at(i) * CH;
-    return v < 0 ? 0 : v > CH ? CH : v;
+    return v > CH ? CH : v;
   };
   KTile tk, tq;
   VTile tv;
   auto fetch = [&](int32_t i) {
     const int32_t valid = valid_at(i);
     const int64_t t0 = int64_t(chunk_at(i)) * CH;
-    tk.load(kn + t0 * p.ks[1], p.ks[1], p.dk, valid, p.vec_k);
-    tv.load(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid, p.vec_v);
-    if constexpr (!LOCAL) tq.load(qn + t0 * p.qs[1], p.qs[1], p.dk, valid, p.vec_q);
+    tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid);
+    tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid);
+    if constexpr (!LOCAL) tq.template load<VEC>(qn + t0 * p.qs[1], p.qs[1], p.dk, valid);
   };
   if (count > 0) fetch(0);
+  if constexpr (!LOCAL) {
+    const int64_t first = int64_t(chunk_hi) * CH, last = int64_t(all_hi) * CH < g.l ? int64_t(all_hi) * CH : g.l;
+    const int32_t wide = p.dv - col0 < 64 * NT ? p.dv - col0 : 64 * NT;
+    for (int64_t e = threadIdx.x; e < (last - first) * wide; e += 256)
+      p.y[((n * g.l + first + e / wide) * g.h + hd) * p.dv + col0 + e % wide] = Elem<DT>(0);
+  }
 
   for (int32_t step = 0; step < count; ++step) {
     const int32_t valid = valid_at(step);
     const int32_t t0 = chunk_at(step) * CH;
-    if (valid == 0) {  // all of it past the sequence's end: the state stands still
-      if constexpr (!LOCAL) {
-        const int32_t rows = g.l - t0 < CH ? g.l - t0 : CH, wide = p.dv - col0 < 64 * NT ? p.dv - col0 : 64 * NT;
-        for (int32_t e = threadIdx.x; e < rows * wide; e += 256)
-          p.y[((n * g.l + t0 + e / wide) * g.h + hd) * p.dv + col0 + e % wide] = Elem<DT>(0);
-      }
-      if (step + 1 < count) fetch(step + 1);
-      continue;
-    }
-    if (valid != known) decays(valid);
     __syncthreads();  // the chunk before has been read
     tk.template store<true>(lds_k);
     tv.template store<false>(lds_v);
@@ -384,7 +357,10 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
                 M::mul(KTile::along(lds_k, tile, kb), KTile::along(lds_q, wave, kb), acc);
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[4 * i + r] = acc[r] * between[tile][r];
+              for (int r = 0; r < 4; ++r) {
+              const int far = 16 * wave + c - (16 * tile + 4 * g4 + r), d = back ? -far : far;
+              x[4 * i + r] = d < 0 ? 0.0f : acc[r] * power_k[d < 0 ? 0 : d];
+            }
           }
           Frag f[1];
           split<DT>(x, f);
@@ -414,9 +390,12 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
         }
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
+        const int d = back ? valid - 1 - (16 * m + c) : 16 * m + c + 1;
+        const float from_start = power[d < 0 ? 0 : d];
 #pragma unroll
-        for (int b = 0; b < NT; ++b) o[m][b] *= from_start[m];
+        for (int b = 0; b < NT; ++b) o[m][b] *= from_start;
+      }
       __syncthreads();  // the products of q and k are there
     }
 
@@ -449,7 +428,7 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
           Pack<DT, 4> out;
 #pragma unroll
           for (int r = 0; r < 4; ++r) out.e[r] = from_f<DT>(live ? o[m][b][r] * p.scale_y : 0.0f);
-          if (p.vec_y) {
+          if constexpr (VEC) {
             if (j < p.dv) store_pack<DT, 4>(y + j, out);
           } else {
 #pragma unroll
@@ -461,6 +440,7 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
     }
 
     // ---- S <- decay S + k^T (decayed v)
+    const Decay whole = valid == CH ? full : Decay(gd * float(valid));
 #pragma unroll
     for (int a = 0; a < DKT; ++a)
 #pragma unroll
@@ -469,6 +449,12 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
         for (int r = 0; r < 4; ++r) s[a][b][r] = whole(s[a][b][r]);
 #pragma unroll
     for (int kb = 0; kb < Sh::kBlocks; ++kb) {
+      float to_end[PE];
+#pragma unroll
+      for (int e = 0; e < PE; ++e) {
+        const int t = kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4, d = back ? t + 1 : valid - 1 - t;
+        to_end[e] = power_k[d < 0 ? 0 : d];
+      }
       Frag vt[NT][M::kTerms];
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
@@ -483,7 +469,7 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
           for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
         }
 #pragma unroll
-        for (int e = 0; e < PE; ++e) x[e] *= to_end[kb][e];
+        for (int e = 0; e < PE; ++e) x[e] *= to_end[e];
         split<DT>(x, vt[b]);
       }
 #pragma unroll

@@ -1,0 +1,10 @@
+// Linear attention's chunk kernels for f16.
+#include "linear_attention_launch.hpp"
+
+namespace cnhwc {
+namespace seq {
+
+template hipError_t launch_passes<CNHWC_F16>(Passes<CNHWC_F16>&, int, LaGeo, const Cut&, int64_t, char*, hipStream_t);
+
+}  // namespace seq
+}  // namespace cnhwc

@@ -1,0 +1,61 @@
+// Linear attention's passes on the host: how they are cut, and their launches.
+#pragma once
+#include "internal.hpp"
+#include "linear_attention.hpp"
+#include "seq_host.hpp"
+
+namespace cnhwc {
+namespace seq {
+
+// The form of a pass: 16-row tiles of a state, 64-column parts of a workgroup (1 or 2).
+template <typename F>
+void with_shape(int32_t dk, int32_t dv, F&& f) {
+  auto wide = [&](auto dkt) {
+    if (dv <= 64) f(dkt, std::integral_constant<int, 1>{});
+    else f(dkt, std::integral_constant<int, 2>{});
+  };
+  if (dk <= 32) wide(std::integral_constant<int, 2>{});
+  else if (dk <= 64) wide(std::integral_constant<int, 4>{});
+  else if (dk <= 128) wide(std::integral_constant<int, 8>{});
+  else wide(std::integral_constant<int, 16>{});
+}
+
+// How a pass is cut: its chunk, the workgroups along a state's columns, the runs of
+// chunks, and the bytes of the states between them.  A function of the sizes alone.
+struct Cut {
+  int32_t chunk, parts, chunks, run, runs;
+  int32_t per;     // float4 of a head's state in lane order
+  uint64_t bytes;
+};
+template <int DT>
+Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64_t passes) {
+  Cut c{};
+  with_shape(dk, dv, [&](auto dkt, auto nt) {
+    constexpr int DKT = decltype(dkt)::value, NT = decltype(nt)::value;
+    using Sh = ChunkShape<DT, DKT, NT>;
+    c.chunk = Sh::kChunk;
+    c.parts = (dv + 64 * NT - 1) / (64 * NT);
+    c.per = c.parts * 4 * DKT * NT * 64;
+    c.chunks = int32_t((d.l + c.chunk - 1) / c.chunk);
+    const int64_t all = d.n * d.h * c.parts * passes, room = 256 * Sh::kOccupancy;
+    int64_t runs = all * 2 > room ? 1 : room / all;
+    if (runs > c.chunks / 4) runs = c.chunks / 4;
+    if (runs < 1) runs = 1;
+    c.run = int32_t((c.chunks + runs - 1) / runs);
+    c.runs = (c.chunks + c.run - 1) / c.run;
+  });
+  c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16;
+  return c;
+}
+
+inline bool whole(const void* p, const int64_t (&s)[3], int32_t c, int64_t piece, uint64_t es) {
+  return aligned(p, piece * es) && c % piece == 0 && s[0] % piece == 0 && s[1] % piece == 0 && s[2] % piece == 0;
+}
+
+// One or several passes of the same form; each type's kernels are in a source of their own.
+template <int DT>
+hipError_t launch_passes(Passes<DT>& ps, int count, LaGeo g, const Cut& c, int64_t heads, char* workspace,
+                         hipStream_t st);
+
+}  // namespace seq
+}  // namespace cnhwc
