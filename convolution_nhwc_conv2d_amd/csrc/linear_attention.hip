@@ -86,77 +86,17 @@ __global__ __launch_bounds__(256) void la_step_kernel(Pass<DT> p, LaGeo g) {
   }
 }
 
-// The gradient of log_decay: with T[t] = exp(g) (T[t-1] + S[t-1]), the state's
-// derivative, sum_t scale dy[t] q[t] T[t] + dstate T[L].  part: one sum for each workgroup.
-template <int DT, int NI>
-__global__ __launch_bounds__(256) void la_decay_grad_kernel(Pass<DT> p, const Elem<DT>* dy, int64_t ds0, int64_t ds1,
-                                                            int64_t ds2, const float* dstate_out, LaGeo g,
-                                                            float* part) {
-  __shared__ float sum[4];
-  const int64_t nh = blockIdx.x;
-  const int64_t n = nh / g.h, hd = nh - n * g.h;
-  const int j0 = int(blockIdx.y) * 64 + int(threadIdx.x & 15) * 4, r0 = threadIdx.x >> 4;
-  const int64_t base = nh * p.dk * p.dv;
-  float s[NI][4], grow[NI][4];
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = r0 + 16 * i, j = j0 + e;
-      s[i][e] = p.state && r < p.dk && j < p.dv ? p.state[base + r * p.state_k + j * p.state_v] : 0.0f;
-      grow[i][e] = 0.0f;
-    }
-  const Decay decay(rate(g.log_decay[hd]));
-  const int32_t len = valid_len(g.lengths, n, g.l);
-  double total = 0.0;
-  for (int32_t t = 0; t < len; ++t) {
-    float acc = 0.0f;
-#pragma unroll
-    for (int a = 0; a < NI; ++a) {
-      const int r = r0 + 16 * a;
-      const float k = r < p.dk ? to_f<DT>(p.k[n * p.ks[0] + t * p.ks[1] + hd * p.ks[2] + r]) : 0.0f;
-      const float q = r < p.dk ? to_f<DT>(p.q[n * p.qs[0] + t * p.qs[1] + hd * p.qs[2] + r]) : 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + e;
-        const float v = j < p.dv ? to_f<DT>(p.v[n * p.vs[0] + t * p.vs[1] + hd * p.vs[2] + j]) : 0.0f;
-        const float d = j < p.dv ? to_f<DT>(dy[n * ds0 + t * ds1 + hd * ds2 + j]) : 0.0f;
-        grow[a][e] = decay(grow[a][e] + s[a][e]);
-        s[a][e] = __builtin_fmaf(k, v, decay(s[a][e]));
-        acc = __builtin_fmaf(q * d, grow[a][e], acc);
-      }
-    }
-    total += double(acc);
-  }
-  total *= p.scale_y;
-  if (dstate_out) {
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = r0 + 16 * i, j = j0 + e;
-        if (r < p.dk && j < p.dv) total += double(dstate_out[base + int64_t(r) * p.dv + j] * grow[i][e]);
-      }
-  }
-  const float one = group_sum<64>(float(total));
-  if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = one;
-  __syncthreads();
-  if (threadIdx.x == 0) part[nh * gridDim.y + blockIdx.y] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-}
-
-__global__ __launch_bounds__(256) void la_decay_sum_kernel(const float* __restrict__ part, float* __restrict__ out,
-                                                           int64_t seqs, int32_t heads, int32_t blocks) {
-  const int64_t h = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (h >= heads) return;
-  double v = 0.0;
-  for (int64_t n = 0; n < seqs; ++n)
-    for (int32_t b = 0; b < blocks; ++b) v += double(part[(n * heads + h) * blocks + b]);
-  out[h] = float(v);
-}
-
 // ---------------------------------------------------------------- host
 
 using Desc = cnhwc_linear_attention_desc_t;
+
+// f(the type's constant)
+template <typename F>
+auto with_type(const Desc& d, F&& f) {
+  if (d.dtype == CNHWC_F32) return f(std::integral_constant<int, CNHWC_F32>{});
+  if (d.dtype == CNHWC_F16) return f(std::integral_constant<int, CNHWC_F16>{});
+  return f(std::integral_constant<int, CNHWC_BF16>{});
+}
 
 template <typename F>
 void with_rows(int32_t dk, F&& f) {  // rows of 16 that a thread holds one of
@@ -275,11 +215,8 @@ void backward_cuts(const Desc& d, Cut& v, Cut& qk) {
 }
 uint64_t backward_bytes(const Desc& d, bool decay_grad) {
   Cut v, qk;
-  if (d.dtype == CNHWC_F32) backward_cuts<CNHWC_F32>(d, v, qk);
-  else if (d.dtype == CNHWC_F16) backward_cuts<CNHWC_F16>(d, v, qk);
-  else backward_cuts<CNHWC_BF16>(d, v, qk);
-  const uint64_t part = decay_grad ? uint64_t(d.n) * d.h * ((d.dv + 63) / 64) * 4 : 0;
-  return v.bytes + 2 * qk.bytes + (part + 15) / 16 * 16;
+  with_type(d, [&](auto dt) { backward_cuts<dt.value>(d, v, qk); });
+  return v.bytes + 2 * qk.bytes + (decay_grad ? with_type(d, [&](auto dt) { return decay_cut_of<dt.value>(d).bytes; }) : 0);
 }
 
 template <int DT>
@@ -306,20 +243,15 @@ hipError_t backward_t(const Desc& d, const cnhwc_linear_attention_inputs_t& in, 
     if (e == hipSuccess) e = launch_passes(pv, 1, g, cv, nh, workspace + 2 * cqk.bytes, st);
   }
   if (e != hipSuccess) return e;
-  float* part = reinterpret_cast<float*>(workspace + cv.bytes + 2 * cqk.bytes);
-  if (gr.log_decay) {
-    Pass<DT> s = pass_of<DT>(in.q, d.q_stride, in.k, d.k_stride, in.v, d.v_stride, nullptr, d.dk, d.dv, d.scale, false);
-    s.state = in.state;
-    const unsigned blocks = unsigned((d.dv + 63) / 64);
-    with_rows(d.dk, [&](auto ni) {
-      hipLaunchKernelGGL((la_decay_grad_kernel<DT, decltype(ni)::value>), dim3(unsigned(nh), blocks), dim3(256), 0, st,
-                         s, static_cast<const Elem<DT>*>(dy), d.dy_stride[0], d.dy_stride[1], d.dy_stride[2],
-                         dstate_out, g, part);
-    });
-    hipLaunchKernelGGL(la_decay_sum_kernel, dim3(unsigned((d.h + 255) / 256)), dim3(256), 0, st, part, gr.log_decay,
-                       d.n, int32_t(d.h), int32_t(blocks));
-  }
-  return hipGetLastError();
+  if (!gr.log_decay) return hipSuccess;
+  DecayPass<DT> t{};
+  t.a = pass_of<DT>(in.q, d.q_stride, in.k, d.k_stride, in.v, d.v_stride, nullptr, d.dk, d.dv, d.scale, false);
+  t.a.state = in.state;
+  t.dy = static_cast<const Elem<DT>*>(dy);
+  for (int i = 0; i < 3; ++i) t.dys[i] = d.dy_stride[i];
+  t.dstate = dstate_out;
+  return launch_decay(t, g, decay_cut_of<DT>(d), nh, workspace + cv.bytes + 2 * cqk.bytes,
+                      gr.log_decay, st);
 }
 
 }  // namespace
@@ -334,9 +266,7 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_fwd_workspace(const Desc* desc,
   if (st != CNHWC_OK) return st;
   if (!bytes) return CNHWC_ERR_INVALID_ARGUMENT;
   const Desc& d = *desc;
-  *bytes = d.dtype == CNHWC_F32   ? cut_of<CNHWC_F32>(d, d.dk, d.dv, 1).bytes
-           : d.dtype == CNHWC_F16 ? cut_of<CNHWC_F16>(d, d.dk, d.dv, 1).bytes
-                                  : cut_of<CNHWC_BF16>(d, d.dk, d.dv, 1).bytes;
+  *bytes = with_type(d, [&](auto dt) { return cut_of<dt.value>(d, d.dk, d.dv, 1).bytes; });
   return CNHWC_OK;
 }
 
@@ -359,9 +289,7 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_fwd(const Desc* desc, const cnh
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   char* ws = static_cast<char*>(workspace);
-  const hipError_t e = d.dtype == CNHWC_F32   ? forward_t<CNHWC_F32>(d, *in, y, state_out, ws, s)
-                       : d.dtype == CNHWC_F16 ? forward_t<CNHWC_F16>(d, *in, y, state_out, ws, s)
-                                              : forward_t<CNHWC_BF16>(d, *in, y, state_out, ws, s);
+  const hipError_t e = with_type(d, [&](auto dt) { return forward_t<dt.value>(d, *in, y, state_out, ws, s); });
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }
 
@@ -401,9 +329,7 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_bwd(const Desc* desc, const cnh
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
   char* ws = static_cast<char*>(workspace);
-  const hipError_t e = d.dtype == CNHWC_F32   ? backward_t<CNHWC_F32>(d, *in, dy, dstate_out, *grads, ws, s)
-                       : d.dtype == CNHWC_F16 ? backward_t<CNHWC_F16>(d, *in, dy, dstate_out, *grads, ws, s)
-                                              : backward_t<CNHWC_BF16>(d, *in, dy, dstate_out, *grads, ws, s);
+  const hipError_t e = with_type(d, [&](auto dt) { return backward_t<dt.value>(d, *in, dy, dstate_out, *grads, ws, s); });
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }
 
@@ -420,8 +346,6 @@ extern "C" cnhwc_status_t cnhwc_linear_attention_step(const Desc* desc, const cn
   bf.out(state_out, uint64_t(d.n) * d.h * d.dk * d.dv * 4, 16, true);
   if (!bf.ok()) return CNHWC_ERR_INVALID_ARGUMENT;
   hipStream_t s = reinterpret_cast<hipStream_t>(hip_stream);
-  const hipError_t e = d.dtype == CNHWC_F32   ? step_t<CNHWC_F32>(d, *in, y, state_out, s)
-                       : d.dtype == CNHWC_F16 ? step_t<CNHWC_F16>(d, *in, y, state_out, s)
-                                              : step_t<CNHWC_BF16>(d, *in, y, state_out, s);
+  const hipError_t e = with_type(d, [&](auto dt) { return step_t<dt.value>(d, *in, y, state_out, s); });
   return e == hipSuccess ? CNHWC_OK : CNHWC_ERR_HIP;
 }

@@ -537,5 +537,280 @@ __global__ __launch_bounds__(256) void la_join_kernel(Passes<DT> passes, LaGeo g
   }
 }
 
+// ---------------------------------------------------------------- the decay's gradient
+//
+// With T[t] = e^g (T[t-1] + S[t-1]), the state's derivative by g, the gradient is
+// sum_t scale dy[t] q[t] T[t] + dstate T[L].  In a chunk that starts from S and T
+//   dy[u] . q[u] T[u] = e^(g (u+1)) dy[u] . q[u] (T + (u+1) S)
+//                       + sum_{s < u} (u-s) e^(g (u-s)) (q[u] . k[s]) (dy[u] . v[s])
+//   T' = e^(g C) (T + C S) + sum_t k[t]^T ((C-1-t) e^(g (C-1-t)) v[t])
+// Every sum here is over what it is about: the shorter form sum_t t (q dq - k dk)
+// would lose the gradient in the difference of sums that grow with the length.  A
+// workgroup holds 64 columns of both states; S, T and the decayed v are taken in all
+// their terms, so nothing is rounded below fp32.
+template <int DT>
+struct DecayPass {
+  Pass<DT> a;               // q, k, v, the initial state; y, state_out unused
+  const Elem<DT>* dy;
+  int64_t dys[3];
+  const float* dstate;      // [DK,DV], or NULL
+  float* sums;              // one for each workgroup
+};
+
+template <int DT, int DKT>
+struct DecayShape {
+  static constexpr int kChunk = ChunkShape<DT, DKT, 1>::kChunk;
+  using KTile = Rows2D<DT, DKT * 16, kChunk>;
+  using VTile = Rows2D<DT, 64, kChunk>;
+  static constexpr int kLds = 2 * KTile::kBytes + 2 * VTile::kBytes;
+  static constexpr int kOccupancy = kLds <= 76 * 1024 && DKT <= 8 ? 2 : 1;
+};
+
+template <int DT, int DKT, bool LOCAL, bool VEC>
+__global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_decay_kernel(DecayPass<DT> pass,
+                                                                                         LaGeo g) {
+  using Sh = DecayShape<DT, DKT>;
+  using M = Mma<DT>;
+  using Frag = typename M::Frag;
+  using KTile = typename Sh::KTile;
+  using VTile = typename Sh::VTile;
+  constexpr int CH = Sh::kChunk, MT = CH / 16, PE = M::kPiece, PB = M::kDeep / 16, TERMS = M::kTerms;
+  constexpr int kBlocks = CH / M::kDeep;
+  __shared__ __attribute__((aligned(16))) char lds[LOCAL ? KTile::kBytes + VTile::kBytes : Sh::kLds];
+  __shared__ float power[CH + 1], red[4];
+  char* const lds_k = lds;
+  char* const lds_v = lds + KTile::kBytes;
+  char* const lds_q = lds_v + VTile::kBytes;
+  char* const lds_d = lds_q + KTile::kBytes;
+
+  const Pass<DT>& p = pass.a;
+  const int lane = threadIdx.x & 63, c = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t parts = (p.dv + 63) / 64, part = int32_t(blockIdx.x % unsigned(parts));
+  const int64_t row = blockIdx.x / unsigned(parts);
+  const int32_t runs = LOCAL ? g.runs - 1 : g.runs;
+  const int64_t nh = row / runs;
+  const int32_t run = int32_t(row - nh * runs);
+  const int64_t n = nh / g.h, hd = nh - n * g.h;
+  const int32_t len = valid_len(g.lengths, n, g.l);
+  const float gd = rate(g.log_decay[hd]);
+  const int32_t chunk_lo = run * g.run, all_hi = chunk_lo + g.run < g.chunks ? chunk_lo + g.run : g.chunks;
+  const int32_t used = (len + CH - 1) / CH;
+  const int32_t chunk_hi = used < chunk_lo ? chunk_lo : used < all_hi ? used : all_hi;
+  const int32_t col0 = part * 64, j = col0 + wave * 16 + c;
+
+  v4f s[DKT], grow[DKT];  // rows 16 a + 4 g + r, column j
+  float4* const kept = p.kept + ((nh * (g.runs - 1) * parts + part) * 4 + wave) * (2 * DKT * 64) + lane;
+  const int64_t kept_step = int64_t(parts) * 4 * (2 * DKT * 64);
+  const float* st = p.state && run == 0 ? p.state + nh * p.dk * p.dv : nullptr;
+#pragma unroll
+  for (int a = 0; a < DKT; ++a) {
+    if (!LOCAL && run > 0) {
+      s[a] = __builtin_bit_cast(v4f, kept[(run - 1) * kept_step + 2 * a * 64]);
+      grow[a] = __builtin_bit_cast(v4f, kept[(run - 1) * kept_step + (2 * a + 1) * 64]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int32_t i = 16 * a + 4 * g4 + r;
+        s[a][r] = st && i < p.dk && j < p.dv ? st[int64_t(i) * p.dv + j] : 0.0f;
+        grow[a][r] = 0.0f;
+      }
+    }
+  }
+  if (threadIdx.x <= CH) power[threadIdx.x] = exp_full(gd * float(int(threadIdx.x)));
+
+  const Elem<DT>* const qn = p.q + n * p.qs[0] + hd * p.qs[2];
+  const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
+  const Elem<DT>* const vn = p.v + n * p.vs[0] + hd * p.vs[2] + col0;
+  const Elem<DT>* const dn = LOCAL ? nullptr : pass.dy + n * pass.dys[0] + hd * pass.dys[2] + col0;
+  KTile tk, tq;
+  VTile tv, td;
+  auto fetch = [&](int32_t chunk) {
+    const int64_t t0 = int64_t(chunk) * CH;
+    const int32_t valid = len - t0 > CH ? CH : int32_t(len - t0);
+    tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid);
+    tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid);
+    if constexpr (!LOCAL) {
+      tq.template load<VEC>(qn + t0 * p.qs[1], p.qs[1], p.dk, valid);
+      td.template load<VEC>(dn + t0 * pass.dys[1], pass.dys[1], p.dv - col0, valid);
+    }
+  };
+  if (chunk_lo < chunk_hi) fetch(chunk_lo);
+  double total = 0.0;
+  for (int32_t chunk = chunk_lo; chunk < chunk_hi; ++chunk) {
+    const int32_t valid = len - chunk * CH > CH ? CH : len - chunk * CH;
+    __syncthreads();  // the chunk before has been read
+    tk.template store<true>(lds_k);
+    tv.template store<true>(lds_v);
+    if constexpr (!LOCAL) {
+      tq.template store<true>(lds_q);
+      td.template store<true>(lds_d);
+    }
+    __syncthreads();
+    if (chunk + 1 < chunk_hi) fetch(chunk + 1);
+
+    if constexpr (!LOCAL) {
+      float sum = 0.0f;
+      // ---- pairs of positions: the wavefront's 16 u = 16 wave + c, s = 16 i + 4 g + r
+      if (wave < MT) {
+        for (int i = 0; i <= wave; ++i) {
+          v4f x = {0.0f, 0.0f, 0.0f, 0.0f}, y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int kb = 0; kb < DKT * 16 / M::kDeep; ++kb)
+            M::mul(KTile::along(lds_k, i, kb), KTile::along(lds_q, wave, kb), x);
+#pragma unroll
+          for (int kb = 0; kb < 64 / M::kDeep; ++kb)
+            M::mul(VTile::along(lds_v, i, kb), VTile::along(lds_d, wave, kb), y);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int d = 16 * (wave - i) + c - 4 * g4 - r;
+            if (d > 0) sum = __builtin_fmaf(x[r] * y[r], float(d) * power[d], sum);
+          }
+        }
+      }
+      // ---- through the states at the chunk's start
+      v4f xs[MT], ys[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xs[m] = ys[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kb = 0; kb < DKT * 16 / M::kDeep; ++kb) {
+        float fs[PE], ft[PE];
+#pragma unroll
+        for (int e = 0; e < PE; ++e) fs[e] = s[kb * PB + e / 4][e % 4], ft[e] = grow[kb * PB + e / 4][e % 4];
+        Frag a[TERMS], b[TERMS];
+        split<DT>(fs, a);
+        split<DT>(ft, b);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const Frag f = KTile::along(lds_q, m, kb);
+#pragma unroll
+          for (int t = 0; t < TERMS; ++t) {
+            M::mul(a[t], f, xs[m]);
+            M::mul(b[t], f, ys[m]);
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const v4f x = xs[m], y = ys[m];
+        // rows: channels 16 wave + 4 g + r; column: position 16 m + c (0 past the valid ones, as dy is)
+        const char* d = lds_d + (16 * m + c) * VTile::kStride;
+        float dy[4];
+        if constexpr (PE == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(d + (16 * wave + 4 * g4) * 4);
+          dy[0] = f.x, dy[1] = f.y, dy[2] = f.z, dy[3] = f.w;
+        } else {
+          const uint2 f = *reinterpret_cast<const uint2*>(d + (wave >> 1) * 64 + g4 * 16 + (wave & 1) * 8);
+          dy[0] = low2(f.x), dy[1] = high2(f.x), dy[2] = low2(f.y), dy[3] = high2(f.y);
+        }
+        const float far = float(16 * m + c + 1);
+        float one = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) one = __builtin_fmaf(dy[r], __builtin_fmaf(far, x[r], y[r]), one);
+        sum = __builtin_fmaf(power[16 * m + c + 1], one, sum);
+      }
+      total += double(sum);
+    }
+
+    // ---- both states to the chunk's end
+    const Decay whole(gd * float(valid));
+#pragma unroll
+    for (int a = 0; a < DKT; ++a)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        grow[a][r] = whole(__builtin_fmaf(float(valid), s[a][r], grow[a][r]));
+        s[a][r] = whole(s[a][r]);
+      }
+#pragma unroll
+    for (int kb = 0; kb < kBlocks; ++kb) {
+      const Frag f = VTile::template across<true>(lds_v, wave, kb);
+      float x[PE], y[PE];
+      if constexpr (PE == 4) {
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+      } else {
+        const uint4 u4 = __builtin_bit_cast(uint4, f);
+        const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < PE; ++e) {
+        const int d = valid - 1 - (kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4), far = d < 0 ? 0 : d;
+        x[e] *= power[far];
+        y[e] = x[e] * float(far);
+      }
+      Frag vs[TERMS], vt[TERMS];
+      split<DT>(x, vs);
+      split<DT>(y, vt);
+#pragma unroll
+      for (int a = 0; a < DKT; ++a) {
+        const Frag k = KTile::template across<true>(lds_k, a, kb);
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          M::mul(k, vs[t], s[a]);
+          M::mul(k, vt[t], grow[a]);
+        }
+      }
+    }
+  }
+
+  if constexpr (LOCAL) {
+#pragma unroll
+    for (int a = 0; a < DKT; ++a) {
+      kept[run * kept_step + 2 * a * 64] = __builtin_bit_cast(float4, s[a]);
+      kept[run * kept_step + (2 * a + 1) * 64] = __builtin_bit_cast(float4, grow[a]);
+    }
+  } else {
+    total *= double(p.scale_y);
+    if (pass.dstate && run == g.runs - 1) {
+      const float* ds = pass.dstate + nh * p.dk * p.dv;
+      float sum = 0.0f;
+#pragma unroll
+      for (int a = 0; a < DKT; ++a)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int32_t i = 16 * a + 4 * g4 + r;
+          if (i < p.dk && j < p.dv) sum = __builtin_fmaf(ds[int64_t(i) * p.dv + j], grow[a][r], sum);
+        }
+      total += double(sum);
+    }
+    const float one = group_sum<64>(float(total));
+    if (lane == 0) red[wave] = one;
+    __syncthreads();
+    if (threadIdx.x == 0) pass.sums[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+  }
+}
+
+// Along the runs, in place, as la_join_kernel; the two states of a row of 16 lie side by side.
+template <int DT>
+__global__ __launch_bounds__(256) void la_decay_join_kernel(DecayPass<DT> pass, LaGeo g, int64_t heads, int32_t per,
+                                                            int32_t chunk) {
+  const int32_t slots = g.runs - 1, half = per / 2;
+  const int64_t total = heads * half;
+  for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+    const int64_t nh = id / half;
+    const int32_t i = int32_t(id - nh * half);
+    const int64_t n = nh / g.h, hd = nh - n * g.h;
+    const int32_t len = valid_len(g.lengths, n, g.l);
+    const float gd = rate(g.log_decay[hd]);
+    float4* at = pass.a.kept + nh * slots * per + (i >> 6) * 128 + (i & 63);
+    v4f h = {0.0f, 0.0f, 0.0f, 0.0f}, t = h;
+    for (int32_t k = 0; k < slots; ++k, at += per) {
+      const int32_t lo = k * g.run * chunk, hi = (k + 1) * g.run * chunk;
+      const int32_t valid = (hi < len ? hi : len) - lo;
+      const float count = float(valid < 0 ? 0 : valid);
+      const Decay d(gd * count);
+      const v4f s = __builtin_bit_cast(v4f, at[0]), grow = __builtin_bit_cast(v4f, at[64]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        t[r] = d(__builtin_fmaf(count, h[r], t[r])) + grow[r];
+        h[r] = d(h[r]) + s[r];
+      }
+      at[0] = __builtin_bit_cast(float4, h);
+      at[64] = __builtin_bit_cast(float4, t);
+    }
+  }
+}
+
 }  // namespace seq
 }  // namespace cnhwc

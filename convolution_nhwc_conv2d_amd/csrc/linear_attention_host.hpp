@@ -27,6 +27,14 @@ struct Cut {
   int32_t per;     // float4 of a head's state in lane order
   uint64_t bytes;
 };
+inline void cut_runs(Cut& c, int64_t l, int64_t all, int64_t room) {
+  c.chunks = int32_t((l + c.chunk - 1) / c.chunk);
+  int64_t runs = all * 2 > room ? 1 : room / all;
+  if (runs > c.chunks / 4) runs = c.chunks / 4;
+  if (runs < 1) runs = 1;
+  c.run = int32_t((c.chunks + runs - 1) / runs);
+  c.runs = (c.chunks + c.run - 1) / c.run;
+}
 template <int DT>
 Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64_t passes) {
   Cut c{};
@@ -36,13 +44,7 @@ Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64
     c.chunk = Sh::kChunk;
     c.parts = (dv + 64 * NT - 1) / (64 * NT);
     c.per = c.parts * 4 * DKT * NT * 64;
-    c.chunks = int32_t((d.l + c.chunk - 1) / c.chunk);
-    const int64_t all = d.n * d.h * c.parts * passes, room = 256 * Sh::kOccupancy;
-    int64_t runs = all * 2 > room ? 1 : room / all;
-    if (runs > c.chunks / 4) runs = c.chunks / 4;
-    if (runs < 1) runs = 1;
-    c.run = int32_t((c.chunks + runs - 1) / runs);
-    c.runs = (c.chunks + c.run - 1) / c.run;
+    cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kOccupancy);
   });
   c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16;
   return c;
@@ -52,10 +54,30 @@ inline bool whole(const void* p, const int64_t (&s)[3], int32_t c, int64_t piece
   return aligned(p, piece * es) && c % piece == 0 && s[0] % piece == 0 && s[1] % piece == 0 && s[2] % piece == 0;
 }
 
+// The same of the decay's gradient: both states, 64 columns a workgroup, and the
+// workgroups' sums behind them.
+template <int DT>
+Cut decay_cut_of(const cnhwc_linear_attention_desc_t& d) {
+  Cut c{};
+  with_shape(d.dk, 64, [&](auto dkt, auto) {
+    constexpr int DKT = decltype(dkt)::value;
+    using Sh = DecayShape<DT, DKT>;
+    c.chunk = Sh::kChunk;
+    c.parts = (d.dv + 63) / 64;
+    c.per = c.parts * 4 * DKT * 64 * 2;
+    cut_runs(c, d.l, d.n * d.h * c.parts, 256 * Sh::kOccupancy);
+  });
+  c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16 + (uint64_t(d.n) * d.h * c.parts * c.runs * 4 + 15) / 16 * 16;
+  return c;
+}
+
 // One or several passes of the same form; each type's kernels are in a source of their own.
 template <int DT>
 hipError_t launch_passes(Passes<DT>& ps, int count, LaGeo g, const Cut& c, int64_t heads, char* workspace,
                          hipStream_t st);
+template <int DT>
+hipError_t launch_decay(DecayPass<DT>& pass, LaGeo g, const Cut& c, int64_t heads, char* workspace, float* out,
+                        hipStream_t st);
 
 }  // namespace seq
 }  // namespace cnhwc
