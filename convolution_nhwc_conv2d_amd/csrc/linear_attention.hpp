@@ -66,6 +66,23 @@ struct Decay {
     keep = slow ? 1.0f : 0.0f;
   }
   __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(m, x, keep * x); }
+  // of many: one instruction each
+  template <int A, int B>
+  __device__ __forceinline__ void apply(v4f (&s)[A][B]) const {
+    if (keep != 0.0f) {
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[a][b][r] = __builtin_fmaf(m, s[a][b][r], s[a][b][r]);
+    } else {
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+#pragma unroll
+        for (int b = 0; b < B; ++b) s[a][b] *= m;
+    }
+  }
 };
 
 // What the matrix products are made of.  bf16: operands as they are, 32 deep; an
@@ -95,9 +112,10 @@ struct Mma<CNHWC_BF16> {
   }
 };
 
-// Two floats as bf16, the first in the lower half; and back.
+// Two floats as bf16 in one conversion, the first in the lower half; and back.
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return uint32_t(from_f<CNHWC_BF16>(a)) | uint32_t(from_f<CNHWC_BF16>(b)) << 16;
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
 }
 __device__ __forceinline__ float low2(uint32_t v) { return __builtin_bit_cast(float, v << 16); }
 __device__ __forceinline__ float high2(uint32_t v) { return __builtin_bit_cast(float, v & 0xffff0000u); }
@@ -124,26 +142,38 @@ __device__ __forceinline__ void split(const float (&x)[P], typename Mma<DT>::Fra
   }
 }
 
-// A tile of CH positions by COLS channels on its way from memory into LDS: rows of
-// COLS elements and 16 bytes more, so that the 16 rows that are read together lie in
-// different banks.  bf16 rows whose channels are a product's depth have each 32
-// of them in the order of the lanes (element 16 i + 4 g + r at 8 g + 4 i + r).
+// A tile of CH positions by COLS channels on its way from memory into LDS, rows of
+// positions.  fp32: 16 bytes behind each row, so that the 16 rows that are read
+// together lie in different banks.  bf16: 32 bytes, which does it for the reads across
+// the rows (4 rows of 32 bytes), and in every second eight rows the 8-byte pieces
+// change places in pairs, which does it for the reads along them (16 rows of 8).
 template <int DT, int COLS, int CH>
 struct Rows2D {
   using M = Mma<DT>;
   using T = typename M::T;
-  static constexpr int kPiece = M::kPiece, kPer = COLS / kPiece, kCount = CH * kPer / 256;
-  static constexpr int kStride = COLS * int(sizeof(T)) + 16, kBytes = CH * kStride;
+  static constexpr int kPiece = M::kPiece, kPer = COLS / kPiece, kCount = CH * kPer / 256, kStep = 256 / kPer;
+  static constexpr bool kHalf = sizeof(T) == 2;
+  static constexpr int kStride = COLS * int(sizeof(T)) + (kHalf ? 32 : 16), kBytes = CH * kStride;
   static_assert(kCount * 256 == CH * kPer, "whole pieces for every thread");
   Pack<DT, kPiece> v[kCount];
 
-  // rows past `valid` and channels past `cols` are 0 and not read
+  static __device__ __forceinline__ int swap(int row) { return kHalf ? row & 8 : 0; }  // in bytes
+
+  // Rows past `valid` and channels past `cols` are 0 and not read.  VEC: whole pieces,
+  // and 64 rows within 32 bits.
   template <bool VEC>
   __device__ __forceinline__ void load(const Elem<DT>* __restrict__ base, int64_t stride, int32_t cols,
                                        int32_t valid) {
+    const int row0 = int(threadIdx.x) / kPer, col = int(threadIdx.x) % kPer * kPiece;
+    if (VEC && valid == CH && cols >= COLS) {
+      const uint32_t at = uint32_t(row0) * uint32_t(stride) + uint32_t(col);
+#pragma unroll
+      for (int i = 0; i < kCount; ++i) v[i] = load_pack<DT, kPiece>(base + i * kStep * stride + at);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const int id = int(threadIdx.x) + 256 * i, row = id / kPer, col = id % kPer * kPiece;
+      const int row = row0 + kStep * i;
       Pack<DT, kPiece> x{};
       if (row < valid && col < cols) {
         const Elem<DT>* p = base + row * stride + col;
@@ -159,53 +189,108 @@ struct Rows2D {
     }
   }
 
-  template <bool DEPTH>
   __device__ __forceinline__ void store(char* lds) const {
+    const int row0 = int(threadIdx.x) / kPer, col = int(threadIdx.x) % kPer * kPiece;
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const int id = int(threadIdx.x) + 256 * i, row = id / kPer, col = id % kPer * kPiece;
+      const int row = row0 + kStep * i;
       char* p = lds + row * kStride;
-      if constexpr (kPiece == 4) {
+      if constexpr (!kHalf) {
         *reinterpret_cast<float4*>(p + col * 4) =
             make_float4(to_f<DT>(v[i].e[0]), to_f<DT>(v[i].e[1]), to_f<DT>(v[i].e[2]), to_f<DT>(v[i].e[3]));
       } else {
         const uint4 x = __builtin_bit_cast(uint4, v[i]);
-        if constexpr (DEPTH) {
-          char* o = p + (col & ~31) * 2 + (col & 8) * 4 + (col & 16) / 2;
-          *reinterpret_cast<uint2*>(o) = make_uint2(x.x, x.y);
-          *reinterpret_cast<uint2*>(o + 16) = make_uint2(x.z, x.w);
-        } else {
-          *reinterpret_cast<uint4*>(p + col * 2) = x;
-        }
+        *reinterpret_cast<uint2*>(p + ((col * 2) ^ swap(row))) = make_uint2(x.x, x.y);
+        *reinterpret_cast<uint2*>(p + ((col * 2 + 8) ^ swap(row))) = make_uint2(x.z, x.w);
       }
     }
   }
 
   // The operand whose rows (or columns) are this tile's rows 16 i + (lane & 15), depth block kb.
   static __device__ __forceinline__ typename M::Frag along(const char* lds, int i, int kb) {
-    const int lane = threadIdx.x & 63;
-    return *reinterpret_cast<const typename M::Frag*>(lds + (16 * i + (lane & 15)) * kStride + kb * 64 + (lane >> 4) * 16);
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const char* p = lds + (16 * i + c) * kStride + kb * 64;
+    if constexpr (!kHalf) {
+      return *reinterpret_cast<const float4*>(p + g * 16);
+    } else {
+      p += (g * 8) ^ swap(c);
+      const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 32);
+      return make_uint4(a.x, a.y, b.x, b.y);
+    }
+  }
+  // Stores what along() reads, for the 16 rows that the lanes are.
+  static __device__ __forceinline__ void put(char* lds, int i, int kb, const typename M::Frag& f) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    char* p = lds + (16 * i + c) * kStride + kb * 64;
+    if constexpr (!kHalf) {
+      *reinterpret_cast<float4*>(p + g * 16) = f;
+    } else {
+      p += (g * 8) ^ swap(c);
+      *reinterpret_cast<uint2*>(p) = make_uint2(f.x, f.y);
+      *reinterpret_cast<uint2*>(p + 32) = make_uint2(f.z, f.w);
+    }
+  }
+  // Channels 16 j + 4 g ... of position 16 i + c.
+  static __device__ __forceinline__ void four(const char* lds, int i, int j, float (&x)[4]) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const char* p = lds + (16 * i + c) * kStride;
+    if constexpr (!kHalf) {
+      const float4 f = *reinterpret_cast<const float4*>(p + j * 64 + g * 16);
+      x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+    } else {
+      const uint2 f = *reinterpret_cast<const uint2*>(p + j * 32 + ((g * 8) ^ swap(c)));
+      x[0] = low2(f.x), x[1] = high2(f.x), x[2] = low2(f.y), x[3] = high2(f.y);
+    }
   }
 
   // The operand whose rows (or columns) are this tile's channels 16 j + (lane & 15) and
   // whose depth is its positions, block kb.  bf16: the LDS read that transposes.
-  template <bool DEPTH>
   static __device__ __forceinline__ typename M::Frag across(const char* lds, int j, int kb) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    if constexpr (kPiece == 4) {
+    if constexpr (!kHalf) {
       const float* p = reinterpret_cast<const float*>(lds + (16 * kb + 4 * g) * kStride) + 16 * j + c;
       constexpr int s = kStride / 4;
       return make_float4(p[0], p[s], p[2 * s], p[3 * s]);
     } else {
       typedef short v4s __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) v4s lds_v4s;
-      const int col = DEPTH ? (j >> 1) * 32 + (c & 3) * 8 + (j & 1) * 4 : 16 * j + (c & 3) * 4;
-      const char* p = lds + (32 * kb + 4 * g + (c >> 2)) * kStride + col * 2;
+      const int row = 4 * g + (c >> 2);
+      const char* p = lds + (32 * kb + row) * kStride + j * 32 + (((c & 3) * 8) ^ swap(row));
       const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
       const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 16 * kStride));
       const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
       return make_uint4(x.x, x.y, y.x, y.y);
     }
+  }
+};
+
+// exp(g d) of the positions of a chunk, in LDS: from the entering state to a position, from a
+// position to the chunk's end (0 past it), and from position to position.  Held in
+// registers (36 of them) they would cost the second workgroup of a compute unit its place.
+template <int CH>
+struct Powers {
+  float rise[CH];       // exp(g (i + 1))
+  float fall[2 * CH];   // exp(g (CH - 1 - i)); 0 from CH on
+  float far[2 * CH];    // exp(g |i - CH|)
+
+  // by: a factor of the ways to the end and of those between positions
+  __device__ __forceinline__ void fill(float gd, float by, bool back) {
+    const int i = threadIdx.x;
+    if (i < CH) {
+      const float r = exp_full(gd * float(i + 1)), f = exp_full(gd * float(CH - 1 - i));
+      rise[i] = back ? r * by : r;
+      fall[i] = back ? f : f * by;
+    } else if (i < 2 * CH) {
+      fall[i] = 0.0f;
+    }
+    if (i < 2 * CH) far[i] = exp_full(gd * float(i < CH ? CH - i : i - CH)) * by;
+  }
+  // of position t, from the start (back: to it) or to the end
+  __device__ __forceinline__ const float* from_start(bool back, int valid) const {
+    return back ? fall + (CH - valid) : rise;
+  }
+  __device__ __forceinline__ const float* to_end(bool back, int valid) const {
+    return back ? rise : fall + (CH - valid);
   }
 };
 
@@ -243,7 +328,7 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
   using PTile = typename Sh::PTile;
   constexpr int CH = Sh::kChunk, MT = Sh::kTiles, PE = M::kPiece, PB = Sh::kPerBlock;
   __shared__ __attribute__((aligned(16))) char lds[LOCAL ? KTile::kBytes + VTile::kBytes : Sh::kLds];
-  __shared__ float power[CH + 1], power_k[CH + 1];
+  __shared__ Powers<CH> power;
   char* const lds_k = lds;
   char* const lds_v = lds + KTile::kBytes;
   char* const lds_q = lds_v + VTile::kBytes;
@@ -294,13 +379,7 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
         }
   }
 
-  // ---- decays over up to a chunk: exp(g d), and times scale_k.  Held in registers
-  // (36 of them) they would cost the second workgroup of a compute unit its place.
-  if (threadIdx.x <= CH) {
-    const float d = exp_full(gd * float(int(threadIdx.x)));
-    power[threadIdx.x] = d;
-    power_k[threadIdx.x] = d * p.scale_k;
-  }
+  power.fill(gd, p.scale_k, back);
   const Decay full(gd * float(CH));
 
   const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
@@ -332,9 +411,9 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
     const int32_t valid = valid_at(step);
     const int32_t t0 = chunk_at(step) * CH;
     __syncthreads();  // the chunk before has been read
-    tk.template store<true>(lds_k);
-    tv.template store<false>(lds_v);
-    if constexpr (!LOCAL) tq.template store<true>(lds_q);
+    tk.store(lds_k);
+    tv.store(lds_v);
+    if constexpr (!LOCAL) tq.store(lds_q);
     __syncthreads();
     if (step + 1 < count) fetch(step + 1);
 
@@ -358,13 +437,14 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
             }
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-              const int far = 16 * wave + c - (16 * tile + 4 * g4 + r), d = back ? -far : far;
-              x[4 * i + r] = d < 0 ? 0.0f : acc[r] * power_k[d < 0 ? 0 : d];
+              const int d = c - 4 * g4 - r;  // on the diagonal: whether u comes before s
+              const float by = power.far[CH + 16 * (wave - tile) + d];
+              x[4 * i + r] = tile == wave && (back ? d > 0 : d < 0) ? 0.0f : acc[r] * by;
             }
           }
           Frag f[1];
           split<DT>(x, f);
-          *reinterpret_cast<Frag*>(lds_p + (16 * wave + c) * PTile::kStride + b * 64 + g4 * 16) = f[0];
+          PTile::put(lds_p, wave, b, f[0]);
         }
       }
       // ---- S^T q^T, decayed from the chunk's start
@@ -389,12 +469,12 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
           for (int b = 0; b < NT; ++b) M::mul(st[b][0], f, o[m][b]);
         }
       }
+      const float* const from_start = power.from_start(back, valid) + c;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int d = back ? valid - 1 - (16 * m + c) : 16 * m + c + 1;
-        const float from_start = power[d < 0 ? 0 : d];
+        const float by = from_start[16 * m];
 #pragma unroll
-        for (int b = 0; b < NT; ++b) o[m][b] *= from_start;
+        for (int b = 0; b < NT; ++b) o[m][b] *= by;
       }
       __syncthreads();  // the products of q and k are there
     }
@@ -403,7 +483,7 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
 #pragma unroll
     for (int kb = 0; kb < Sh::kBlocks; ++kb)
 #pragma unroll
-      for (int b = 0; b < NT; ++b) vf[kb][b] = VTile::template across<false>(lds_v, wave * NT + b, kb);
+      for (int b = 0; b < NT; ++b) vf[kb][b] = VTile::across(lds_v, wave * NT + b, kb);
 
     if constexpr (!LOCAL) {
 #pragma unroll
@@ -440,21 +520,10 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
     }
 
     // ---- S <- decay S + k^T (decayed v)
-    const Decay whole = valid == CH ? full : Decay(gd * float(valid));
-#pragma unroll
-    for (int a = 0; a < DKT; ++a)
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[a][b][r] = whole(s[a][b][r]);
+    (valid == CH ? full : Decay(gd * float(valid))).apply(s);
+    const float* const to_end = power.to_end(back, valid) + 4 * g4;
 #pragma unroll
     for (int kb = 0; kb < Sh::kBlocks; ++kb) {
-      float to_end[PE];
-#pragma unroll
-      for (int e = 0; e < PE; ++e) {
-        const int t = kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4, d = back ? t + 1 : valid - 1 - t;
-        to_end[e] = power_k[d < 0 ? 0 : d];
-      }
       Frag vt[NT][M::kTerms];
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
@@ -469,12 +538,12 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
           for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
         }
 #pragma unroll
-        for (int e = 0; e < PE; ++e) x[e] *= to_end[e];
+        for (int e = 0; e < PE; ++e) x[e] *= to_end[kb * M::kDeep + (e / 4) * 16 + e % 4];
         split<DT>(x, vt[b]);
       }
 #pragma unroll
       for (int a = 0; a < DKT; ++a) {
-        const Frag f = KTile::template across<true>(lds_k, a, kb);
+        const Frag f = KTile::across(lds_k, a, kb);
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -577,7 +646,8 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
   constexpr int CH = Sh::kChunk, MT = CH / 16, PE = M::kPiece, PB = M::kDeep / 16, TERMS = M::kTerms;
   constexpr int kBlocks = CH / M::kDeep;
   __shared__ __attribute__((aligned(16))) char lds[LOCAL ? KTile::kBytes + VTile::kBytes : Sh::kLds];
-  __shared__ float power[CH + 1], red[4];
+  __shared__ Powers<CH> power;
+  __shared__ float red[4];
   char* const lds_k = lds;
   char* const lds_v = lds + KTile::kBytes;
   char* const lds_q = lds_v + VTile::kBytes;
@@ -617,7 +687,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
       }
     }
   }
-  if (threadIdx.x <= CH) power[threadIdx.x] = exp_full(gd * float(int(threadIdx.x)));
+  power.fill(gd, 1.0f, false);
 
   const Elem<DT>* const qn = p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
@@ -640,11 +710,11 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
   for (int32_t chunk = chunk_lo; chunk < chunk_hi; ++chunk) {
     const int32_t valid = len - chunk * CH > CH ? CH : len - chunk * CH;
     __syncthreads();  // the chunk before has been read
-    tk.template store<true>(lds_k);
-    tv.template store<true>(lds_v);
+    tk.store(lds_k);
+    tv.store(lds_v);
     if constexpr (!LOCAL) {
-      tq.template store<true>(lds_q);
-      td.template store<true>(lds_d);
+      tq.store(lds_q);
+      td.store(lds_d);
     }
     __syncthreads();
     if (chunk + 1 < chunk_hi) fetch(chunk + 1);
@@ -664,7 +734,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int d = 16 * (wave - i) + c - 4 * g4 - r;
-            if (d > 0) sum = __builtin_fmaf(x[r] * y[r], float(d) * power[d], sum);
+            if (d > 0) sum = __builtin_fmaf(x[r] * y[r], float(d) * power.far[CH + d], sum);
           }
         }
       }
@@ -694,20 +764,13 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
       for (int m = 0; m < MT; ++m) {
         const v4f x = xs[m], y = ys[m];
         // rows: channels 16 wave + 4 g + r; column: position 16 m + c (0 past the valid ones, as dy is)
-        const char* d = lds_d + (16 * m + c) * VTile::kStride;
         float dy[4];
-        if constexpr (PE == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(d + (16 * wave + 4 * g4) * 4);
-          dy[0] = f.x, dy[1] = f.y, dy[2] = f.z, dy[3] = f.w;
-        } else {
-          const uint2 f = *reinterpret_cast<const uint2*>(d + (wave >> 1) * 64 + g4 * 16 + (wave & 1) * 8);
-          dy[0] = low2(f.x), dy[1] = high2(f.x), dy[2] = low2(f.y), dy[3] = high2(f.y);
-        }
+        VTile::four(lds_d, m, wave, dy);
         const float far = float(16 * m + c + 1);
         float one = 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) one = __builtin_fmaf(dy[r], __builtin_fmaf(far, x[r], y[r]), one);
-        sum = __builtin_fmaf(power[16 * m + c + 1], one, sum);
+        sum = __builtin_fmaf(power.rise[16 * m + c], one, sum);
       }
       total += double(sum);
     }
@@ -723,7 +786,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
       }
 #pragma unroll
     for (int kb = 0; kb < kBlocks; ++kb) {
-      const Frag f = VTile::template across<true>(lds_v, wave, kb);
+      const Frag f = VTile::across(lds_v, wave, kb);
       float x[PE], y[PE];
       if constexpr (PE == 4) {
         x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
@@ -735,16 +798,16 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
       }
 #pragma unroll
       for (int e = 0; e < PE; ++e) {
-        const int d = valid - 1 - (kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4), far = d < 0 ? 0 : d;
-        x[e] *= power[far];
-        y[e] = x[e] * float(far);
+        const int t = kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4;
+        x[e] *= power.fall[CH - valid + t];
+        y[e] = x[e] * float(valid - 1 - t);
       }
       Frag vs[TERMS], vt[TERMS];
       split<DT>(x, vs);
       split<DT>(y, vt);
 #pragma unroll
       for (int a = 0; a < DKT; ++a) {
-        const Frag k = KTile::template across<true>(lds_k, a, kb);
+        const Frag k = KTile::across(lds_k, a, kb);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) {
           M::mul(k, vs[t], s[a]);

@@ -50,8 +50,9 @@ Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64
   return c;
 }
 
+// Whole pieces to load, and 64 rows within 32 bits of a byte offset.
 inline bool whole(const void* p, const int64_t (&s)[3], int32_t c, int64_t piece, uint64_t es) {
-  return aligned(p, piece * es) && c % piece == 0 && s[0] % piece == 0 && s[1] % piece == 0 && s[2] % piece == 0;
+  return aligned(p, piece * es) && c % piece == 0 && s[1] < (1 << 23) && s[0] % piece == 0 && s[1] % piece == 0 && s[2] % piece == 0;
 }
 
 // The same of the decay's gradient: both states, 64 columns a workgroup, and the
