@@ -200,8 +200,8 @@ hipError_t step_t(const Desc& d, const cnhwc_linear_attention_inputs_t& in, void
 template <int DT>
 bool one_form(const Desc& d) {
   int a = 0, b = 0;
-  with_shape(d.dk, d.dv, [&](auto dkt, auto nt) { a = dkt.value * 4 + nt.value; });
-  with_shape(d.dv, d.dk, [&](auto dkt, auto nt) { b = dkt.value * 4 + nt.value; });
+  with_shape(d.dk, d.dv, [&](auto dkt, auto w) { a = dkt.value * 16 + w.value; });
+  with_shape(d.dv, d.dk, [&](auto dkt, auto w) { b = dkt.value * 16 + w.value; });
   return a == b && (d.dk + 127) / 128 == (d.dv + 127) / 128;
 }
 template <int DT>

@@ -7,8 +7,8 @@
 // which is four matrix products: q k^T under its decays, that times v, q S, and k^T
 // times the decayed v.  A pass from the end has u and s the other way round.
 //
-// A workgroup owns one head's state, or 64 NT columns of it, for a run of chunks.  The
-// four wavefronts have 16 NT columns each, in fp32 accumulators: a lane holds
+// A workgroup owns one head's state, or 64 or 128 columns of it, for a run of chunks.  A
+// wavefront has 16 columns, in fp32 accumulators: a lane holds
 // four consecutive rows of one column, which is just what the next product takes
 // as its left operand (S^T), so the state never leaves the registers.  y is computed
 // transposed for the same reason, and a lane then stores consecutive channels.
@@ -67,20 +67,16 @@ struct Decay {
   }
   __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(m, x, keep * x); }
   // of many: one instruction each
-  template <int A, int B>
-  __device__ __forceinline__ void apply(v4f (&s)[A][B]) const {
+  template <int A>
+  __device__ __forceinline__ void apply(v4f (&s)[A]) const {
     if (keep != 0.0f) {
 #pragma unroll
       for (int a = 0; a < A; ++a)
 #pragma unroll
-        for (int b = 0; b < B; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[a][b][r] = __builtin_fmaf(m, s[a][b][r], s[a][b][r]);
+        for (int r = 0; r < 4; ++r) s[a][r] = __builtin_fmaf(m, s[a][r], s[a][r]);
     } else {
 #pragma unroll
-      for (int a = 0; a < A; ++a)
-#pragma unroll
-        for (int b = 0; b < B; ++b) s[a][b] *= m;
+      for (int a = 0; a < A; ++a) s[a] *= m;
     }
   }
 };
@@ -142,64 +138,84 @@ __device__ __forceinline__ void split(const float (&x)[P], typename Mma<DT>::Fra
   }
 }
 
+// An operand's elements as floats.
+template <int DT, int P>
+__device__ __forceinline__ void unpack(const typename Mma<DT>::Frag& f, float (&x)[P]) {
+  if constexpr (P == 4) {
+    x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+  } else {
+    const uint32_t u[4] = {__builtin_bit_cast(uint4, f).x, __builtin_bit_cast(uint4, f).y, __builtin_bit_cast(uint4, f).z,
+                           __builtin_bit_cast(uint4, f).w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
+  }
+}
+
 // A tile of CH positions by COLS channels on its way from memory into LDS, rows of
 // positions.  fp32: 16 bytes behind each row, so that the 16 rows that are read
 // together lie in different banks.  bf16: 32 bytes, which does it for the reads across
 // the rows (4 rows of 32 bytes), and in every second eight rows the 8-byte pieces
 // change places in pairs, which does it for the reads along them (16 rows of 8).
-template <int DT, int COLS, int CH>
+template <int DT, int COLS, int CH, int THREADS>
 struct Rows2D {
   using M = Mma<DT>;
   using T = typename M::T;
-  static constexpr int kPiece = M::kPiece, kPer = COLS / kPiece, kCount = CH * kPer / 256, kStep = 256 / kPer;
+  static constexpr int kPiece = M::kPiece, kPer = COLS / kPiece, kStep = THREADS / kPer;
+  static constexpr int kCount = (CH + kStep - 1) / kStep;  // pieces of a thread; of some of the threads where
+  static constexpr bool kSome = CH % kStep != 0;           // the tile is smaller than the workgroup
   static constexpr bool kHalf = sizeof(T) == 2;
   static constexpr int kStride = COLS * int(sizeof(T)) + (kHalf ? 32 : 16), kBytes = CH * kStride;
-  static_assert(kCount * 256 == CH * kPer, "whole pieces for every thread");
-  Pack<DT, kPiece> v[kCount];
+  static_assert(kCount == 1 || !kSome, "whole pieces for every thread");
+  using Raw = PackBits<DT, kPiece>;  // held whole: as elements they would be taken apart on arrival
+  Raw v[kCount];
 
   static __device__ __forceinline__ int swap(int row) { return kHalf ? row & 8 : 0; }  // in bytes
 
-  // Rows past `valid` and channels past `cols` are 0 and not read.  VEC: whole pieces,
-  // and 64 rows within 32 bits.
+  // Rows past `valid` and channels past `cols` are not read: VEC (whole pieces, 64 rows
+  // within 32 bits of an offset) reads others instead, without a branch for every piece;
+  // store() leaves them out.
   template <bool VEC>
   __device__ __forceinline__ void load(const Elem<DT>* __restrict__ base, int64_t stride, int32_t cols,
                                        int32_t valid) {
     const int row0 = int(threadIdx.x) / kPer, col = int(threadIdx.x) % kPer * kPiece;
-    if (VEC && valid == CH && cols >= COLS) {
-      const uint32_t at = uint32_t(row0) * uint32_t(stride) + uint32_t(col);
-#pragma unroll
-      for (int i = 0; i < kCount; ++i) v[i] = load_pack<DT, kPiece>(base + i * kStep * stride + at);
-      return;
-    }
+    const uint32_t at = uint32_t(col < cols ? col : 0), last = uint32_t(valid - 1);
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
-      const int row = row0 + kStep * i;
-      Pack<DT, kPiece> x{};
-      if (row < valid && col < cols) {
-        const Elem<DT>* p = base + row * stride + col;
-        if constexpr (VEC) {
-          x = load_pack<DT, kPiece>(p);
-        } else {
+      const uint32_t row = uint32_t(row0 + kStep * i);
+      if constexpr (VEC) {
+        v[i] = *reinterpret_cast<const Raw*>(base + (__umul24(row < last ? row : last, uint32_t(stride)) + at));
+      } else {
+        Pack<DT, kPiece> x{};
+        if (row <= last) {
+          const Elem<DT>* p = base + row * stride + col;
 #pragma unroll
           for (int e = 0; e < kPiece; ++e)
             if (col + e < cols) x.e[e] = p[e];
         }
+        v[i] = __builtin_bit_cast(Raw, x);
       }
-      v[i] = x;
     }
   }
 
-  __device__ __forceinline__ void store(char* lds) const {
+  // all: no row and no channel is left out
+  __device__ __forceinline__ void store(char* lds, bool all, int32_t cols, int32_t valid) {
     const int row0 = int(threadIdx.x) / kPer, col = int(threadIdx.x) % kPer * kPiece;
+    if (!all) {
+#pragma unroll
+      for (int i = 0; i < kCount; ++i)
+        if (row0 + kStep * i >= valid || col >= cols) v[i] = Raw{};
+    }
+    if (kSome && row0 >= CH) return;
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
       const int row = row0 + kStep * i;
       char* p = lds + row * kStride;
       if constexpr (!kHalf) {
+        const Pack<DT, 4> x = __builtin_bit_cast(Pack<DT, 4>, v[i]);
         *reinterpret_cast<float4*>(p + col * 4) =
-            make_float4(to_f<DT>(v[i].e[0]), to_f<DT>(v[i].e[1]), to_f<DT>(v[i].e[2]), to_f<DT>(v[i].e[3]));
+            make_float4(to_f<DT>(x.e[0]), to_f<DT>(x.e[1]), to_f<DT>(x.e[2]), to_f<DT>(x.e[3]));
       } else {
-        const uint4 x = __builtin_bit_cast(uint4, v[i]);
+        const uint4 x = v[i];
         *reinterpret_cast<uint2*>(p + ((col * 2) ^ swap(row))) = make_uint2(x.x, x.y);
         *reinterpret_cast<uint2*>(p + ((col * 2 + 8) ^ swap(row))) = make_uint2(x.z, x.w);
       }
@@ -294,20 +310,22 @@ struct Powers {
   }
 };
 
-// The chunk of a pass's kernels, LDS and occupancy.
-template <int DT, int DKT, int NT>
+// The chunk of a pass's kernels and what they take: W wavefronts of 16 columns each.
+template <int DT, int DKT, int W>
 struct ChunkShape {
   using M = Mma<DT>;
-  static constexpr int kChunk = sizeof(typename M::T) == 4 && DKT == 16 ? 32 : 64;
+  static constexpr int kChunk = 32;
+  static constexpr int kThreads = 64 * W, kCols = 16 * W;
   static constexpr int kTiles = kChunk / 16;                  // of 16 positions
   static constexpr int kDepth = DKT * 16 / M::kDeep;          // blocks of a state's rows
   static constexpr int kBlocks = kChunk / M::kDeep;           // blocks of positions
   static constexpr int kPerBlock = M::kDeep / 16;             // 16-row tiles of a block
-  using KTile = Rows2D<DT, DKT * 16, kChunk>;                 // q and k
-  using VTile = Rows2D<DT, NT * 64, kChunk>;
-  using PTile = Rows2D<DT, kChunk, kChunk>;
+  using KTile = Rows2D<DT, DKT * 16, kChunk, kThreads>;       // q and k
+  using VTile = Rows2D<DT, kCols, kChunk, kThreads>;
+  using PTile = Rows2D<DT, kChunk, kChunk, kThreads>;
   static constexpr int kLds = 2 * KTile::kBytes + VTile::kBytes + PTile::kBytes;
-  static constexpr int kOccupancy = kLds <= 80 * 1024 && DKT <= 8 ? 2 : 1;
+  static constexpr int kGroups = kLds <= 78 * 1024 ? 2 : 1;   // workgroups of a compute unit
+  static constexpr int kWaves = kGroups * W / 4;              // wavefronts of a SIMD
 };
 
 template <int DT>
@@ -315,29 +333,27 @@ struct Passes {
   Pass<DT> p[3];
 };
 
-// LOCAL: the state that a run of chunks leaves from a zero state (the first run: from
-// the initial one), for all runs but the last.  Otherwise y and the final state.
-template <int DT, int DKT, int NT, bool LOCAL, bool VEC>
-__global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la_chunk_kernel(Passes<DT> passes,
-                                                                                            LaGeo g) {
-  using Sh = ChunkShape<DT, DKT, NT>;
+// What a workgroup does.  LOCAL: the state that a run of chunks leaves from a zero state
+// (the first run: from the initial one), for all runs but the last.  Otherwise y and
+// the final state.
+template <int DT, int DKT, int W, bool LOCAL, bool VEC, bool BACK>
+__device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, char* lds,
+                                          Powers<ChunkShape<DT, DKT, W>::kChunk>& power) {
+  using Sh = ChunkShape<DT, DKT, W>;
   using M = typename Sh::M;
   using Frag = typename M::Frag;
   using KTile = typename Sh::KTile;
   using VTile = typename Sh::VTile;
   using PTile = typename Sh::PTile;
   constexpr int CH = Sh::kChunk, MT = Sh::kTiles, PE = M::kPiece, PB = Sh::kPerBlock;
-  __shared__ __attribute__((aligned(16))) char lds[LOCAL ? KTile::kBytes + VTile::kBytes : Sh::kLds];
-  __shared__ Powers<CH> power;
   char* const lds_k = lds;
   char* const lds_v = lds + KTile::kBytes;
   char* const lds_q = lds_v + VTile::kBytes;
   char* const lds_p = lds_q + KTile::kBytes;
 
-  const Pass<DT>& p = passes.p[blockIdx.y];
   const int lane = threadIdx.x & 63, c = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t parts = (p.dv + 64 * NT - 1) / (64 * NT);  // workgroups along the state's columns
+  const int32_t parts = (p.dv + Sh::kCols - 1) / Sh::kCols;  // workgroups along the state's columns
   const int32_t part = int32_t(blockIdx.x % unsigned(parts));
   const int64_t row = blockIdx.x / unsigned(parts);
   const int32_t runs = LOCAL ? g.runs - 1 : g.runs;
@@ -346,50 +362,45 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
   const int64_t n = nh / g.h, hd = nh - n * g.h;
   const int32_t len = valid_len(g.lengths, n, g.l);
   const float gd = rate(g.log_decay[hd]);
-  const bool back = p.back;
 
-  const int32_t at = back ? g.runs - 1 - run : run;
+  const int32_t at = BACK ? g.runs - 1 - run : run;
   // the run's chunks with valid positions; past them the state stands still
   const int32_t chunk_lo = at * g.run, all_hi = chunk_lo + g.run < g.chunks ? chunk_lo + g.run : g.chunks;
   const int32_t used = (len + CH - 1) / CH;
   const int32_t chunk_hi = used < chunk_lo ? chunk_lo : used < all_hi ? used : all_hi;
   const int32_t count = chunk_hi - chunk_lo;
-  const int32_t col0 = part * 64 * NT;                // first column of the workgroup, and
-  const int32_t j0 = col0 + wave * 16 * NT;           // of the wavefront
+  const int32_t col0 = part * Sh::kCols, j = col0 + wave * 16 + c;
 
-  // ---- the state: rows 16 a + 4 g + r, column j0 + 16 b + c
-  v4f s[DKT][NT];
-  float4* const kept = p.kept + ((nh * (g.runs - 1) * parts + part) * 4 + wave) * (DKT * NT * 64) + lane;
-  const int64_t kept_step = int64_t(parts) * 4 * (DKT * NT * 64);  // to the next run's
+  // ---- the state: rows 16 a + 4 g + r of column j
+  v4f s[DKT];
+  float4* const kept = p.kept + ((nh * (g.runs - 1) * parts + part) * W + wave) * (DKT * 64) + lane;
+  const int64_t kept_step = int64_t(parts) * W * (DKT * 64);  // to the next run's
   if (!LOCAL && run > 0) {
 #pragma unroll
-    for (int a = 0; a < DKT; ++a)
-#pragma unroll
-      for (int b = 0; b < NT; ++b) s[a][b] = __builtin_bit_cast(v4f, kept[(run - 1) * kept_step + (a * NT + b) * 64]);
+    for (int a = 0; a < DKT; ++a) s[a] = __builtin_bit_cast(v4f, kept[(run - 1) * kept_step + a * 64]);
   } else {
     const float* st = p.state && run == 0 ? p.state + nh * p.dk * p.dv : nullptr;
 #pragma unroll
     for (int a = 0; a < DKT; ++a)
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int32_t i = 16 * a + 4 * g4 + r, j = j0 + 16 * b + c;
-          s[a][b][r] = st && i < p.dk && j < p.dv ? st[i * p.state_k + j * p.state_v] : 0.0f;
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int32_t i = 16 * a + 4 * g4 + r;
+        s[a][r] = st && i < p.dk && j < p.dv ? st[i * p.state_k + j * p.state_v] : 0.0f;
+      }
   }
 
-  power.fill(gd, p.scale_k, back);
+  power.fill(gd, p.scale_k, BACK);
   const Decay full(gd * float(CH));
 
   const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
   const Elem<DT>* const vn = p.v + n * p.vs[0] + hd * p.vs[2] + col0;
-  auto chunk_at = [&](int32_t i) { return back ? chunk_hi - 1 - i : chunk_lo + i; };
+  auto chunk_at = [&](int32_t i) { return BACK ? chunk_hi - 1 - i : chunk_lo + i; };
   auto valid_at = [&](int32_t i) {
     const int32_t v = len - chunk_at(i) * CH;
     return v > CH ? CH : v;
   };
+  const bool filled = p.dk == DKT * 16 && p.dv - col0 >= Sh::kCols;
   KTile tk, tq;
   VTile tv;
   auto fetch = [&](int32_t i) {
@@ -402,173 +413,183 @@ __global__ __launch_bounds__(256, (ChunkShape<DT, DKT, NT>::kOccupancy)) void la
   if (count > 0) fetch(0);
   if constexpr (!LOCAL) {
     const int64_t first = int64_t(chunk_hi) * CH, last = int64_t(all_hi) * CH < g.l ? int64_t(all_hi) * CH : g.l;
-    const int32_t wide = p.dv - col0 < 64 * NT ? p.dv - col0 : 64 * NT;
-    for (int64_t e = threadIdx.x; e < (last - first) * wide; e += 256)
+    const int32_t wide = p.dv - col0 < Sh::kCols ? p.dv - col0 : Sh::kCols;
+    for (int64_t e = threadIdx.x; e < (last - first) * wide; e += Sh::kThreads)
       p.y[((n * g.l + first + e / wide) * g.h + hd) * p.dv + col0 + e % wide] = Elem<DT>(0);
   }
+
+  // a lane has four channels of the positions 16 m + c
+  using Raw4 = PackBits<DT, 4>;
+  Raw4 out[LOCAL ? 1 : MT];
+  int32_t out_t0 = 0;
+  const int32_t j4 = col0 + wave * 16 + 4 * g4;
+  auto put_y = [&]() __attribute__((always_inline)) {
+    const int32_t rows = g.l - out_t0 < CH ? g.l - out_t0 : CH, live = len - out_t0;
+    Elem<DT>* const base = p.y + ((n * g.l + out_t0) * g.h + hd) * p.dv;
+    const int64_t step = int64_t(g.h) * p.dv;
+    if constexpr (VEC) {
+      const uint32_t to = __umul24(c, uint32_t(step)) + j4;  // 64 rows within 32 bits
+      if (j4 < p.dv) {
+        if (live >= CH) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) *reinterpret_cast<Raw4*>(base + m * 16 * step + to) = out[m];
+        } else {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            if (16 * m + c < rows) *reinterpret_cast<Raw4*>(base + m * 16 * step + to) = 16 * m + c < live ? out[m] : Raw4{};
+        }
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (16 * m + c >= rows) continue;
+        const Pack<DT, 4> x = __builtin_bit_cast(Pack<DT, 4>, 16 * m + c < live ? out[m] : Raw4{});
+        Elem<DT>* y = base + (16 * m + c) * step + j4;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (j4 + r < p.dv) y[r] = x.e[r];
+      }
+    }
+  };
 
   for (int32_t step = 0; step < count; ++step) {
     const int32_t valid = valid_at(step);
     const int32_t t0 = chunk_at(step) * CH;
     __syncthreads();  // the chunk before has been read
-    tk.store(lds_k);
-    tv.store(lds_v);
-    if constexpr (!LOCAL) tq.store(lds_q);
+    const bool all = filled && valid == CH;
+    tk.store(lds_k, all, p.dk, valid);
+    tv.store(lds_v, all, p.dv - col0, valid);
+    if constexpr (!LOCAL) tq.store(lds_q, all, p.dk, valid);
     __syncthreads();
+    if constexpr (!LOCAL) {
+      if (step > 0) put_y();
+    }
     if (step + 1 < count) fetch(step + 1);
 
-    v4f o[LOCAL ? 1 : MT][NT];
+    v4f o[LOCAL ? 1 : MT];
     if constexpr (!LOCAL) {
-      // ---- (q k^T)^T under its decays: this wavefront's 16 columns of q, to LDS as rows
-      if (wave < MT) {
+      // ---- (q k^T)^T under its decays, to LDS as rows of q: 16 rows by a block of k's
+      // positions to a wavefront
+      const int u = wave % MT;
+      for (int b = wave / MT; b < Sh::kBlocks; b += W / MT) {
+        if (BACK ? b < u / PB : b > u / PB) continue;
+        float x[PE];
 #pragma unroll
-        for (int b = 0; b < Sh::kBlocks; ++b) {
-          const bool any = back ? b >= wave / PB : b <= wave / PB;
-          if (!any) continue;
-          float x[PE];
+        for (int i = 0; i < PB; ++i) {
+          const int tile = b * PB + i;
+          v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (BACK ? tile >= u : tile <= u) {
 #pragma unroll
-          for (int i = 0; i < PB; ++i) {
-            const int tile = b * PB + i;
-            v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (back ? tile >= wave : tile <= wave) {
-#pragma unroll
-              for (int kb = 0; kb < Sh::kDepth; ++kb)
-                M::mul(KTile::along(lds_k, tile, kb), KTile::along(lds_q, wave, kb), acc);
-            }
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-              const int d = c - 4 * g4 - r;  // on the diagonal: whether u comes before s
-              const float by = power.far[CH + 16 * (wave - tile) + d];
-              x[4 * i + r] = tile == wave && (back ? d > 0 : d < 0) ? 0.0f : acc[r] * by;
-            }
+            for (int kb = 0; kb < Sh::kDepth; ++kb)
+              M::mul(KTile::along(lds_k, tile, kb), KTile::along(lds_q, u, kb), acc);
           }
-          Frag f[1];
-          split<DT>(x, f);
-          PTile::put(lds_p, wave, b, f[0]);
+          const int far = 16 * (u - tile) + c - 4 * g4;  // from k's position (its first) to q's
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float by = power.far[CH + far - r];
+            asm volatile("" : "+v"(by));  // read in any case: no branch around it
+            x[4 * i + r] = (BACK ? far > r : far < r) ? 0.0f : acc[r] * by;
+          }
         }
+        Frag f[1];
+        split<DT>(x, f);
+        PTile::put(lds_p, u, b, f[0]);
       }
       // ---- S^T q^T, decayed from the chunk's start
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int b = 0; b < NT; ++b) o[m][b] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int m = 0; m < MT; ++m) o[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int kb = 0; kb < Sh::kDepth; ++kb) {
-        Frag st[NT][1];
+        float x[PE];
 #pragma unroll
-        for (int b = 0; b < NT; ++b) {
-          float x[PE];
+        for (int e = 0; e < PE; ++e) x[e] = s[kb * PB + e / 4][e % 4];
+        Frag st[1];
+        split<DT>(x, st);
 #pragma unroll
-          for (int e = 0; e < PE; ++e) x[e] = s[kb * PB + e / 4][b][e % 4];
-          split<DT>(x, st[b]);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const Frag f = KTile::along(lds_q, m, kb);
-#pragma unroll
-          for (int b = 0; b < NT; ++b) M::mul(st[b][0], f, o[m][b]);
-        }
+        for (int m = 0; m < MT; ++m) M::mul(st[0], KTile::along(lds_q, m, kb), o[m]);
       }
-      const float* const from_start = power.from_start(back, valid) + c;
+      const float* const from_start = power.from_start(BACK, valid) + c;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const float by = from_start[16 * m];
-#pragma unroll
-        for (int b = 0; b < NT; ++b) o[m][b] *= by;
-      }
+      for (int m = 0; m < MT; ++m) o[m] *= from_start[16 * m];
       __syncthreads();  // the products of q and k are there
     }
 
-    Frag vf[Sh::kBlocks][NT];
+    Frag vf[Sh::kBlocks];
 #pragma unroll
-    for (int kb = 0; kb < Sh::kBlocks; ++kb)
-#pragma unroll
-      for (int b = 0; b < NT; ++b) vf[kb][b] = VTile::across(lds_v, wave * NT + b, kb);
+    for (int kb = 0; kb < Sh::kBlocks; ++kb) vf[kb] = VTile::across(lds_v, wave, kb);
 
     if constexpr (!LOCAL) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int kb = 0; kb < Sh::kBlocks; ++kb) {
-          if (back ? kb < m / PB : kb > m / PB) continue;
-          const Frag f = PTile::along(lds_p, m, kb);
-#pragma unroll
-          for (int b = 0; b < NT; ++b) M::mul(vf[kb][b], f, o[m][b]);
+          if (BACK ? kb < m / PB : kb > m / PB) continue;
+          M::mul(vf[kb], PTile::along(lds_p, m, kb), o[m]);
         }
-      // ---- y: a lane has channels j0 + 16 b + 4 g ... of position 16 m + c
+      // ---- y, to be stored when the next chunk has arrived: the wait for that chunk
+      // would be for these stores too
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const int32_t t = t0 + 16 * m + c;
-        if (t >= g.l) continue;
-        Elem<DT>* y = p.y + ((n * g.l + t) * g.h + hd) * p.dv;
-        const bool live = t < len;
+        const v4f f = o[m] * p.scale_y;
+        if constexpr (DT == CNHWC_BF16) {
+          out[m] = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+        } else {
+          Pack<DT, 4> x;
 #pragma unroll
-        for (int b = 0; b < NT; ++b) {
-          const int32_t j = j0 + 16 * b + 4 * g4;
-          Pack<DT, 4> out;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) out.e[r] = from_f<DT>(live ? o[m][b][r] * p.scale_y : 0.0f);
-          if constexpr (VEC) {
-            if (j < p.dv) store_pack<DT, 4>(y + j, out);
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (j + r < p.dv) y[j + r] = out.e[r];
-          }
+          for (int r = 0; r < 4; ++r) x.e[r] = from_f<DT>(f[r]);
+          out[m] = __builtin_bit_cast(Raw4, x);
         }
       }
+      out_t0 = t0;
     }
 
     // ---- S <- decay S + k^T (decayed v)
     (valid == CH ? full : Decay(gd * float(valid))).apply(s);
-    const float* const to_end = power.to_end(back, valid) + 4 * g4;
+    const float* const to_end = power.to_end(BACK, valid) + 4 * g4;
 #pragma unroll
     for (int kb = 0; kb < Sh::kBlocks; ++kb) {
-      Frag vt[NT][M::kTerms];
+      float x[PE];
+      unpack<DT>(vf[kb], x);
 #pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        float x[PE];
-        if constexpr (PE == 4) {
-          const float4 f = vf[kb][b];
-          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-        } else {
-          const uint4 f = vf[kb][b];
-          const uint32_t u[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < PE; ++e) x[e] *= to_end[kb * M::kDeep + (e / 4) * 16 + e % 4];
-        split<DT>(x, vt[b]);
-      }
+      for (int e = 0; e < PE; ++e) x[e] *= to_end[kb * M::kDeep + (e / 4) * 16 + e % 4];
+      Frag vt[M::kTerms];
+      split<DT>(x, vt);
 #pragma unroll
       for (int a = 0; a < DKT; ++a) {
         const Frag f = KTile::across(lds_k, a, kb);
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
-#pragma unroll
-          for (int t = 0; t < M::kTerms; ++t) M::mul(f, vt[b][t], s[a][b]);
+        for (int t = 0; t < M::kTerms; ++t) M::mul(f, vt[t], s[a]);
       }
     }
   }
 
+  if constexpr (!LOCAL) {
+    if (count > 0) put_y();
+  }
   if constexpr (LOCAL) {
 #pragma unroll
-    for (int a = 0; a < DKT; ++a)
-#pragma unroll
-      for (int b = 0; b < NT; ++b) kept[run * kept_step + (a * NT + b) * 64] = __builtin_bit_cast(float4, s[a][b]);
+    for (int a = 0; a < DKT; ++a) kept[run * kept_step + a * 64] = __builtin_bit_cast(float4, s[a]);
   } else if (p.state_out && run == g.runs - 1) {
     float* st = p.state_out + nh * p.dk * p.dv;
 #pragma unroll
     for (int a = 0; a < DKT; ++a)
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int32_t i = 16 * a + 4 * g4 + r, j = j0 + 16 * b + c;
-          if (i < p.dk && j < p.dv) st[i * p.state_k + j * p.state_v] = s[a][b][r];
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int32_t i = 16 * a + 4 * g4 + r;
+        if (i < p.dk && j < p.dv) st[i * p.state_k + j * p.state_v] = s[a][r];
+      }
   }
+}
+
+template <int DT, int DKT, int W, bool LOCAL, bool VEC>
+__global__ __launch_bounds__(64 * W, (ChunkShape<DT, DKT, W>::kWaves)) void la_chunk_kernel(Passes<DT> passes,
+                                                                                           LaGeo g) {
+  using Sh = ChunkShape<DT, DKT, W>;
+  __shared__ __attribute__((aligned(16))) char lds[LOCAL ? Sh::KTile::kBytes + Sh::VTile::kBytes : Sh::kLds];
+  __shared__ Powers<Sh::kChunk> power;
+  const Pass<DT>& p = passes.p[blockIdx.y];
+  if (p.back) la_chunks<DT, DKT, W, LOCAL, VEC, true>(p, g, lds, power);
+  else la_chunks<DT, DKT, W, LOCAL, VEC, false>(p, g, lds, power);
 }
 
 // Along the runs, in place: what each leaves from a zero state -> the state that
@@ -628,9 +649,9 @@ struct DecayPass {
 
 template <int DT, int DKT>
 struct DecayShape {
-  static constexpr int kChunk = ChunkShape<DT, DKT, 1>::kChunk;
-  using KTile = Rows2D<DT, DKT * 16, kChunk>;
-  using VTile = Rows2D<DT, 64, kChunk>;
+  static constexpr int kChunk = sizeof(typename Mma<DT>::T) == 4 && DKT == 16 ? 32 : 64;
+  using KTile = Rows2D<DT, DKT * 16, kChunk, 256>;
+  using VTile = Rows2D<DT, 64, kChunk, 256>;
   static constexpr int kLds = 2 * KTile::kBytes + 2 * VTile::kBytes;
   static constexpr int kOccupancy = kLds <= 76 * 1024 && DKT <= 8 ? 2 : 1;
 };
@@ -693,6 +714,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
   const Elem<DT>* const vn = p.v + n * p.vs[0] + hd * p.vs[2] + col0;
   const Elem<DT>* const dn = LOCAL ? nullptr : pass.dy + n * pass.dys[0] + hd * pass.dys[2] + col0;
+  const bool filled = p.dk == DKT * 16 && p.dv - col0 >= 64;
   KTile tk, tq;
   VTile tv, td;
   auto fetch = [&](int32_t chunk) {
@@ -710,11 +732,12 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
   for (int32_t chunk = chunk_lo; chunk < chunk_hi; ++chunk) {
     const int32_t valid = len - chunk * CH > CH ? CH : len - chunk * CH;
     __syncthreads();  // the chunk before has been read
-    tk.store(lds_k);
-    tv.store(lds_v);
+    const bool all = filled && valid == CH;
+    tk.store(lds_k, all, p.dk, valid);
+    tv.store(lds_v, all, p.dv - col0, valid);
     if constexpr (!LOCAL) {
-      tq.store(lds_q);
-      td.store(lds_d);
+      tq.store(lds_q, all, p.dk, valid);
+      td.store(lds_d, all, p.dv - col0, valid);
     }
     __syncthreads();
     if (chunk + 1 < chunk_hi) fetch(chunk + 1);
@@ -788,14 +811,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
     for (int kb = 0; kb < kBlocks; ++kb) {
       const Frag f = VTile::across(lds_v, wave, kb);
       float x[PE], y[PE];
-      if constexpr (PE == 4) {
-        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-      } else {
-        const uint4 u4 = __builtin_bit_cast(uint4, f);
-        const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
-      }
+      unpack<DT>(f, x);
 #pragma unroll
       for (int e = 0; e < PE; ++e) {
         const int t = kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4;

@@ -7,12 +7,12 @@
 namespace cnhwc {
 namespace seq {
 
-// The form of a pass: 16-row tiles of a state, 64-column parts of a workgroup (1 or 2).
+// The form of a pass: 16-row tiles of a state, wavefronts of a workgroup, 16 columns each.
 template <typename F>
 void with_shape(int32_t dk, int32_t dv, F&& f) {
   auto wide = [&](auto dkt) {
-    if (dv <= 64) f(dkt, std::integral_constant<int, 1>{});
-    else f(dkt, std::integral_constant<int, 2>{});
+    if (dv <= 64) f(dkt, std::integral_constant<int, 4>{});
+    else f(dkt, std::integral_constant<int, 8>{});
   };
   if (dk <= 32) wide(std::integral_constant<int, 2>{});
   else if (dk <= 64) wide(std::integral_constant<int, 4>{});
@@ -38,13 +38,13 @@ inline void cut_runs(Cut& c, int64_t l, int64_t all, int64_t room) {
 template <int DT>
 Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64_t passes) {
   Cut c{};
-  with_shape(dk, dv, [&](auto dkt, auto nt) {
-    constexpr int DKT = decltype(dkt)::value, NT = decltype(nt)::value;
-    using Sh = ChunkShape<DT, DKT, NT>;
+  with_shape(dk, dv, [&](auto dkt, auto w) {
+    constexpr int DKT = decltype(dkt)::value, W = decltype(w)::value;
+    using Sh = ChunkShape<DT, DKT, W>;
     c.chunk = Sh::kChunk;
-    c.parts = (dv + 64 * NT - 1) / (64 * NT);
-    c.per = c.parts * 4 * DKT * NT * 64;
-    cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kOccupancy);
+    c.parts = (dv + Sh::kCols - 1) / Sh::kCols;
+    c.per = c.parts * W * DKT * 64;
+    cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kGroups);
   });
   c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16;
   return c;

@@ -15,22 +15,22 @@ hipError_t launch_passes(Passes<DT>& ps, int count, LaGeo g, const Cut& c, int64
   for (int i = 0; i < count; ++i) {
     Pass<DT>& p = ps.p[i];
     vec = vec && whole(p.q, p.qs, p.dk, kPiece, es) && whole(p.k, p.ks, p.dk, kPiece, es) &&
-          whole(p.v, p.vs, p.dv, kPiece, es) && aligned(p.y, 4 * es);
+          whole(p.v, p.vs, p.dv, kPiece, es) && aligned(p.y, 4 * es) && int64_t(g.h) * p.dv < (1 << 23);
     p.kept = reinterpret_cast<float4*>(workspace + i * c.bytes);
   }
-  with_shape(ps.p[0].dk, ps.p[0].dv, [&](auto dkt, auto nt) {
-    constexpr int DKT = decltype(dkt)::value, NT = decltype(nt)::value;
+  with_shape(ps.p[0].dk, ps.p[0].dv, [&](auto dkt, auto w) {
+    constexpr int DKT = decltype(dkt)::value, W = decltype(w)::value;
     const int64_t blocks = heads * c.parts;
     auto run = [&](auto v) {
       constexpr bool VEC = decltype(v)::value;
       if (c.runs > 1) {
-        hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, NT, true, VEC>), dim3(unsigned(blocks * (c.runs - 1)), count),
-                           dim3(256), 0, st, ps, g);
+        hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, W, true, VEC>), dim3(unsigned(blocks * (c.runs - 1)), count),
+                           dim3(64 * W), 0, st, ps, g);
         const int64_t total = heads * c.per;
         hipLaunchKernelGGL((la_join_kernel<DT>), dim3(grid_of(ceil_div(total, int64_t(256))).x, count), dim3(256), 0,
                            st, ps, g, heads, c.per, c.chunk);
       }
-      hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, NT, false, VEC>), dim3(unsigned(blocks * c.runs), count), dim3(256),
+      hipLaunchKernelGGL((la_chunk_kernel<DT, DKT, W, false, VEC>), dim3(unsigned(blocks * c.runs), count), dim3(64 * W),
                          0, st, ps, g);
     };
     if (vec) run(std::true_type{});
