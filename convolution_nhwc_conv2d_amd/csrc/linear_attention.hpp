@@ -152,11 +152,14 @@ __device__ __forceinline__ void unpack(const typename Mma<DT>::Frag& f, float (&
 }
 
 // A tile of CH positions by COLS channels on its way from memory into LDS, rows of
-// positions.  fp32: 16 bytes behind each row, so that the 16 rows that are read
-// together lie in different banks.  bf16: 32 bytes, which does it for the reads across
-// the rows (4 rows of 32 bytes), and in every second eight rows the 8-byte pieces
-// change places in pairs, which does it for the reads along them (16 rows of 8).
-template <int DT, int COLS, int CH, int THREADS>
+// positions.  DEPTH: its channels are the depth of a product, and in bf16 each 32 of them
+// stand in the order of the lanes (element 16 i + 4 g + r at 8 g + 4 i + r), so that an
+// operand is one read of 16 bytes.  (In their own order it would be two of 8, which the
+// compiler joins into a ds_read2_b64: 16 cycles a wavefront, where a ds_read_b128 takes 4
+// and a transposing read 2.)  Behind a row 32 bytes in bf16 and 16 in fp32: the
+// rows that are read together then lie in different banks (but for the transposing
+// reads of a DEPTH tile, two to a bank, 4 cycles).
+template <int DT, int COLS, int CH, int THREADS, bool DEPTH>
 struct Rows2D {
   using M = Mma<DT>;
   using T = typename M::T;
@@ -168,8 +171,6 @@ struct Rows2D {
   static_assert(kCount == 1 || !kSome, "whole pieces for every thread");
   using Raw = PackBits<DT, kPiece>;  // held whole: as elements they would be taken apart on arrival
   Raw v[kCount];
-
-  static __device__ __forceinline__ int swap(int row) { return kHalf ? row & 8 : 0; }  // in bytes
 
   // Rows past `valid` and channels past `cols` are not read: VEC (whole pieces, 64 rows
   // within 32 bits of an offset) reads others instead, without a branch for every piece;
@@ -215,46 +216,38 @@ struct Rows2D {
         *reinterpret_cast<float4*>(p + col * 4) =
             make_float4(to_f<DT>(x.e[0]), to_f<DT>(x.e[1]), to_f<DT>(x.e[2]), to_f<DT>(x.e[3]));
       } else {
-        const uint4 x = v[i];
-        *reinterpret_cast<uint2*>(p + ((col * 2) ^ swap(row))) = make_uint2(x.x, x.y);
-        *reinterpret_cast<uint2*>(p + ((col * 2 + 8) ^ swap(row))) = make_uint2(x.z, x.w);
+        if constexpr (DEPTH) {
+          char* o = p + (col & ~31) * 2 + (col & 8) * 4 + (col & 16) / 2;
+          *reinterpret_cast<uint2*>(o) = make_uint2(v[i].x, v[i].y);
+          *reinterpret_cast<uint2*>(o + 16) = make_uint2(v[i].z, v[i].w);
+        } else {
+          *reinterpret_cast<uint4*>(p + col * 2) = v[i];
+        }
       }
     }
   }
 
   // The operand whose rows (or columns) are this tile's rows 16 i + (lane & 15), depth block kb.
   static __device__ __forceinline__ typename M::Frag along(const char* lds, int i, int kb) {
-    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const char* p = lds + (16 * i + c) * kStride + kb * 64;
-    if constexpr (!kHalf) {
-      return *reinterpret_cast<const float4*>(p + g * 16);
-    } else {
-      p += (g * 8) ^ swap(c);
-      const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 32);
-      return make_uint4(a.x, a.y, b.x, b.y);
-    }
+    static_assert(DEPTH, "the order of the lanes");
+    const int lane = threadIdx.x & 63;
+    return *reinterpret_cast<const typename M::Frag*>(lds + (16 * i + (lane & 15)) * kStride + kb * 64 + (lane >> 4) * 16);
   }
   // Stores what along() reads, for the 16 rows that the lanes are.
   static __device__ __forceinline__ void put(char* lds, int i, int kb, const typename M::Frag& f) {
-    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    char* p = lds + (16 * i + c) * kStride + kb * 64;
-    if constexpr (!kHalf) {
-      *reinterpret_cast<float4*>(p + g * 16) = f;
-    } else {
-      p += (g * 8) ^ swap(c);
-      *reinterpret_cast<uint2*>(p) = make_uint2(f.x, f.y);
-      *reinterpret_cast<uint2*>(p + 32) = make_uint2(f.z, f.w);
-    }
+    const int lane = threadIdx.x & 63;
+    *reinterpret_cast<typename M::Frag*>(lds + (16 * i + (lane & 15)) * kStride + kb * 64 + (lane >> 4) * 16) = f;
   }
   // Channels 16 j + 4 g ... of position 16 i + c.
   static __device__ __forceinline__ void four(const char* lds, int i, int j, float (&x)[4]) {
+    static_assert(DEPTH, "the order of the lanes");
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const char* p = lds + (16 * i + c) * kStride;
     if constexpr (!kHalf) {
       const float4 f = *reinterpret_cast<const float4*>(p + j * 64 + g * 16);
       x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
     } else {
-      const uint2 f = *reinterpret_cast<const uint2*>(p + j * 32 + ((g * 8) ^ swap(c)));
+      const uint2 f = *reinterpret_cast<const uint2*>(p + (j >> 1) * 64 + g * 16 + (j & 1) * 8);
       x[0] = low2(f.x), x[1] = high2(f.x), x[2] = low2(f.y), x[3] = high2(f.y);
     }
   }
@@ -270,8 +263,8 @@ struct Rows2D {
     } else {
       typedef short v4s __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) v4s lds_v4s;
-      const int row = 4 * g + (c >> 2);
-      const char* p = lds + (32 * kb + row) * kStride + j * 32 + (((c & 3) * 8) ^ swap(row));
+      const int at = DEPTH ? (j >> 1) * 64 + (c & 3) * 16 + (j & 1) * 8 : j * 32 + (c & 3) * 8;
+      const char* p = lds + (32 * kb + 4 * g + (c >> 2)) * kStride + at;
       const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
       const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 16 * kStride));
       const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
@@ -320,9 +313,9 @@ struct ChunkShape {
   static constexpr int kDepth = DKT * 16 / M::kDeep;          // blocks of a state's rows
   static constexpr int kBlocks = kChunk / M::kDeep;           // blocks of positions
   static constexpr int kPerBlock = M::kDeep / 16;             // 16-row tiles of a block
-  using KTile = Rows2D<DT, DKT * 16, kChunk, kThreads>;       // q and k
-  using VTile = Rows2D<DT, kCols, kChunk, kThreads>;
-  using PTile = Rows2D<DT, kChunk, kChunk, kThreads>;
+  using KTile = Rows2D<DT, DKT * 16, kChunk, kThreads, true>;       // q and k
+  using VTile = Rows2D<DT, kCols, kChunk, kThreads, false>;
+  using PTile = Rows2D<DT, kChunk, kChunk, kThreads, true>;
   static constexpr int kLds = 2 * KTile::kBytes + VTile::kBytes + PTile::kBytes;
   static constexpr int kGroups = kLds <= 78 * 1024 ? 2 : 1;   // workgroups of a compute unit
   static constexpr int kWaves = kGroups * W / 4;              // wavefronts of a SIMD
@@ -650,8 +643,8 @@ struct DecayPass {
 template <int DT, int DKT>
 struct DecayShape {
   static constexpr int kChunk = sizeof(typename Mma<DT>::T) == 4 && DKT == 16 ? 32 : 64;
-  using KTile = Rows2D<DT, DKT * 16, kChunk, 256>;
-  using VTile = Rows2D<DT, 64, kChunk, 256>;
+  using KTile = Rows2D<DT, DKT * 16, kChunk, 256, true>;
+  using VTile = Rows2D<DT, 64, kChunk, 256, true>;
   static constexpr int kLds = 2 * KTile::kBytes + 2 * VTile::kBytes;
   static constexpr int kOccupancy = kLds <= 76 * 1024 && DKT <= 8 ? 2 : 1;
 };
