@@ -41,6 +41,7 @@ struct Pass {
   int32_t dk, dv;
   bool back;               // positions from the end, the state decays after its use
   float scale_k, scale_y;  // of what enters the state, of what leaves it
+  bool halves;             // where not whole 16-byte pieces can be loaded: 8-byte ones can
   float4* kept;            // the states that enter all runs of chunks but the first, in lane order
 };
 
@@ -81,16 +82,46 @@ struct Decay {
   }
 };
 
-// What the matrix products are made of.  bf16: operands as they are, 32 deep; an
-// fp32 operand is one to three bf16 terms (8 digits each).  Otherwise fp32, 16 deep
-// in four instructions.  The depth runs over the lanes' four groups g in an order
-// that the accumulators have (16 i + 4 g + r): a lane's elements are rows
-// 4 g ... 4 g + 3 of one 16-row tile (fp32), or of two (bf16).
-template <int DT>
+// What the matrix products are made of.  bf16 and f16: operands as they are, 32 deep; an
+// fp32 operand is one or several 16-bit terms that add up to it (8 or 11 digits each).
+// fp32: 16 deep in four instructions.  The depth runs over the lanes' four groups g in
+// the order that the accumulators have (16 i + 4 g + r): a lane's elements are rows
+// 4 g ... 4 g + 3 of one 16-row tile (fp32), or of two (16 bits).
+template <int CT>
 struct Mma {
+  using T = uint16_t;
+  using Frag = uint4;
+  static constexpr bool kBf16 = CT == CNHWC_BF16;
+  static constexpr int kDeep = 32, kPiece = 8, kTerms = kBf16 ? 3 : 2;
+  static constexpr bool kScaled = !kBf16;  // fp32 operands are brought into f16's range first
+  static __device__ __forceinline__ void mul(const Frag& a, const Frag& b, v4f& c) {
+    if constexpr (kBf16)
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+    else
+      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
+  // Two floats in one conversion, the first in the lower half; and back.
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    if constexpr (kBf16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2h));
+  }
+  static __device__ __forceinline__ float low(uint32_t v) {
+    if constexpr (kBf16) return __builtin_bit_cast(float, v << 16);
+    else return to_f<CNHWC_F16>(uint16_t(v));
+  }
+  static __device__ __forceinline__ float high(uint32_t v) {
+    if constexpr (kBf16) return __builtin_bit_cast(float, v & 0xffff0000u);
+    else return to_f<CNHWC_F16>(uint16_t(v >> 16));
+  }
+};
+template <>
+struct Mma<CNHWC_F32> {
   using T = float;
   using Frag = float4;
   static constexpr int kDeep = 16, kPiece = 4, kTerms = 1;
+  static constexpr bool kScaled = false;
   static __device__ __forceinline__ void mul(const Frag& a, const Frag& b, v4f& c) {
     c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x, b.x, c, 0, 0, 0);
     c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.y, b.y, c, 0, 0, 0);
@@ -98,30 +129,14 @@ struct Mma {
     c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.w, b.w, c, 0, 0, 0);
   }
 };
-template <>
-struct Mma<CNHWC_BF16> {
-  using T = uint16_t;
-  using Frag = uint4;
-  static constexpr int kDeep = 32, kPiece = 8, kTerms = 3;
-  static __device__ __forceinline__ void mul(const Frag& a, const Frag& b, v4f& c) {
-    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
-  }
-};
 
-// Two floats as bf16 in one conversion, the first in the lower half; and back.
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
-}
-__device__ __forceinline__ float low2(uint32_t v) { return __builtin_bit_cast(float, v << 16); }
-__device__ __forceinline__ float high2(uint32_t v) { return __builtin_bit_cast(float, v & 0xffff0000u); }
-
-// An operand of kPiece floats as TERMS operands that add up to it.
-template <int DT, int TERMS, int P>
-__device__ __forceinline__ void split(const float (&x)[P], typename Mma<DT>::Frag (&f)[TERMS]) {
+// An operand of P floats as TERMS operands that add up to it.
+template <int CT, int TERMS, int P>
+__device__ __forceinline__ void split(const float (&x)[P], typename Mma<CT>::Frag (&f)[TERMS]) {
   if constexpr (P == 4) {
     f[0] = make_float4(x[0], x[1], x[2], x[3]);
   } else {
+    using M = Mma<CT>;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = x[i];
@@ -130,8 +145,8 @@ __device__ __forceinline__ void split(const float (&x)[P], typename Mma<DT>::Fra
       uint32_t p[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = pack2(v[2 * i], v[2 * i + 1]);
-        if (t + 1 < TERMS) v[2 * i] -= low2(p[i]), v[2 * i + 1] -= high2(p[i]);
+        p[i] = M::pack(v[2 * i], v[2 * i + 1]);
+        if (t + 1 < TERMS) v[2 * i] -= M::low(p[i]), v[2 * i + 1] -= M::high(p[i]);
       }
       f[t] = make_uint4(p[0], p[1], p[2], p[3]);
     }
@@ -139,17 +154,33 @@ __device__ __forceinline__ void split(const float (&x)[P], typename Mma<DT>::Fra
 }
 
 // An operand's elements as floats.
-template <int DT, int P>
-__device__ __forceinline__ void unpack(const typename Mma<DT>::Frag& f, float (&x)[P]) {
+template <int CT, int P>
+__device__ __forceinline__ void unpack(const typename Mma<CT>::Frag& f, float (&x)[P]) {
   if constexpr (P == 4) {
     x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
   } else {
-    const uint32_t u[4] = {__builtin_bit_cast(uint4, f).x, __builtin_bit_cast(uint4, f).y, __builtin_bit_cast(uint4, f).z,
-                           __builtin_bit_cast(uint4, f).w};
+    const uint32_t u[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[2 * e] = low2(u[e]), x[2 * e + 1] = high2(u[e]);
+    for (int e = 0; e < 4; ++e) x[2 * e] = Mma<CT>::low(u[e]), x[2 * e + 1] = Mma<CT>::high(u[e]);
   }
 }
+
+// Powers of two that bring fp32 values into f16's range and back: the largest of them to
+// [2^14, 2^15), so that what is 2^28 times smaller still has all its digits.  Infinities
+// and NaN are passed over: the values beside them keep theirs.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = __builtin_fabsf(x);
+  return a <= FLT_MAX ? a : 0.0f;
+}
+struct Range {
+  float in, out;
+  __device__ __forceinline__ explicit Range(float largest) {
+    int e = 15 - __builtin_amdgcn_frexp_expf(largest);
+    e = e < -110 ? -110 : e > 110 ? 110 : e;
+    in = __builtin_bit_cast(float, (127 + e) << 23);
+    out = __builtin_bit_cast(float, (127 - e) << 23);
+  }
+};
 
 // A tile of CH positions by COLS channels on its way from memory into LDS, rows of
 // positions.  DEPTH: its channels are the depth of a product, and in bf16 each 32 of them
@@ -159,9 +190,9 @@ __device__ __forceinline__ void unpack(const typename Mma<DT>::Frag& f, float (&
 // and a transposing read 2.)  Behind a row 32 bytes in bf16 and 16 in fp32: the
 // rows that are read together then lie in different banks (but for the transposing
 // reads of a DEPTH tile, two to a bank, 4 cycles).
-template <int DT, int COLS, int CH, int THREADS, bool DEPTH>
+template <int DT, int CT, int COLS, int CH, int THREADS, bool DEPTH>
 struct Rows2D {
-  using M = Mma<DT>;
+  using M = Mma<CT>;
   using T = typename M::T;
   static constexpr int kPiece = M::kPiece, kPer = COLS / kPiece, kStep = THREADS / kPer;
   static constexpr int kCount = (CH + kStep - 1) / kStep;  // pieces of a thread; of some of the threads where
@@ -174,10 +205,10 @@ struct Rows2D {
 
   // Rows past `valid` and channels past `cols` are not read: VEC (whole pieces, 64 rows
   // within 32 bits of an offset) reads others instead, without a branch for every piece;
-  // store() leaves them out.
+  // store() leaves them out.  halves: of 16-bit elements four at a time can be read.
   template <bool VEC>
   __device__ __forceinline__ void load(const Elem<DT>* __restrict__ base, int64_t stride, int32_t cols,
-                                       int32_t valid) {
+                                       int32_t valid, bool halves) {
     const int row0 = int(threadIdx.x) / kPer, col = int(threadIdx.x) % kPer * kPiece;
     const uint32_t at = uint32_t(col < cols ? col : 0), last = uint32_t(valid - 1);
 #pragma unroll
@@ -189,9 +220,19 @@ struct Rows2D {
         Pack<DT, kPiece> x{};
         if (row <= last) {
           const Elem<DT>* p = base + row * stride + col;
+          if (kPiece == 8 && halves) {
 #pragma unroll
-          for (int e = 0; e < kPiece; ++e)
-            if (col + e < cols) x.e[e] = p[e];
+            for (int e = 0; e < kPiece; e += 4)
+              if (col + e < cols) {
+                const Pack<DT, 4> y = load_pack<DT, 4>(p + e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x.e[e + k] = y.e[k];
+              }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e)
+              if (col + e < cols) x.e[e] = p[e];
+          }
         }
         v[i] = __builtin_bit_cast(Raw, x);
       }
@@ -248,7 +289,7 @@ struct Rows2D {
       x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
     } else {
       const uint2 f = *reinterpret_cast<const uint2*>(p + (j >> 1) * 64 + g * 16 + (j & 1) * 8);
-      x[0] = low2(f.x), x[1] = high2(f.x), x[2] = low2(f.y), x[3] = high2(f.y);
+      x[0] = M::low(f.x), x[1] = M::high(f.x), x[2] = M::low(f.y), x[3] = M::high(f.y);
     }
   }
 
@@ -281,6 +322,7 @@ struct Powers {
   float rise[CH];       // exp(g (i + 1))
   float fall[2 * CH];   // exp(g (CH - 1 - i)); 0 from CH on
   float far[2 * CH];    // exp(g |i - CH|)
+  float row[CH];        // f16: what brings a row of products of q and k back from its range
 
   // by: a factor of the ways to the end and of those between positions
   __device__ __forceinline__ void fill(float gd, float by, bool back) {
@@ -313,11 +355,13 @@ struct ChunkShape {
   static constexpr int kDepth = DKT * 16 / M::kDeep;          // blocks of a state's rows
   static constexpr int kBlocks = kChunk / M::kDeep;           // blocks of positions
   static constexpr int kPerBlock = M::kDeep / 16;             // 16-row tiles of a block
-  using KTile = Rows2D<DT, DKT * 16, kChunk, kThreads, true>;       // q and k
-  using VTile = Rows2D<DT, kCols, kChunk, kThreads, false>;
-  using PTile = Rows2D<DT, kChunk, kChunk, kThreads, true>;
+  using KTile = Rows2D<DT, DT, DKT * 16, kChunk, kThreads, true>;       // q and k
+  using VTile = Rows2D<DT, DT, kCols, kChunk, kThreads, false>;
+  using PTile = Rows2D<DT, DT, kChunk, kChunk, kThreads, true>;
   static constexpr int kLds = 2 * KTile::kBytes + VTile::kBytes + PTile::kBytes;
-  static constexpr int kGroups = kLds <= 78 * 1024 ? 2 : 1;   // workgroups of a compute unit
+  // workgroups of a compute unit: 128 registers hold 128 rows of a state (64 beside fp32) and what goes with
+  // them, 256 rows take more
+  static constexpr int kGroups = kLds <= 78 * 1024 && DKT * W <= (sizeof(typename M::T) == 2 ? 64 : 32) ? 2 : 1;
   static constexpr int kWaves = kGroups * W / 4;              // wavefronts of a SIMD
 };
 
@@ -399,9 +443,9 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
   auto fetch = [&](int32_t i) {
     const int32_t valid = valid_at(i);
     const int64_t t0 = int64_t(chunk_at(i)) * CH;
-    tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid);
-    tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid);
-    if constexpr (!LOCAL) tq.template load<VEC>(qn + t0 * p.qs[1], p.qs[1], p.dk, valid);
+    tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid, p.halves);
+    tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid, p.halves);
+    if constexpr (!LOCAL) tq.template load<VEC>(qn + t0 * p.qs[1], p.qs[1], p.dk, valid, p.halves);
   };
   if (count > 0) fetch(0);
   if constexpr (!LOCAL) {
@@ -484,6 +528,16 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
             x[4 * i + r] = (BACK ? far > r : far < r) ? 0.0f : acc[r] * by;
           }
         }
+        if constexpr (M::kScaled) {
+          static_assert(Sh::kBlocks == 1, "a row of products lies in one wavefront");
+          float largest = 0.0f;
+#pragma unroll
+          for (int e = 0; e < PE; ++e) largest = __builtin_fmaxf(largest, finite_abs(x[e]));
+          const Range to(max_halves(max_row_pairs(largest)));
+#pragma unroll
+          for (int e = 0; e < PE; ++e) x[e] *= to.in;
+          if (g4 == 0) power.row[16 * u + c] = to.out;
+        }
         Frag f[1];
         split<DT>(x, f);
         PTile::put(lds_p, u, b, f[0]);
@@ -491,11 +545,20 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
       // ---- S^T q^T, decayed from the chunk's start
 #pragma unroll
       for (int m = 0; m < MT; ++m) o[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      Range of_s(1.0f);
+      if constexpr (M::kScaled) {
+        float largest = 0.0f;
+#pragma unroll
+        for (int a = 0; a < DKT; ++a)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) largest = __builtin_fmaxf(largest, finite_abs(s[a][r]));
+        of_s = Range(group_max<64>(largest));
+      }
 #pragma unroll
       for (int kb = 0; kb < Sh::kDepth; ++kb) {
         float x[PE];
 #pragma unroll
-        for (int e = 0; e < PE; ++e) x[e] = s[kb * PB + e / 4][e % 4];
+        for (int e = 0; e < PE; ++e) x[e] = s[kb * PB + e / 4][e % 4] * (M::kScaled ? of_s.in : 1.0f);
         Frag st[1];
         split<DT>(x, st);
 #pragma unroll
@@ -503,7 +566,7 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
       }
       const float* const from_start = power.from_start(BACK, valid) + c;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) o[m] *= from_start[16 * m];
+      for (int m = 0; m < MT; ++m) o[m] *= from_start[16 * m] * (M::kScaled ? of_s.out : 1.0f);
       __syncthreads();  // the products of q and k are there
     }
 
@@ -513,19 +576,28 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
 
     if constexpr (!LOCAL) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
+        v4f acc = M::kScaled ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : o[m];
 #pragma unroll
         for (int kb = 0; kb < Sh::kBlocks; ++kb) {
           if (BACK ? kb < m / PB : kb > m / PB) continue;
-          M::mul(vf[kb], PTile::along(lds_p, m, kb), o[m]);
+          M::mul(vf[kb], PTile::along(lds_p, m, kb), acc);
         }
+        if constexpr (M::kScaled) {
+          const float by = power.row[16 * m + c];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[m][r] = __builtin_fmaf(acc[r], by, o[m][r]);
+        } else {
+          o[m] = acc;
+        }
+      }
       // ---- y, to be stored when the next chunk has arrived: the wait for that chunk
       // would be for these stores too
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const v4f f = o[m] * p.scale_y;
-        if constexpr (DT == CNHWC_BF16) {
-          out[m] = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+        if constexpr (DT != CNHWC_F32) {
+          out[m] = make_uint2(M::pack(f[0], f[1]), M::pack(f[2], f[3]));
         } else {
           Pack<DT, 4> x;
 #pragma unroll
@@ -545,13 +617,29 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
       unpack<DT>(vf[kb], x);
 #pragma unroll
       for (int e = 0; e < PE; ++e) x[e] *= to_end[kb * M::kDeep + (e / 4) * 16 + e % 4];
+      Range of_v(1.0f);  // of the lane's column, which is the state's
+      if constexpr (M::kScaled) {
+        float largest = 0.0f;
+#pragma unroll
+        for (int e = 0; e < PE; ++e) largest = __builtin_fmaxf(largest, finite_abs(x[e]));
+        of_v = Range(max_halves(max_row_pairs(largest)));
+#pragma unroll
+        for (int e = 0; e < PE; ++e) x[e] *= of_v.in;
+      }
       Frag vt[M::kTerms];
       split<DT>(x, vt);
 #pragma unroll
       for (int a = 0; a < DKT; ++a) {
         const Frag f = KTile::across(lds_k, a, kb);
+        v4f acc = M::kScaled ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : s[a];
 #pragma unroll
-        for (int t = 0; t < M::kTerms; ++t) M::mul(f, vt[t], s[a]);
+        for (int t = 0; t < M::kTerms; ++t) M::mul(f, vt[t], acc);
+        if constexpr (M::kScaled) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[a][r] = __builtin_fmaf(acc[r], of_v.out, s[a][r]);
+        } else {
+          s[a] = acc;
+        }
       }
     }
   }
@@ -642,9 +730,10 @@ struct DecayPass {
 
 template <int DT, int DKT>
 struct DecayShape {
-  static constexpr int kChunk = sizeof(typename Mma<DT>::T) == 4 && DKT == 16 ? 32 : 64;
-  using KTile = Rows2D<DT, DKT * 16, kChunk, 256, true>;
-  using VTile = Rows2D<DT, 64, kChunk, 256, true>;
+  static constexpr int CT = DT == CNHWC_F16 ? CNHWC_F32 : DT;  // f16 is taken in fp32
+  static constexpr int kChunk = sizeof(typename Mma<CT>::T) == 4 && DKT == 16 ? 32 : 64;
+  using KTile = Rows2D<DT, CT, DKT * 16, kChunk, 256, true>;
+  using VTile = Rows2D<DT, CT, 64, kChunk, 256, true>;
   static constexpr int kLds = 2 * KTile::kBytes + 2 * VTile::kBytes;
   static constexpr int kOccupancy = kLds <= 76 * 1024 && DKT <= 8 ? 2 : 1;
 };
@@ -653,7 +742,8 @@ template <int DT, int DKT, bool LOCAL, bool VEC>
 __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_decay_kernel(DecayPass<DT> pass,
                                                                                          LaGeo g) {
   using Sh = DecayShape<DT, DKT>;
-  using M = Mma<DT>;
+  constexpr int CT = Sh::CT;
+  using M = Mma<CT>;
   using Frag = typename M::Frag;
   using KTile = typename Sh::KTile;
   using VTile = typename Sh::VTile;
@@ -713,11 +803,11 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
   auto fetch = [&](int32_t chunk) {
     const int64_t t0 = int64_t(chunk) * CH;
     const int32_t valid = len - t0 > CH ? CH : int32_t(len - t0);
-    tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid);
-    tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid);
+    tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid, p.halves);
+    tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid, p.halves);
     if constexpr (!LOCAL) {
-      tq.template load<VEC>(qn + t0 * p.qs[1], p.qs[1], p.dk, valid);
-      td.template load<VEC>(dn + t0 * pass.dys[1], pass.dys[1], p.dv - col0, valid);
+      tq.template load<VEC>(qn + t0 * p.qs[1], p.qs[1], p.dk, valid, p.halves);
+      td.template load<VEC>(dn + t0 * pass.dys[1], pass.dys[1], p.dv - col0, valid, p.halves);
     }
   };
   if (chunk_lo < chunk_hi) fetch(chunk_lo);
@@ -764,8 +854,8 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
 #pragma unroll
         for (int e = 0; e < PE; ++e) fs[e] = s[kb * PB + e / 4][e % 4], ft[e] = grow[kb * PB + e / 4][e % 4];
         Frag a[TERMS], b[TERMS];
-        split<DT>(fs, a);
-        split<DT>(ft, b);
+        split<CT>(fs, a);
+        split<CT>(ft, b);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const Frag f = KTile::along(lds_q, m, kb);
@@ -804,7 +894,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
     for (int kb = 0; kb < kBlocks; ++kb) {
       const Frag f = VTile::across(lds_v, wave, kb);
       float x[PE], y[PE];
-      unpack<DT>(f, x);
+      unpack<CT>(f, x);
 #pragma unroll
       for (int e = 0; e < PE; ++e) {
         const int t = kb * M::kDeep + (e / 4) * 16 + 4 * g4 + e % 4;
@@ -812,8 +902,8 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
         y[e] = x[e] * float(valid - 1 - t);
       }
       Frag vs[TERMS], vt[TERMS];
-      split<DT>(x, vs);
-      split<DT>(y, vt);
+      split<CT>(x, vs);
+      split<CT>(y, vt);
 #pragma unroll
       for (int a = 0; a < DKT; ++a) {
         const Frag k = KTile::across(lds_k, a, kb);

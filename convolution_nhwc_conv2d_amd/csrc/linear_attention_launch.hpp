@@ -11,13 +11,15 @@ hipError_t launch_passes(Passes<DT>& ps, int count, LaGeo g, const Cut& c, int64
   const uint64_t es = sizeof(Elem<DT>);
   constexpr int kPiece = Mma<DT>::kPiece;
   g.chunks = c.chunks, g.run = c.run, g.runs = c.runs;
-  bool vec = true;
+  bool vec = true, halves = true;
   for (int i = 0; i < count; ++i) {
     Pass<DT>& p = ps.p[i];
     vec = vec && whole(p.q, p.qs, p.dk, kPiece, es) && whole(p.k, p.ks, p.dk, kPiece, es) &&
           whole(p.v, p.vs, p.dv, kPiece, es) && aligned(p.y, 4 * es) && int64_t(g.h) * p.dv < (1 << 23);
+    halves = halves && whole(p.q, p.qs, p.dk, 4, es) && whole(p.k, p.ks, p.dk, 4, es) && whole(p.v, p.vs, p.dv, 4, es);
     p.kept = reinterpret_cast<float4*>(workspace + i * c.bytes);
   }
+  for (int i = 0; i < count; ++i) ps.p[i].halves = halves;
   with_shape(ps.p[0].dk, ps.p[0].dv, [&](auto dkt, auto w) {
     constexpr int DKT = decltype(dkt)::value, W = decltype(w)::value;
     const int64_t blocks = heads * c.parts;
@@ -60,11 +62,13 @@ template <int DT>
 hipError_t launch_decay(DecayPass<DT>& pass, LaGeo g, const Cut& c, int64_t heads, char* workspace, float* out,
                         hipStream_t st) {
   const uint64_t es = sizeof(Elem<DT>);
-  constexpr int kPiece = Mma<DT>::kPiece;
+  constexpr int kPiece = Mma<DT == CNHWC_F16 ? CNHWC_F32 : DT>::kPiece;
   g.chunks = c.chunks, g.run = c.run, g.runs = c.runs;
   Pass<DT>& p = pass.a;
   const bool vec = whole(p.q, p.qs, p.dk, kPiece, es) && whole(p.k, p.ks, p.dk, kPiece, es) &&
                    whole(p.v, p.vs, p.dv, kPiece, es) && whole(pass.dy, pass.dys, p.dv, kPiece, es);
+  p.halves = whole(p.q, p.qs, p.dk, 4, es) && whole(p.k, p.ks, p.dk, 4, es) && whole(p.v, p.vs, p.dv, 4, es) &&
+             whole(pass.dy, pass.dys, p.dv, 4, es);
   const uint64_t states = uint64_t(heads) * (c.runs - 1) * c.per * 16;
   p.kept = reinterpret_cast<float4*>(workspace);
   pass.sums = reinterpret_cast<float*>(workspace + states);
