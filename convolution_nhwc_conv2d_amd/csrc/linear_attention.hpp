@@ -732,15 +732,20 @@ template <int DT, int DKT>
 struct DecayShape {
   static constexpr int CT = DT == CNHWC_F16 ? CNHWC_F32 : DT;  // f16 is taken in fp32
   static constexpr int kChunk = sizeof(typename Mma<CT>::T) == 4 && DKT == 16 ? 32 : 64;
-  using KTile = Rows2D<DT, CT, DKT * 16, kChunk, 256, true>;
-  using VTile = Rows2D<DT, CT, 64, kChunk, 256, true>;
+  // Four wavefronts of 16 columns, twice where the state has rows enough: one has the
+  // upper half of them, one the lower (every sum here is a sum over the rows too).  One
+  // workgroup of 64 columns a compute unit then has two wavefronts on a SIMD.
+  static constexpr int kSplit = DKT >= 4 ? 2 : 1, kTiles = DKT / kSplit, kThreads = 256 * kSplit;
+  using KTile = Rows2D<DT, CT, DKT * 16, kChunk, kThreads, true>;
+  using VTile = Rows2D<DT, CT, 64, kChunk, kThreads, true>;
   static constexpr int kLds = 2 * KTile::kBytes + 2 * VTile::kBytes;
-  static constexpr int kOccupancy = kLds <= 76 * 1024 && DKT <= 8 ? 2 : 1;
+  static constexpr int kGroups = (DKT == 2 || (DKT == 4 && sizeof(typename Mma<CT>::T) == 2)) && kLds <= 76 * 1024 ? 2 : 1;
 };
 
 template <int DT, int DKT, bool LOCAL, bool VEC>
-__global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_decay_kernel(DecayPass<DT> pass,
-                                                                                         LaGeo g) {
+__global__ __launch_bounds__((DecayShape<DT, DKT>::kThreads),
+                             (DecayShape<DT, DKT>::kGroups * DecayShape<DT, DKT>::kSplit)) void la_decay_kernel(
+    DecayPass<DT> pass, LaGeo g) {
   using Sh = DecayShape<DT, DKT>;
   constexpr int CT = Sh::CT;
   using M = Mma<CT>;
@@ -748,10 +753,10 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
   using KTile = typename Sh::KTile;
   using VTile = typename Sh::VTile;
   constexpr int CH = Sh::kChunk, MT = CH / 16, PE = M::kPiece, PB = M::kDeep / 16, TERMS = M::kTerms;
-  constexpr int kBlocks = CH / M::kDeep;
+  constexpr int kBlocks = CH / M::kDeep, TA = Sh::kTiles, KD = TA * 16 / M::kDeep;
   __shared__ __attribute__((aligned(16))) char lds[LOCAL ? KTile::kBytes + VTile::kBytes : Sh::kLds];
   __shared__ Powers<CH> power;
-  __shared__ float red[4];
+  __shared__ float red[4 * Sh::kSplit];
   char* const lds_k = lds;
   char* const lds_v = lds + KTile::kBytes;
   char* const lds_q = lds_v + VTile::kBytes;
@@ -759,7 +764,8 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
 
   const Pass<DT>& p = pass.a;
   const int lane = threadIdx.x & 63, c = lane & 15, g4 = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = every & 3, half = every >> 2;  // columns; rows of the states
   const int32_t parts = (p.dv + 63) / 64, part = int32_t(blockIdx.x % unsigned(parts));
   const int64_t row = blockIdx.x / unsigned(parts);
   const int32_t runs = LOCAL ? g.runs - 1 : g.runs;
@@ -773,19 +779,20 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
   const int32_t chunk_hi = used < chunk_lo ? chunk_lo : used < all_hi ? used : all_hi;
   const int32_t col0 = part * 64, j = col0 + wave * 16 + c;
 
-  v4f s[DKT], grow[DKT];  // rows 16 a + 4 g + r, column j
-  float4* const kept = p.kept + ((nh * (g.runs - 1) * parts + part) * 4 + wave) * (2 * DKT * 64) + lane;
+  v4f s[TA], grow[TA];  // rows row0 + 16 a + 4 g + r, column j
+  const int32_t row0 = half * TA * 16 + 4 * g4;
+  float4* const kept = p.kept + ((nh * (g.runs - 1) * parts + part) * (4 * Sh::kSplit) + every) * (2 * TA * 64) + lane;
   const int64_t kept_step = int64_t(parts) * 4 * (2 * DKT * 64);
   const float* st = p.state && run == 0 ? p.state + nh * p.dk * p.dv : nullptr;
 #pragma unroll
-  for (int a = 0; a < DKT; ++a) {
+  for (int a = 0; a < TA; ++a) {
     if (!LOCAL && run > 0) {
       s[a] = __builtin_bit_cast(v4f, kept[(run - 1) * kept_step + 2 * a * 64]);
       grow[a] = __builtin_bit_cast(v4f, kept[(run - 1) * kept_step + (2 * a + 1) * 64]);
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int32_t i = 16 * a + 4 * g4 + r;
+        const int32_t i = row0 + 16 * a + r;
         s[a][r] = st && i < p.dk && j < p.dv ? st[int64_t(i) * p.dv + j] : 0.0f;
         grow[a][r] = 0.0f;
       }
@@ -829,7 +836,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
       float sum = 0.0f;
       // ---- pairs of positions: the wavefront's 16 u = 16 wave + c, s = 16 i + 4 g + r
       if (wave < MT) {
-        for (int i = 0; i <= wave; ++i) {
+        for (int i = half; i <= wave; i += Sh::kSplit) {
           v4f x = {0.0f, 0.0f, 0.0f, 0.0f}, y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int kb = 0; kb < DKT * 16 / M::kDeep; ++kb)
@@ -849,7 +856,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
 #pragma unroll
       for (int m = 0; m < MT; ++m) xs[m] = ys[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int kb = 0; kb < DKT * 16 / M::kDeep; ++kb) {
+      for (int kb = 0; kb < KD; ++kb) {
         float fs[PE], ft[PE];
 #pragma unroll
         for (int e = 0; e < PE; ++e) fs[e] = s[kb * PB + e / 4][e % 4], ft[e] = grow[kb * PB + e / 4][e % 4];
@@ -858,7 +865,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
         split<CT>(ft, b);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const Frag f = KTile::along(lds_q, m, kb);
+          const Frag f = KTile::along(lds_q, m, half * KD + kb);
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) {
             M::mul(a[t], f, xs[m]);
@@ -884,7 +891,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
     // ---- both states to the chunk's end
     const Decay whole(gd * float(valid));
 #pragma unroll
-    for (int a = 0; a < DKT; ++a)
+    for (int a = 0; a < TA; ++a)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         grow[a][r] = whole(__builtin_fmaf(float(valid), s[a][r], grow[a][r]));
@@ -905,8 +912,8 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
       split<CT>(x, vs);
       split<CT>(y, vt);
 #pragma unroll
-      for (int a = 0; a < DKT; ++a) {
-        const Frag k = KTile::across(lds_k, a, kb);
+      for (int a = 0; a < TA; ++a) {
+        const Frag k = KTile::across(lds_k, half * TA + a, kb);
 #pragma unroll
         for (int t = 0; t < TERMS; ++t) {
           M::mul(k, vs[t], s[a]);
@@ -918,7 +925,7 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
 
   if constexpr (LOCAL) {
 #pragma unroll
-    for (int a = 0; a < DKT; ++a) {
+    for (int a = 0; a < TA; ++a) {
       kept[run * kept_step + 2 * a * 64] = __builtin_bit_cast(float4, s[a]);
       kept[run * kept_step + (2 * a + 1) * 64] = __builtin_bit_cast(float4, grow[a]);
     }
@@ -928,18 +935,23 @@ __global__ __launch_bounds__(256, (DecayShape<DT, DKT>::kOccupancy)) void la_dec
       const float* ds = pass.dstate + nh * p.dk * p.dv;
       float sum = 0.0f;
 #pragma unroll
-      for (int a = 0; a < DKT; ++a)
+      for (int a = 0; a < TA; ++a)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int32_t i = 16 * a + 4 * g4 + r;
+          const int32_t i = row0 + 16 * a + r;
           if (i < p.dk && j < p.dv) sum = __builtin_fmaf(ds[int64_t(i) * p.dv + j], grow[a][r], sum);
         }
       total += double(sum);
     }
     const float one = group_sum<64>(float(total));
-    if (lane == 0) red[wave] = one;
+    if (lane == 0) red[every] = one;
     __syncthreads();
-    if (threadIdx.x == 0) pass.sums[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+    if (threadIdx.x == 0) {
+      float sum = red[0];
+#pragma unroll
+      for (int w = 1; w < 4 * Sh::kSplit; ++w) sum += red[w];
+      pass.sums[blockIdx.x] = sum;
+    }
   }
 }
 

@@ -27,10 +27,16 @@ struct Cut {
   int32_t per;     // float4 of a head's state in lane order
   uint64_t bytes;
 };
+// More than one run costs a kernel over k and v, about 0.6 of the other one, and the
+// states between them: worth it up to five workgroups for eight compute units.
+// Measured (128 x 128 bf16, 2048 positions): 256 workgroups in one run 142 us, in two 180; 192
+// 133 and 160; 128 in four 111, in two 120, fp32 in one 376, in two 290; 64 x 64, 4096
+// positions, 64 workgroups in eight 57, in four 76.  At least three chunks to a run: 1 x 300 x 4
+// heads 17 us with three, 15 with two, 20 with four; 6 x 1023 x 5 heads fp32 38, 41, 37.
 inline void cut_runs(Cut& c, int64_t l, int64_t all, int64_t room) {
   c.chunks = int32_t((l + c.chunk - 1) / c.chunk);
-  int64_t runs = all * 2 > room ? 1 : room / all;
-  if (runs > c.chunks / 4) runs = c.chunks / 4;
+  int64_t runs = all > 160 ? 1 : room / all;
+  if (runs > c.chunks / 3) runs = c.chunks / 3;
   if (runs < 1) runs = 1;
   c.run = int32_t((c.chunks + runs - 1) / runs);
   c.runs = (c.chunks + c.run - 1) / c.run;
@@ -66,7 +72,7 @@ Cut decay_cut_of(const cnhwc_linear_attention_desc_t& d) {
     c.chunk = Sh::kChunk;
     c.parts = (d.dv + 63) / 64;
     c.per = c.parts * 4 * DKT * 64 * 2;
-    cut_runs(c, d.l, d.n * d.h * c.parts, 256 * Sh::kOccupancy);
+    cut_runs(c, d.l, d.n * d.h * c.parts, 256 * Sh::kGroups);
   });
   c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16 + (uint64_t(d.n) * d.h * c.parts * c.runs * 4 + 15) / 16 * 16;
   return c;

@@ -78,13 +78,13 @@ hipError_t launch_decay(DecayPass<DT>& pass, LaGeo g, const Cut& c, int64_t head
     auto run = [&](auto v) {
       constexpr bool VEC = decltype(v)::value;
       if (c.runs > 1) {
-        hipLaunchKernelGGL((la_decay_kernel<DT, DKT, true, VEC>), dim3(unsigned(blocks * (c.runs - 1))), dim3(256), 0,
-                           st, pass, g);
+        hipLaunchKernelGGL((la_decay_kernel<DT, DKT, true, VEC>), dim3(unsigned(blocks * (c.runs - 1))),
+                           dim3(DecayShape<DT, DKT>::kThreads), 0, st, pass, g);
         hipLaunchKernelGGL((la_decay_join_kernel<DT>), grid_of(ceil_div(heads * c.per / 2, int64_t(256))), dim3(256), 0,
                            st, pass, g, heads, c.per, c.chunk);
       }
-      hipLaunchKernelGGL((la_decay_kernel<DT, DKT, false, VEC>), dim3(unsigned(blocks * c.runs)), dim3(256), 0, st,
-                         pass, g);
+      hipLaunchKernelGGL((la_decay_kernel<DT, DKT, false, VEC>), dim3(unsigned(blocks * c.runs)),
+                         dim3(DecayShape<DT, DKT>::kThreads), 0, st, pass, g);
     };
     if (vec) run(std::true_type{});
     else run(std::false_type{});

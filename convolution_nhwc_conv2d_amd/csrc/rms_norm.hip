@@ -70,6 +70,14 @@ __device__ __forceinline__ void store_q8(uint8_t* p, const float (&v)[V]) {
   }
 }
 
+// v / scale to the last digit, so that an element in 8 bits is the nearest one but for
+// what v itself is off: the product with the inverse and what it leaves.  (An infinite
+// scale makes NaN of everything, as the product does.)
+__device__ __forceinline__ float over(float v, float scale, float inv) {
+  const float q = v * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, scale, v), inv, q);
+}
+
 __device__ __forceinline__ float scale_of(float largest) {
   const float s = largest / kQ8Max;
   return s < kScaleMin ? kScaleMin : s;
@@ -183,7 +191,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_fwd_kernel(RmsFwd<D
         of[i] = 0.0f;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          z[i * VE + e] *= rstd * wf[kHold ? i : 0][e];
+          z[i * VE + e] = z[i * VE + e] * rstd * wf[kHold ? i : 0][e];
           of[i] = __builtin_fmaxf(of[i], c0 < g.c ? __builtin_fabsf(z[i * VE + e]) : 0.0f);
         }
         largest = __builtin_fmaxf(largest, of[i]);
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void rms_fwd_kernel(RmsFwd<D
         const float scale = scale_of(of[i]), inv = 1.0f / scale;
         float v[VE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[e] = z[i * VE + e] * inv;
+        for (int e = 0; e < VE; ++e) v[e] = over(z[i * VE + e], scale, inv);
         store_q8<VE>(qr + c0, v);
         if ((c0 & inside) == 0) io.scale[row * groups + (c0 >> shift)] = scale;
       }
@@ -235,7 +243,7 @@ __global__ __launch_bounds__(1024) void rms_fwd_wide_kernel(RmsFwd<DT> io, RmsGe
     for (int64_t c = threadIdx.x; c < g.c; c += 1024) s = __builtin_fmaf(at(c), at(c), s);
     const float rstd = 1.0f / __builtin_sqrtf(row_sum<1024>(s, red, 0) * g.inv_c + g.eps);
     if (io.rstd && threadIdx.x == 0) io.rstd[row] = rstd;
-    auto y_at = [&](int64_t c, float z) { return z * (rstd * (io.w ? load_param<DT>(io.w, c, g.w_f32) : 1.0f)); };
+    auto y_at = [&](int64_t c, float z) { return z * rstd * (io.w ? load_param<DT>(io.w, c, g.w_f32) : 1.0f); };
     // one wavefront to a group, or all of them to the row
     const int32_t span = g.group ? g.group : g.c;
     const int32_t first = g.group ? threadIdx.x >> 6 : 0, next = g.group ? 16 : 1;
@@ -243,19 +251,19 @@ __global__ __launch_bounds__(1024) void rms_fwd_wide_kernel(RmsFwd<DT> io, RmsGe
     const int32_t groups = g.c / span;
     for (int32_t k = first; k < groups; k += next) {
       const int64_t c0 = int64_t(k) * span;
-      float inv = 1.0f;
+      float inv = 1.0f, scale = 1.0f;
       if constexpr (Q8) {
         float largest = 0.0f;
         for (int32_t c = lane; c < span; c += lanes)
           largest = __builtin_fmaxf(largest, __builtin_fabsf(y_at(c0 + c, at(c0 + c))));
-        const float scale = scale_of(g.group ? group_max<64>(largest) : row_max<1024>(largest, red, 1));
+        scale = scale_of(g.group ? group_max<64>(largest) : row_max<1024>(largest, red, 1));
         inv = 1.0f / scale;
         if (lane == 0) io.scale[row * groups + k] = scale;
       }
       for (int32_t c = lane; c < span; c += lanes) {
         const float z = at(c0 + c), v = y_at(c0 + c, z);
         if constexpr (Q8) {
-          const float one[1] = {v * inv};
+          const float one[1] = {over(v, scale, inv)};
           store_q8<1>(io.q + row * g.c + c0 + c, one);
         } else {
           io.y[row * g.c + c0 + c] = from_f<DT>(v);
