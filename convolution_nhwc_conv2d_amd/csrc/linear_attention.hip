@@ -21,56 +21,64 @@ namespace {
 // ---------------------------------------------------------------- position by position
 
 // A token of every sequence: a workgroup holds 64 columns of one head's state, 16 lanes by
-// four columns, 16 row groups, rows r, r + 16, ... of NI.  The state is the traffic,
-// read once and written once.
+// four columns, 16 row groups of NI consecutive rows.  The state is the traffic, read
+// once and written once: VEC with whole vectors of it, and of q and k, whose elements
+// one by one are as many loads as the state's vectors.
 template <int DT, int NI, bool VEC>
 __global__ __launch_bounds__(256) void la_step_kernel(Pass<DT> p, LaGeo g) {
   __shared__ float part[4][64];
   const int64_t nh = blockIdx.x;
   const int64_t n = nh / g.h, hd = nh - n * g.h;
-  const int j0 = int(blockIdx.y) * 64 + int(threadIdx.x & 15) * 4, r0 = threadIdx.x >> 4;
+  const int j0 = int(blockIdx.y) * 64 + int(threadIdx.x & 15) * 4, r0 = int(threadIdx.x >> 4) * NI;
   const int64_t base = nh * p.dk * p.dv;
-  float s[NI][4];
+  const Elem<DT>* qn = p.q + n * p.qs[0] + hd * p.qs[2] + r0;
+  const Elem<DT>* kn = p.k + n * p.ks[0] + hd * p.ks[2] + r0;
+  const Elem<DT>* vn = p.v + n * p.vs[0] + hd * p.vs[2] + j0;
+  float s[NI][4], v[4], k[NI], q[NI], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (VEC) {
+    constexpr int V = NI * sizeof(Elem<DT>) > 16 ? 16 / sizeof(Elem<DT>) : NI;
+    Pack<DT, V> kp[NI / V], qp[NI / V];
+    Pack<DT, 4> vp{};
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = r0 + 16 * i;
-    if constexpr (VEC) {
+    for (int i = 0; i < NI / V; ++i) kp[i] = load_pack<DT, V>(kn + i * V), qp[i] = load_pack<DT, V>(qn + i * V);
+    if (j0 < p.dv) vp = load_pack<DT, 4>(vn);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
       float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (r < p.dk && j0 < p.dv) f = *reinterpret_cast<const float4*>(p.state + base + r * p.dv + j0);
+      if (j0 < p.dv) f = *reinterpret_cast<const float4*>(p.state + base + (r0 + i) * p.dv + j0);
       s[i][0] = f.x, s[i][1] = f.y, s[i][2] = f.z, s[i][3] = f.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] = r < p.dk && j0 + e < p.dv ? p.state[base + r * p.dv + j0 + e] : 0.0f;
     }
-  }
-  const Elem<DT>* qn = p.q + n * p.qs[0] + hd * p.qs[2];
-  const Elem<DT>* kn = p.k + n * p.ks[0] + hd * p.ks[2];
-  const Elem<DT>* vn = p.v + n * p.vs[0] + hd * p.vs[2];
-  float v[4], k[NI], q[NI], acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = j0 + e < p.dv ? to_f<DT>(vn[j0 + e]) : 0.0f;
+    for (int i = 0; i < NI; ++i) k[i] = to_f<DT>(kp[i / V].e[i % V]), q[i] = to_f<DT>(qp[i / V].e[i % V]);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int r = r0 + 16 * i;
-    k[i] = r < p.dk ? to_f<DT>(kn[r]) : 0.0f;
-    q[i] = r < p.dk ? to_f<DT>(qn[r]) : 0.0f;
+    for (int e = 0; e < 4; ++e) v[e] = to_f<DT>(vp.e[e]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bool in = r0 + i < p.dk;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = in && j0 + e < p.dv ? p.state[base + (r0 + i) * p.dv + j0 + e] : 0.0f;
+      k[i] = in ? to_f<DT>(kn[i]) : 0.0f;
+      q[i] = in ? to_f<DT>(qn[i]) : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = j0 + e < p.dv ? to_f<DT>(vn[e]) : 0.0f;
   }
   const Decay decay(rate(g.log_decay[hd]));
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int r = r0 + 16 * i;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       s[i][e] = __builtin_fmaf(k[i], v[e], decay(s[i][e]));
       acc[e] = __builtin_fmaf(q[i], s[i][e], acc[e]);
     }
-    float* to = p.state_out + base + r * p.dv + j0;
+    float* to = p.state_out + base + (r0 + i) * p.dv + j0;
     if constexpr (VEC) {
-      if (r < p.dk && j0 < p.dv) *reinterpret_cast<float4*>(to) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+      if (j0 < p.dv) *reinterpret_cast<float4*>(to) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (r < p.dk && j0 + e < p.dv) to[e] = s[i][e];
+        if (r0 + i < p.dk && j0 + e < p.dv) to[e] = s[i][e];
     }
   }
 #pragma unroll
@@ -99,7 +107,7 @@ auto with_type(const Desc& d, F&& f) {
 }
 
 template <typename F>
-void with_rows(int32_t dk, F&& f) {  // rows of 16 that a thread holds one of
+void with_rows(int32_t dk, F&& f) {  // rows of a thread
   if (dk <= 32) f(std::integral_constant<int, 2>{});
   else if (dk <= 64) f(std::integral_constant<int, 4>{});
   else if (dk <= 128) f(std::integral_constant<int, 8>{});
@@ -111,7 +119,13 @@ void launch_step(const Pass<DT>& p, const LaGeo& g, int64_t nh, hipStream_t st) 
   const dim3 grid(unsigned(nh), unsigned((p.dv + 63) / 64));
   with_rows(p.dk, [&](auto ni) {
     constexpr int NI = decltype(ni)::value;
-    if (p.dv % 4 == 0) hipLaunchKernelGGL((la_step_kernel<DT, NI, true>), grid, dim3(256), 0, st, p, g);
+    constexpr uint64_t es = sizeof(Elem<DT>);
+    constexpr int64_t V = NI * es > 16 ? 16 / es : NI;
+    auto rows = [&](const void* q, const int64_t (&s)[3], int64_t v) {
+      return aligned(q, v * es) && s[0] % v == 0 && s[2] % v == 0;
+    };
+    const bool vec = p.dk == 16 * NI && p.dv % 4 == 0 && rows(p.q, p.qs, V) && rows(p.k, p.ks, V) && rows(p.v, p.vs, 4);
+    if (vec) hipLaunchKernelGGL((la_step_kernel<DT, NI, true>), grid, dim3(256), 0, st, p, g);
     else hipLaunchKernelGGL((la_step_kernel<DT, NI, false>), grid, dim3(256), 0, st, p, g);
   });
 }
@@ -155,8 +169,8 @@ cnhwc_status_t check_desc(const Desc* d, bool bwd) {
       !strides3_ok(*d, d->dv, d->v_stride) || (bwd && !strides3_ok(*d, d->dv, d->dy_stride)))
     return CNHWC_ERR_INVALID_ARGUMENT;
   if (d->dk > CNHWC_LINEAR_ATTENTION_MAX_DIM || d->dv > CNHWC_LINEAR_ATTENTION_MAX_DIM) return CNHWC_ERR_UNSUPPORTED;
-  // the grid's first dimension, and 64-bit offsets
-  if (d->n * d->h > (1ll << 23) || d->l > (1ll << 30) || !dense_ok(d->n * d->h, d->l, d->dk > d->dv ? d->dk : d->dv))
+  // the threads of a launch, and 64-bit offsets
+  if (d->n * d->h > (1ll << 20) || d->l > (1ll << 30) || !dense_ok(d->n * d->h, d->l, d->dk > d->dv ? d->dk : d->dv))
     return CNHWC_ERR_UNSUPPORTED;
   return CNHWC_OK;
 }

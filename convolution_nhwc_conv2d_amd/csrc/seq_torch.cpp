@@ -440,7 +440,7 @@ py::object rms_norm(const Tensor& x, const Opt& weight, double eps, const Opt& r
   const cnhwc_rms_norm_desc_t d = rms_desc(x, r, residual, "residual", wd, eps, 0);
   const Opt y = output(out, x);
   const auto [sum, rstd] = rms_outputs(x, residual, sum_out, stats);
-  if (x.numel() > 0)
+  if (r.n * r.l > 0)
     launch(x, "cnhwc_rms_norm_fwd", [&, sum = sum, rstd = rstd](void* s) {
       return cnhwc_rms_norm_fwd(&d, ptr(x), ptr(residual), ptr(weight), ptr(y), ptr(sum), ptr<float>(rstd), s);
     });
@@ -463,7 +463,7 @@ py::object rms_norm_quantized(const Tensor& x, const Opt& weight, double eps, st
   const Opt q = out ? out : Opt(at::empty(x.sizes(), x.options().dtype(at::kFloat8_e4m3fn)));
   const Opt scale = scale_out ? scale_out : Opt(at::empty(shape, x.options().dtype(at::kFloat)));
   const auto [sum, rstd] = rms_outputs(x, residual, sum_out, stats);
-  if (x.numel() > 0)
+  if (r.n * r.l > 0)
     launch(x, "cnhwc_rms_norm_fwd_q8", [&, sum = sum, rstd = rstd](void* s) {
       return cnhwc_rms_norm_fwd_q8(&d, ptr(x), ptr(residual), ptr(weight), ptr(q), ptr<float>(scale), ptr(sum),
                                    ptr<float>(rstd), s);
@@ -483,7 +483,7 @@ std::tuple<Tensor, Opt> rms_norm_backward(const Tensor& dy, const Tensor& x, con
   d.dy_stride[1] = g.stride[1];
   const Tensor dx = dense_like(x);
   const Opt dw = dense_like(weight);
-  if (x.numel() == 0) {
+  if (r.n * r.l == 0) {
     if (dw) dw->zero_();
     return {dx, dw};
   }

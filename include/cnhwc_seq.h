@@ -246,7 +246,14 @@ cnhwc_status_t cnhwc_rotary(const cnhwc_rotary_desc_t* desc, const void* x, cons
  *   S[t] = exp(log_decay[h]) S[t-1] + k[t]^T v[t],   y[t] = scale q[t] S[t]
  * for each head; the state S is fp32 [N,H,DK,DV].  Decays are meant (log_decay <= 0,
  * minus infinity included); a state that grows past fp32 is not represented.
- * Heads may be shared through strides of 0; gradients are those of each head. */
+ * Heads may be shared through strides of 0; gradients are those of each head.  N * H
+ * above 2^20 and L above 2^30 are UNSUPPORTED.
+ *
+ * Arithmetic: the states, their decays and every sum are fp32.  With 16-bit activations an
+ * operand of a matrix product is rounded to their type once (the products of q and
+ * k under their decays, the state that 32 positions start from) on the way to y and the
+ * gradients of q, k and v; on the way to a state and to log_decay's gradient it is taken
+ * in as many terms as fp32 has digits. */
 #define CNHWC_LINEAR_ATTENTION_MAX_DIM 256
 
 typedef struct {
