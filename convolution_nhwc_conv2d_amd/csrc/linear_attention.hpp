@@ -130,6 +130,45 @@ struct Mma<CNHWC_F32> {
   }
 };
 
+// Whether an operand holds an infinity or NaN.
+template <int CT>
+__device__ __forceinline__ bool odd(const typename Mma<CT>::Frag& f) {
+  if constexpr (CT == CNHWC_F32) {
+    const float m = __builtin_fabsf(f.x) + __builtin_fabsf(f.y) + __builtin_fabsf(f.z) + __builtin_fabsf(f.w);
+    return !(m <= FLT_MAX);  // or a sum past fp32, which the careful way takes as well
+  } else {
+    constexpr uint32_t kAll = CT == CNHWC_BF16 ? 0x7f807f80u : 0x7c007c00u;  // both exponents
+    const uint32_t u[4] = {f.x, f.y, f.z, f.w};
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = ~u[i] & kAll;  // a half that is 0
+      any |= (x - 0x00010001u) & ~x & 0x80008000u;
+    }
+    return any != 0;
+  }
+}
+// An operand with 0 in the place of infinities and NaN; at(e) is called for each of those.
+template <int CT, typename F>
+__device__ __forceinline__ typename Mma<CT>::Frag without_odd(const typename Mma<CT>::Frag& f, F&& at) {
+  if constexpr (CT == CNHWC_F32) {
+    float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (!(__builtin_fabsf(x[e]) <= FLT_MAX)) x[e] = 0.0f, at(e);
+    return make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    constexpr uint32_t kAll = CT == CNHWC_BF16 ? 0x7f80u : 0x7c00u;
+    uint32_t u[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int up = e % 2 * 16;
+      if ((u[e / 2] >> up & kAll) == kAll) u[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u, at(e);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
 // An operand of P floats as TERMS operands that add up to it.
 template <int CT, int TERMS, int P>
 __device__ __forceinline__ void split(const float (&x)[P], typename Mma<CT>::Frag (&f)[TERMS]) {
@@ -323,6 +362,7 @@ struct Powers {
   float fall[2 * CH];   // exp(g (CH - 1 - i)); 0 from CH on
   float far[2 * CH];    // exp(g |i - CH|)
   float row[CH];        // f16: what brings a row of products of q and k back from its range
+  int first[8][4][16];  // where values are not finite: the first such position that a channel meets
 
   // by: a factor of the ways to the end and of those between positions
   __device__ __forceinline__ void fill(float gd, float by, bool back) {
@@ -575,20 +615,63 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
     for (int kb = 0; kb < Sh::kBlocks; ++kb) vf[kb] = VTile::across(lds_v, wave, kb);
 
     if constexpr (!LOCAL) {
+      bool careful = false;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        v4f acc = M::kScaled ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : o[m];
+      for (int kb = 0; kb < Sh::kBlocks; ++kb) careful |= odd<DT>(vf[kb]);
+      if (__builtin_amdgcn_ballot_w64(careful) == 0) {
 #pragma unroll
-        for (int kb = 0; kb < Sh::kBlocks; ++kb) {
-          if (BACK ? kb < m / PB : kb > m / PB) continue;
-          M::mul(vf[kb], PTile::along(lds_p, m, kb), acc);
+        for (int m = 0; m < MT; ++m) {
+          v4f acc = M::kScaled ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : o[m];
+#pragma unroll
+          for (int kb = 0; kb < Sh::kBlocks; ++kb) {
+            if (BACK ? kb < m / PB : kb > m / PB) continue;
+            M::mul(vf[kb], PTile::along(lds_p, m, kb), acc);
+          }
+          if constexpr (M::kScaled) {
+            const float by = power.row[16 * m + c];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[m][r] = __builtin_fmaf(acc[r], by, o[m][r]);
+          } else {
+            o[m] = acc;
+          }
         }
-        if constexpr (M::kScaled) {
-          const float by = power.row[16 * m + c];
+      } else {
+        // An infinity or NaN times the 0 of a pair that comes the wrong way round would reach
+        // the positions before it (behind it).  So 0 in its place, and NaN for the positions
+        // that see it, in its channel.
+        int first = BACK ? -1 : CH;  // of the lane's channel, j0 + c
+        Frag clean[Sh::kBlocks];
+#pragma unroll
+        for (int kb = 0; kb < Sh::kBlocks; ++kb)
+          clean[kb] = without_odd<DT>(vf[kb], [&](int e) {
+            const int t = kb * M::kDeep + e / 4 * 16 + 4 * g4 + e % 4;
+            first = BACK ? (t > first ? t : first) : (t < first ? t : first);
+          });
+        power.first[wave][g4][c] = first;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          int f = power.first[wave][0][4 * g4 + r];
+#pragma unroll
+          for (int g = 1; g < 4; ++g) {
+            const int h = power.first[wave][g][4 * g4 + r];
+            f = BACK ? (h > f ? h : f) : (h < f ? h : f);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            if (BACK ? 16 * m + c <= f : 16 * m + c >= f) o[m][r] = __builtin_nanf("");
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int kb = 0; kb < Sh::kBlocks; ++kb) {
+            if (BACK ? kb < m / PB : kb > m / PB) continue;
+            M::mul(clean[kb], PTile::along(lds_p, m, kb), acc);
+          }
+          const float by = M::kScaled ? power.row[16 * m + c] : 1.0f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[m][r] = __builtin_fmaf(acc[r], by, o[m][r]);
-        } else {
-          o[m] = acc;
         }
       }
       // ---- y, to be stored when the next chunk has arrived: the wait for that chunk
