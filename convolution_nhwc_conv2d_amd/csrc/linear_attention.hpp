@@ -364,17 +364,23 @@ struct Powers {
   float row[CH];        // f16: what brings a row of products of q and k back from its range
   int first[8][4][16];  // where values are not finite: the first such position that a channel meets
 
-  // by: a factor of the ways to the end and of those between positions
-  __device__ __forceinline__ void fill(float gd, float by, bool back) {
+  // by: a factor of the ways to the end and of those between positions.  Ways that are longer
+  // than the sequence are 0: where the state grows (g > 0) they may be past fp32, and infinity
+  // times the zeros behind the sequence would be NaN.
+  __device__ __forceinline__ void fill(float gd, float by, bool back, int32_t len) {
     const int i = threadIdx.x;
     if (i < CH) {
-      const float r = exp_full(gd * float(i + 1)), f = exp_full(gd * float(CH - 1 - i));
+      const float r = i < len ? exp_full(gd * float(i + 1)) : 0.0f;
+      const float f = CH - 1 - i < len ? exp_full(gd * float(CH - 1 - i)) : 0.0f;
       rise[i] = back ? r * by : r;
       fall[i] = back ? f : f * by;
     } else if (i < 2 * CH) {
       fall[i] = 0.0f;
     }
-    if (i < 2 * CH) far[i] = exp_full(gd * float(i < CH ? CH - i : i - CH)) * by;
+    if (i < 2 * CH) {
+      const int d = i < CH ? CH - i : i - CH;
+      far[i] = d < len ? exp_full(gd * float(d)) * by : 0.0f;
+    }
   }
   // of position t, from the start (back: to it) or to the end
   __device__ __forceinline__ const float* from_start(bool back, int valid) const {
@@ -466,7 +472,7 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
       }
   }
 
-  power.fill(gd, p.scale_k, BACK);
+  power.fill(gd, p.scale_k, BACK, len);
   const Decay full(gd * float(CH));
 
   const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
@@ -881,7 +887,7 @@ __global__ __launch_bounds__((DecayShape<DT, DKT>::kThreads),
       }
     }
   }
-  power.fill(gd, 1.0f, false);
+  power.fill(gd, 1.0f, false, len);
 
   const Elem<DT>* const qn = p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];

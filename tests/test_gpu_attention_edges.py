@@ -140,3 +140,26 @@ def test_many_heads():
     assert torch.equal(s[:, 0], kv.sum(1))
     want = torch.stack([(q[:, t, 0, :, None].float() * kv[:, :t + 1].sum(1)).sum(1) for t in range(2)], 1)
     assert torch.equal(y[:, :, 0], want.half())
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_growth_over_few_positions(dt):
+    """Factors e^3 and e^1.5 a position, in sequences so short that every state fits
+    float32, while the same growth over a whole chunk of positions does not."""
+    i = _inputs([6], dt)
+    n, l = 2, 3
+    q, k, v, dy = (i[x][:, :l] for x in ("q", "k", "v", "dy"))
+    growth = torch.tensor([3.0, 1.5, -1.0], device="cuda")
+    lengths = torch.tensor([3, 2], dtype=torch.int32, device="cuda")
+    y, last = cn.linear_attention(q, k, v, growth, scale=0.2, lengths=lengths, return_state=True)
+    r = cn.linear_attention_backward(dy, q, k, v, growth, scale=0.2, lengths=lengths, decay_grad=True)
+    a = [A.wide(t) for t in (q, k, v, growth)] + [0.2, None, lengths]
+    mag = [t.abs() for t in a[:3]] + a[3:]
+    want = A.attention(*a) + tuple(A.attention_backward(A.wide(dy), *a, None)[x] for x in ("q", "k", "v", "log_decay"))
+    size = A.attention(*mag) + tuple(A.attention_backward(A.wide(dy).abs(), *mag, None)[x]
+                                     for x in ("q", "k", "v", "log_decay"))
+    # e^(3 d) of a product that is rounded, d <= 3: 9 more units, in both factors of a term
+    units = 2 * l + 512 + 20
+    for name, got, ref, m in zip(("y", "state", "dq", "dk", "dv", "dlog_decay"), (y, last, r.q, r.k, r.v, r.log_decay),
+                                 want, size):
+        R.check(got, ref.cpu(), m.cpu(), units + (0 if got.dtype == torch.float32 else OPERAND[dt]) + n * l, name)
