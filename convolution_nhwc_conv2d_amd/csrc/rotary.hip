@@ -7,6 +7,9 @@
 // turn there: at position 10^6 the product in 32 bits would be off by 0.03 rad.  Sine and
 // cosine are their Taylor series on [-pi/4, pi/4] (remainders 2e-9 and 1e-10).  A
 // thread turns the same pairs of several heads, so it computes them once for these.
+//
+// Bound by memory, every element read and written once (4 x 4096 x 32 x 128 bf16: 50 us,
+// 5.4 TB/s); a token's call by its launch.
 #include <hip/hip_runtime.h>
 
 #include "internal.hpp"
@@ -46,10 +49,16 @@ __device__ __forceinline__ void turn(double t, float& c, float& s) {
   s = k & 2 ? -y : y;
 }
 
+// Heads whose loads are issued together (4 x 4096 x 32 x 128 bf16: 1 56 us, 2 45, 3 48, 4 52),
+// and heads that share a thread's angles: of two vectors 2 (43 us, 4 44, 8 50; f32 with 16 heads
+// 41, 43, 49), of one 4 (interleaved, 2 heads 50 us, 4 46, 8 48), of single elements, with
+// an angle for each pair, 8 (4 x 2048 x 32 x 100 bf16: 2 40 us, 4 27, 8 24).  These with three
+// sets of inputs in turn, which stay in the cache in part.
+constexpr int kBatch = 2;
+constexpr int heads_of(int ve, bool interleaved) { return ve == 1 ? 8 : interleaved ? 4 : 2; }
+
 // Elements of a unit: VE pairs in two vectors (half), VE / 2 pairs in one
 // (interleaved), one vector of what stays; with VE 1 a pair or an element.
-constexpr int kBatch = 4;  // heads whose loads are issued together
-
 template <int DT, int VE, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void rotary_kernel(const Elem<DT>* x, const double* __restrict__ freqs,
                                                      const int32_t* __restrict__ positions, Elem<DT>* out, RotGeo g) {
@@ -74,7 +83,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Elem<DT>* x, const do
         turn(at * (freqs[i0 + i] * 0.15915494309189533577), cs[i], sn[i]);
         cs[i] *= g.scale, sn[i] *= g.scale;
       }
-      for (int32_t h = h0; h < g.h; h += kBatch * g.head_lanes) {
+      for (int64_t h = h0; h < g.h; h += int64_t(kBatch) * g.head_lanes) {
         Pack<DT, VE> a[kBatch], b[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -101,7 +110,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const Elem<DT>* x, const do
       }
     } else if (x != out) {
       const int32_t c = 2 * g.half + (unit - g.pair_units) * VE;
-      for (int32_t h = h0; h < g.h; h += g.head_lanes)
+      for (int64_t h = h0; h < g.h; h += g.head_lanes)
         store_pack<DT, VE>(yr + h * g.os[2] + c, load_pack<DT, VE>(xr + h * g.xs[2] + c));
     }
   }
@@ -158,12 +167,8 @@ hipError_t rotary_t(const cnhwc_rotary_desc_t& d, RotGeo g, const void* x, const
   const int32_t pairs = d.interleaved && VE > 1 ? VE / 2 : VE;
   g.pair_units = g.half / pairs;
   g.units = g.pair_units + (d.d - d.r) / VE;
-  // a thread takes kBatch heads, fewer where the threads would not fill the device
-  const int64_t one = g.tokens * g.units;
-  int64_t lanes = ceil_div(int64_t(g.h), int64_t(kBatch));
-  while (lanes < g.h && one * lanes < (1 << 17)) lanes *= 2;
-  g.head_lanes = int32_t(lanes < g.h ? lanes : g.h);
-  const dim3 grid = grid_of(ceil_div(one * g.head_lanes, int64_t(256)));
+  g.head_lanes = int32_t(ceil_div(int64_t(g.h), int64_t(heads_of(VE, d.interleaved))));
+  const dim3 grid = grid_of(ceil_div(g.tokens * g.units * g.head_lanes, int64_t(256)));
   if (d.interleaved)
     hipLaunchKernelGGL((rotary_kernel<DT, VE, true>), grid, dim3(256), 0, st, static_cast<const E*>(x), freqs,
                        positions, static_cast<E*>(out), g);

@@ -116,6 +116,21 @@ def test_offsets_past_32_bits():
     assert torch.equal(x, want)
 
 
+def test_as_many_heads_as_there_can_be():
+    """Head counts whose steps pass 32 bits; every head the same, in and out."""
+    h = (1 << 31) - 1
+    row = torch.tensor([0.5, -2.0, 3.0], dtype=torch.bfloat16, device="cuda")
+    x = torch.empty(1, 1, h, 3, dtype=row.dtype, device="cuda")
+    for part in x[0, 0].split(1 << 28):
+        part.copy_(row.expand_as(part))
+    y = cn.rotary(x, cn.rotary_frequencies(2), offset=1)
+    del x
+    one = row.expand(1, 1, 1, 3).contiguous()
+    _check(one, cn.rotary_frequencies(2), "one head", offset=1)
+    want = cn.rotary(one, cn.rotary_frequencies(2), offset=1)
+    assert all(torch.equal(part, want[0, 0].expand_as(part)) for part in y[0, 0].split(1 << 28))
+
+
 def test_infinity_and_nan_stay_in_their_pairs():
     g = np.random.default_rng(6)
     x, f = _rand(g, (1, 4, 2, 16), "f32"), cn.rotary_frequencies(8)
