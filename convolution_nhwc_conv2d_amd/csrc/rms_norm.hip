@@ -17,6 +17,10 @@
 // Every tensor moves once: the row is held in fp32 registers (tiles of norm_rows.hpp).
 // Rows that are not whole 16-byte vectors go element by element, rows wider than
 // the largest tile are read again from the cache.
+//
+// Bound by memory: 4 x 4096 x 4096 bf16 with the residual 99 us (5.4 TB/s), the same in 8
+// bits by groups of 128 93 us (5.1 TB/s), 8 x 2048 x 2048 backward 54 us (5.0 TB/s); a
+// token's row by its launch (kernel 2.3 us).
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -466,8 +470,9 @@ bool vectors(const cnhwc_rms_norm_desc_t& d, const int64_t (&s)[2], const void* 
   return !p || (aligned(p, 16) && d.c % v == 0 && (d.n == 1 || s[0] % v == 0) && (d.l == 1 || s[1] % v == 0));
 }
 
-// As in layer norm: most workgroups of the forward pass, so that w is taken up a
-// few times only, and the elements that a thread holds.
+// Most workgroups of the forward pass, so that w is taken up a few times only (16384 x 4096
+// bf16 with the residual: 1024 workgroups 100 us, 2048 111, 8192 99, 65536 98; in 8 bits 93, 96,
+// 93, 97), and the elements that a thread holds.
 constexpr int64_t kFwdBlocks = 8192;
 constexpr int kFwdRegs = 64, kFwdWide = 32, kBwdRegs = 32, kBwdWide = 16;
 
@@ -486,15 +491,20 @@ hipError_t rms_fwd_t(const RmsGeo& g, const RmsFwd<DT>& io, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Workgroups of the backward pass (rows of partial sums), a function of the shape only.
+// Workgroups of the backward pass (rows of partial sums), a function of the shape only: as
+// many as find their places at once, and no fewer rows than four each.  Measured with
+// 512, 768 and 1024: one vector to a thread, 16384 x 2048 bf16 54, 55, 58 us (256: 86), 65536 x 512
+// 49, 53, 54, 16384 x 1024 f32 50, 52, 54; two, 16384 x 4096 bf16 111, 109, 114, 8192 x 2424 f16 50, 43,
+// 42; four, 8192 x 8192 bf16 117, 139, 132; elements, 16384 x 613 40, 32, 28; a workgroup of more than
+// 256 threads, 2048 x 16384 80 each, 64 with 256.
 int64_t bwd_groups(const cnhwc_rms_norm_desc_t& d, bool vec) {
   const int64_t rows = d.n * d.l;
   const int64_t ve = vec ? 16 / int64_t(dtype_size(d.dtype)) : 1;
   int64_t per = 1, cap = 64;  // thread groups per workgroup; the wide form's row groups
   auto pick = [&](auto tile) {
-    constexpr int TPR = decltype(tile)::tpr;
+    constexpr int TPR = decltype(tile)::tpr, NV = decltype(tile)::nv;
     per = TPR > 256 ? 1 : 256 / TPR;
-    cap = TPR > 256 ? 256 : 1024;
+    cap = TPR > 256 ? 256 : ve == 1 ? 1024 : NV == 2 ? 768 : 512;
   };
   if (ve == 8) with_tile<8, kBwdRegs, kBwdWide>(ceil_div(d.c, 8), pick);
   else if (ve == 4) with_tile<4, kBwdRegs, kBwdWide>(ceil_div(d.c, 4), pick);
