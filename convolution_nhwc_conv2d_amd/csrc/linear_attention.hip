@@ -23,7 +23,8 @@ namespace {
 // A token of every sequence: a workgroup holds 64 columns of one head's state, 16 lanes by
 // four columns, 16 row groups of NI consecutive rows.  The state is the traffic, read
 // once and written once: VEC with whole vectors of it, and of q and k, whose elements
-// one by one are as many loads as the state's vectors.
+// one by one are as many loads as the state's vectors (64 x 16 x 128 x 128 bf16: single elements of
+// all 51 us, whole vectors of the state 33, of q and k too 29, 4.7 TB/s: memory).
 template <int DT, int NI, bool VEC>
 __global__ __launch_bounds__(256) void la_step_kernel(Pass<DT> p, LaGeo g) {
   __shared__ float part[4][64];
@@ -214,8 +215,8 @@ hipError_t step_t(const Desc& d, const cnhwc_linear_attention_inputs_t& in, void
 template <int DT>
 bool one_form(const Desc& d) {
   int a = 0, b = 0;
-  with_shape(d.dk, d.dv, [&](auto dkt, auto w) { a = dkt.value * 16 + w.value; });
-  with_shape(d.dv, d.dk, [&](auto dkt, auto w) { b = dkt.value * 16 + w.value; });
+  with_shape(d.dk, d.dv, false, [&](auto dkt, auto w) { a = dkt.value * 16 + w.value; });
+  with_shape(d.dv, d.dk, false, [&](auto dkt, auto w) { b = dkt.value * 16 + w.value; });
   return a == b && (d.dk + 127) / 128 == (d.dv + 127) / 128;
 }
 template <int DT>

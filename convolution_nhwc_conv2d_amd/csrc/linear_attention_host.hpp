@@ -8,10 +8,16 @@ namespace cnhwc {
 namespace seq {
 
 // The form of a pass: 16-row tiles of a state, wavefronts of a workgroup, 16 columns each.
+// Eight where there are columns for them, since each workgroup takes up all of k and q and
+// their products (bf16, 16 heads of 128 x 128: 1 x 16384 131 us, with four 165; 8 x 2048 126, 169; backward
+// 225, 287; f16 282, 320).  fp32, where the matrix instructions weigh more than what they are fed
+// from, has four (narrow) where half as many columns even out the workgroups, from 128 of eight
+// wavefronts on: 8 x 2048 293 us, with four 266, backward 752, 660; but with 16 of them 313, 349, with
+// 64 (4 x 4096 x 16 x 100 x 80) 296, 310, and with 256 rows 280, 349.
 template <typename F>
-void with_shape(int32_t dk, int32_t dv, F&& f) {
+void with_shape(int32_t dk, int32_t dv, bool narrow, F&& f) {
   auto wide = [&](auto dkt) {
-    if (dv <= 64) f(dkt, std::integral_constant<int, 4>{});
+    if (dv <= 64 || narrow) f(dkt, std::integral_constant<int, 4>{});
     else f(dkt, std::integral_constant<int, 8>{});
   };
   if (dk <= 32) wide(std::integral_constant<int, 2>{});
@@ -25,6 +31,7 @@ void with_shape(int32_t dk, int32_t dv, F&& f) {
 struct Cut {
   int32_t chunk, parts, chunks, run, runs;
   int32_t per;     // float4 of a head's state in lane order
+  bool narrow;
   uint64_t bytes;
 };
 // More than one run costs a kernel over k and v, about 0.6 of the other one, and the
@@ -44,7 +51,8 @@ inline void cut_runs(Cut& c, int64_t l, int64_t all, int64_t room) {
 template <int DT>
 Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64_t passes) {
   Cut c{};
-  with_shape(dk, dv, [&](auto dkt, auto w) {
+  c.narrow = DT == CNHWC_F32 && dk <= 128 && dv <= 128 && d.n * d.h * passes >= 128;
+  with_shape(dk, dv, c.narrow, [&](auto dkt, auto w) {
     constexpr int DKT = decltype(dkt)::value, W = decltype(w)::value;
     using Sh = ChunkShape<DT, DKT, W>;
     c.chunk = Sh::kChunk;
@@ -66,7 +74,7 @@ inline bool whole(const void* p, const int64_t (&s)[3], int32_t c, int64_t piece
 template <int DT>
 Cut decay_cut_of(const cnhwc_linear_attention_desc_t& d) {
   Cut c{};
-  with_shape(d.dk, 64, [&](auto dkt, auto) {
+  with_shape(d.dk, 64, false, [&](auto dkt, auto) {
     constexpr int DKT = decltype(dkt)::value;
     using Sh = DecayShape<DT, DKT>;
     c.chunk = Sh::kChunk;

@@ -20,7 +20,7 @@ hipError_t launch_passes(Passes<DT>& ps, int count, LaGeo g, const Cut& c, int64
     p.kept = reinterpret_cast<float4*>(workspace + i * c.bytes);
   }
   for (int i = 0; i < count; ++i) ps.p[i].halves = halves;
-  with_shape(ps.p[0].dk, ps.p[0].dv, [&](auto dkt, auto w) {
+  with_shape(ps.p[0].dk, ps.p[0].dv, c.narrow, [&](auto dkt, auto w) {
     constexpr int DKT = decltype(dkt)::value, W = decltype(w)::value;
     const int64_t blocks = heads * c.parts;
     auto run = [&](auto v) {
@@ -72,7 +72,7 @@ hipError_t launch_decay(DecayPass<DT>& pass, LaGeo g, const Cut& c, int64_t head
   const uint64_t states = uint64_t(heads) * (c.runs - 1) * c.per * 16;
   p.kept = reinterpret_cast<float4*>(workspace);
   pass.sums = reinterpret_cast<float*>(workspace + states);
-  with_shape(p.dk, 64, [&](auto dkt, auto) {
+  with_shape(p.dk, 64, false, [&](auto dkt, auto) {
     constexpr int DKT = decltype(dkt)::value;
     const int64_t blocks = heads * c.parts;
     auto run = [&](auto v) {

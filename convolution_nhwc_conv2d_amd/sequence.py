@@ -302,7 +302,8 @@ def selective_scan_step(u, delta, a, b, c, state, *, skip=None, gate=None, delta
 
 def rms_norm(x, weight=None, eps=1e-6, *, residual=None, return_stats=False, out=None, sum_out=None):
     """y[..., C] = z * rstd * weight over the channels of each row, z = x + residual
-    and rstd = 1 / sqrt(mean z^2 + eps).  weight [C] has x's dtype or float32.
+    and rstd = 1 / sqrt(mean z^2 + eps).  weight [C] has x's dtype or float32.  The mean
+    is float32: a row with elements beyond about 1e19 has rstd 0.
 
     With residual: (y, z), z rounded to x's dtype and y taken from z before that;
     sum_out, where z goes, may be residual itself (dense, updated in place).  With

@@ -180,7 +180,8 @@ cnhwc_status_t cnhwc_scan_step(const cnhwc_scan_desc_t* desc, const cnhwc_scan_i
 /* ------------------------------------------------------------ root-mean-square norm
  * z = x + residual (x alone without one), rstd = 1 / sqrt(mean z^2 + eps) over the C
  * channels of each of the N*L rows, y = z rstd w.  sum receives z in the
- * activations' dtype; y comes from z before that rounding.
+ * activations' dtype; y comes from z before that rounding.  The mean is fp32: a row
+ * with elements beyond about 1e19 has rstd 0, and so y 0.
  *
  * The 8-bit form stores q in e4m3 (OCP: 448 the largest value) and scale, fp32, so
  * that y = q * scale: scale = max |y| / 448 over the row [N*L], or over each group of
@@ -245,7 +246,8 @@ cnhwc_status_t cnhwc_rotary(const cnhwc_rotary_desc_t* desc, const void* x, cons
 /* ------------------------------------------------------------ linear attention
  *   S[t] = exp(log_decay[h]) S[t-1] + k[t]^T v[t],   y[t] = scale q[t] S[t]
  * for each head; the state S is fp32 [N,H,DK,DV].  Decays are meant (log_decay <= 0,
- * minus infinity included); a state that grows past fp32 is not represented.
+ * minus infinity included); a state that grows past fp32 is not represented.  An
+ * infinity or NaN in v reaches, as NaN, the y of its channel from its position on.
  * Heads may be shared through strides of 0; gradients are those of each head.  N * H
  * above 2^20 and L above 2^30 are UNSUPPORTED.
  *

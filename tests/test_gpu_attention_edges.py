@@ -163,3 +163,32 @@ def test_growth_over_few_positions(dt):
     for name, got, ref, m in zip(("y", "state", "dq", "dk", "dv", "dlog_decay"), (y, last, r.q, r.k, r.v, r.log_decay),
                                  want, size):
         R.check(got, ref.cpu(), m.cpu(), units + (0 if got.dtype == torch.float32 else OPERAND[dt]) + n * l, name)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("dk,dv", [(128, 128), (72, 100), (40, 100), (100, 40), (130, 90)])
+def test_heads_that_fill_the_device(dk, dv, dt):
+    """130 heads, so that float32's passes take half as many columns a workgroup where there are
+    more than 64; ragged, with states."""
+    g = np.random.default_rng([7, dk, dv])
+    n, l, h = 5, 70, 26
+    r = lambda *sh: R.rand(g, *sh).cuda()
+    q, k, v, dy = (r(n, l, h, d).to(DT[dt]) for d in (dk, dk, dv, dv))
+    state, dstate = r(n, h, dk, dv).float(), r(n, h, dk, dv).float()
+    decay = -torch.from_numpy(np.exp(g.uniform(-6, 0, h)).astype(np.float32)).cuda()
+    lengths = torch.tensor([70, 0, 33, 64, 1], dtype=torch.int32, device="cuda")
+    y, last = cn.linear_attention(q, k, v, decay, scale=0.1, state=state, lengths=lengths, return_state=True)
+    b = cn.linear_attention_backward(dy, q, k, v, decay, scale=0.1, state=state, lengths=lengths, dstate=dstate,
+                                     decay_grad=True)
+    a = [A.wide(t) for t in (q, k, v, decay)] + [0.1, A.wide(state), lengths]
+    mag = [t.abs() for t in a[:3]] + a[3:5] + [a[5].abs(), lengths]
+    names = ("q", "k", "v", "log_decay", "state")
+    ref, size = A.attention(*a), A.attention(*mag)
+    back, bsize = A.attention_backward(A.wide(dy), *a, A.wide(dstate)), A.attention_backward(
+        A.wide(dy).abs(), *mag, A.wide(dstate).abs())
+    units = 2 * l + 512
+    R.check(y, ref[0].cpu(), size[0].cpu(), units + OPERAND[dt], "y")
+    R.check(last, ref[1].cpu(), size[1].cpu(), units, "state")
+    for name, got in zip(names, b):
+        more = n * l if name == "log_decay" else 0 if name == "state" else OPERAND[dt]
+        R.check(got, back[name].cpu(), bsize[name].cpu(), units + more, "d" + name)
