@@ -38,13 +38,18 @@ struct Cut {
 // states between them: worth it up to five workgroups for eight compute units.
 // Measured (128 x 128 bf16, 2048 positions): 256 workgroups in one run 142 us, in two 180; 192
 // 133 and 160; 128 in four 111, in two 120, fp32 in one 376, in two 290; 64 x 64, 4096
-// positions, 64 workgroups in eight 57, in four 76.  At least three chunks to a run: 1 x 300 x 4
-// heads 17 us with three, 15 with two, 20 with four; 6 x 1023 x 5 heads fp32 38, 41, 37.
-inline void cut_runs(Cut& c, int64_t l, int64_t all, int64_t room) {
+// positions, 64 workgroups in eight 57, in four 76.  At least three chunks to a run, fewer only
+// while every run has a compute unit to itself (1 x 300 x 4 heads of 64 x 64 one chunk 15 us, three
+// 19; 3 x 591 x 96 x 100 fp32 25, 46, its decay's gradient 48 us less; 2 x 1000 x 8 heads of 64 x 128 two
+// 25, three 25, one 32, fp32 29, 35, 35; but 1 x 4096 x 8 x 128 x 128 two 48, three 38), and one run up
+// to `few` chunks, whose time the two other kernels would not save.
+inline void cut_runs(Cut& c, int64_t l, int64_t all, int64_t room, int64_t few) {
   c.chunks = int32_t((l + c.chunk - 1) / c.chunk);
   int64_t runs = all > 160 ? 1 : room / all;
-  if (runs > c.chunks / 3) runs = c.chunks / 3;
-  if (runs < 1) runs = 1;
+  int64_t most = c.chunks / 3 > 256 / all ? c.chunks / 3 : 256 / all;
+  if (most > c.chunks) most = c.chunks;
+  if (runs > most) runs = most;
+  if (runs < 1 || c.chunks <= few) runs = 1;
   c.run = int32_t((c.chunks + runs - 1) / runs);
   c.runs = (c.chunks + c.run - 1) / c.run;
 }
@@ -58,7 +63,7 @@ Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64
     c.chunk = Sh::kChunk;
     c.parts = (dv + Sh::kCols - 1) / Sh::kCols;
     c.per = c.parts * W * DKT * 64;
-    cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kGroups);
+    cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kGroups, 5);
   });
   c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16;
   return c;
@@ -80,7 +85,7 @@ Cut decay_cut_of(const cnhwc_linear_attention_desc_t& d) {
     c.chunk = Sh::kChunk;
     c.parts = (d.dv + 63) / 64;
     c.per = c.parts * 4 * DKT * 64 * 2;
-    cut_runs(c, d.l, d.n * d.h * c.parts, 256 * Sh::kGroups);
+    cut_runs(c, d.l, d.n * d.h * c.parts, 256 * Sh::kGroups, 3);
   });
   c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16 + (uint64_t(d.n) * d.h * c.parts * c.runs * 4 + 15) / 16 * 16;
   return c;
