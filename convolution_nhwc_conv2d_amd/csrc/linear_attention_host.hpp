@@ -63,7 +63,10 @@ Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64
     c.chunk = Sh::kChunk;
     c.parts = (dv + Sh::kCols - 1) / Sh::kCols;
     c.per = c.parts * W * DKT * 64;
-    cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kGroups, 5);
+    // a chunk in fp32 takes longer: 1 x 128 x 4 heads of 128 x 128 in four runs 20 us, in one 28, 64 x 64 15
+    // and 14, 32 x 32 14 and 11; 2 x 130 x 8 of 64 x 96 in five 18, in one 23
+    const int few = DT == CNHWC_F32 && DKT * W > 16 ? 3 : 5;
+    cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kGroups, few);
   });
   c.bytes = uint64_t(d.n) * d.h * (c.runs - 1) * c.per * 16;
   return c;
