@@ -71,18 +71,18 @@ __device__ __forceinline__ float rate(float g) { return g < -FLT_MAX ? -FLT_MAX 
 // digits where exp(g), rounded, would be off by 2^-25 at every position, 10^-4
 // after 4096 of them.
 struct Decay {
-  float m;     // exp(g) - 1, or exp(g)
-  float keep;  // 1, or 0
+  float m;    // exp(g) - 1, or exp(g)
+  bool slow;  // the first
   __device__ __forceinline__ explicit Decay(float g) {
-    const bool slow = __builtin_fabsf(g) < 0.5f;
+    slow = __builtin_fabsf(g) < 0.5f;
     m = slow ? expm1f(g) : exp_full(g);
-    keep = slow ? 1.0f : 0.0f;
   }
-  __device__ __forceinline__ float operator()(float x) const { return __builtin_fmaf(m, x, keep * x); }
+  // a choice, not a sum with 0 x: that would make NaN of an infinite state
+  __device__ __forceinline__ float operator()(float x) const { return slow ? __builtin_fmaf(m, x, x) : m * x; }
   // of many: one instruction each
   template <int A>
   __device__ __forceinline__ void apply(v4f (&s)[A]) const {
-    if (keep != 0.0f) {
+    if (slow) {
 #pragma unroll
       for (int a = 0; a < A; ++a)
 #pragma unroll
