@@ -94,6 +94,18 @@ struct Decay {
   }
 };
 
+// Positions that a chunk's products take at a time: all of them, fewer where the state grows
+// so fast that a way across the chunk would pass e^44, half of fp32's range: a value of
+// k or v that the other one's zeros keep out of the state would be past fp32 with it, and
+// infinity times 0 NaN.  f16, where a product's small operands lose digits beside large
+// ones (Range), goes to e^8.  Decays, which is what this is for, take whole chunks.
+template <int DT>
+__device__ __forceinline__ int32_t step_shift(float g, int32_t chunk) {
+  int32_t shift = 0;
+  for (const float most = DT == CNHWC_F16 ? 8.0f : 44.0f; chunk >> shift > 1 && g * float(chunk >> shift) > most;) ++shift;
+  return __builtin_amdgcn_readfirstlane(shift);
+}
+
 // What the matrix products are made of.  bf16 and f16: operands as they are, 32 deep; an
 // fp32 operand is one or several 16-bit terms that add up to it (8 or 11 digits each).
 // fp32: 16 deep in four instructions.  The depth runs over the lanes' four groups g in
@@ -410,7 +422,7 @@ struct Powers {
 template <int DT, int DKT, int W>
 struct ChunkShape {
   using M = Mma<DT>;
-  static constexpr int kChunk = 32;
+  static constexpr int kShift = 5, kChunk = 1 << kShift;
   static constexpr int kThreads = 64 * W, kCols = 16 * W;
   static constexpr int kTiles = kChunk / 16;                  // of 16 positions
   static constexpr int kDepth = DKT * 16 / M::kDeep;          // blocks of a state's rows
@@ -462,11 +474,11 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
   const float gd = rate(g.log_decay[hd]);
 
   const int32_t at = BACK ? g.runs - 1 - run : run;
-  // the run's chunks with valid positions; past them the state stands still
-  const int32_t chunk_lo = at * g.run, all_hi = chunk_lo + g.run < g.chunks ? chunk_lo + g.run : g.chunks;
-  const int32_t used = (len + CH - 1) / CH;
-  const int32_t chunk_hi = used < chunk_lo ? chunk_lo : used < all_hi ? used : all_hi;
-  const int32_t count = chunk_hi - chunk_lo;
+  // the run's positions; past the valid ones the state stands still
+  const int32_t lo = at * g.run * CH, hi = lo + g.run * CH < g.l ? lo + g.run * CH : g.l;
+  const int32_t end = len < lo ? lo : len < hi ? len : hi;
+  const int32_t shift = step_shift<DT>(gd, CH), stride = CH >> shift;
+  const int32_t count = (end - lo + stride - 1) >> (Sh::kShift - shift);
   const int32_t col0 = part * Sh::kCols, j = col0 + wave * 16 + c;
 
   // ---- the state: rows 16 a + 4 g + r of column j
@@ -487,32 +499,34 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
       }
   }
 
-  power.fill(gd, p.scale_k, BACK, len);
-  const Decay full(gd * float(CH));
+  power.fill(gd, p.scale_k, BACK, len < stride ? len : stride);
+  const Decay full(gd * float(stride));
 
   const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
   const Elem<DT>* const vn = p.v + n * p.vs[0] + hd * p.vs[2] + col0;
-  auto chunk_at = [&](int32_t i) { return BACK ? chunk_hi - 1 - i : chunk_lo + i; };
+  auto start_of = [&](int32_t i) { return lo + ((BACK ? count - 1 - i : i) << (Sh::kShift - shift)); };
   auto valid_at = [&](int32_t i) {
-    const int32_t v = len - chunk_at(i) * CH;
-    return v > CH ? CH : v;
+    const int32_t v = end - start_of(i);
+    return v > stride ? stride : v;
   };
   const bool filled = p.dk == DKT * 16 && p.dv - col0 >= Sh::kCols;
   KTile tk, tq;
   VTile tv;
-  auto fetch = [&](int32_t i) {
-    const int32_t valid = valid_at(i);
-    const int64_t t0 = int64_t(chunk_at(i)) * CH;
+  auto fetch = [&](int64_t t0) {  // whole chunks: a smaller step's rows are left out on the way to LDS
+    const int32_t valid = end - t0 > CH ? CH : int32_t(end - t0);
     tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid, p.halves);
     tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid, p.halves);
     if constexpr (!LOCAL) tq.template load<VEC>(qn + t0 * p.qs[1], p.qs[1], p.dk, valid, p.halves);
   };
-  if (count > 0) fetch(0);
+  if (end > lo) {  // loads that do not wait for the decay's; from the end a smaller step starts again
+    fetch(BACK ? lo + ((end - lo - 1) & ~(CH - 1)) : lo);
+    if (BACK && shift > 0) fetch(start_of(0));
+  }
   if constexpr (!LOCAL) {
-    const int64_t first = int64_t(chunk_hi) * CH, last = int64_t(all_hi) * CH < g.l ? int64_t(all_hi) * CH : g.l;
+    const int64_t first = start_of(BACK ? -1 : count);  // behind what the steps store
     const int32_t wide = p.dv - col0 < Sh::kCols ? p.dv - col0 : Sh::kCols;
-    for (int64_t e = threadIdx.x; e < (last - first) * wide; e += Sh::kThreads)
+    for (int64_t e = threadIdx.x; e < (hi - first) * wide; e += Sh::kThreads)
       p.y[((n * g.l + first + e / wide) * g.h + hd) * p.dv + col0 + e % wide] = Elem<DT>(0);
   }
 
@@ -522,13 +536,13 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
   int32_t out_t0 = 0;
   const int32_t j4 = col0 + wave * 16 + 4 * g4;
   auto put_y = [&]() __attribute__((always_inline)) {
-    const int32_t rows = g.l - out_t0 < CH ? g.l - out_t0 : CH, live = len - out_t0;
+    const int32_t rows = g.l - out_t0 < stride ? g.l - out_t0 : stride, live = len - out_t0;
     Elem<DT>* const base = p.y + ((n * g.l + out_t0) * g.h + hd) * p.dv;
     const int64_t step = int64_t(g.h) * p.dv;
     if constexpr (VEC) {
       const uint32_t to = __umul24(c, uint32_t(step)) + j4;  // 64 rows within 32 bits
       if (j4 < p.dv) {
-        if (live >= CH) {
+        if (rows == CH && live >= CH) {
 #pragma unroll
           for (int m = 0; m < MT; ++m) *reinterpret_cast<Raw4*>(base + m * 16 * step + to) = out[m];
         } else {
@@ -552,7 +566,7 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
 
   for (int32_t step = 0; step < count; ++step) {
     const int32_t valid = valid_at(step);
-    const int32_t t0 = chunk_at(step) * CH;
+    const int32_t t0 = start_of(step);
     __syncthreads();  // the chunk before has been read
     const bool all = filled && valid == CH;
     tk.store(lds_k, all, p.dk, valid);
@@ -562,7 +576,7 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
     if constexpr (!LOCAL) {
       if (step > 0) put_y();
     }
-    if (step + 1 < count) fetch(step + 1);
+    if (step + 1 < count) fetch(start_of(step + 1));
 
     v4f o[LOCAL ? 1 : MT];
     if constexpr (!LOCAL) {
@@ -713,7 +727,7 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
     }
 
     // ---- S <- decay S + k^T (decayed v)
-    (valid == CH ? full : Decay(gd * float(valid))).apply(s);
+    (valid == stride ? full : Decay(gd * float(valid))).apply(s);
     const float* const to_end = power.to_end(BACK, valid) + 4 * g4;
 #pragma unroll
     for (int kb = 0; kb < Sh::kBlocks; ++kb) {
@@ -884,9 +898,8 @@ __global__ __launch_bounds__((DecayShape<DT, DKT>::kThreads),
   const int64_t n = nh / g.h, hd = nh - n * g.h;
   const int32_t len = valid_len(g.lengths, n, g.l);
   const float gd = rate(g.log_decay[hd]);
-  const int32_t chunk_lo = run * g.run, all_hi = chunk_lo + g.run < g.chunks ? chunk_lo + g.run : g.chunks;
-  const int32_t used = (len + CH - 1) / CH;
-  const int32_t chunk_hi = used < chunk_lo ? chunk_lo : used < all_hi ? used : all_hi;
+  const int32_t lo = run * g.run * CH, hi = lo + g.run * CH < len ? lo + g.run * CH : len;  // the run's valid positions
+  const int32_t stride = CH >> step_shift<CT>(gd, CH);
   const int32_t col0 = part * 64, j = col0 + wave * 16 + c;
 
   v4f s[TA], grow[TA];  // rows row0 + 16 a + 4 g + r, column j
@@ -908,7 +921,7 @@ __global__ __launch_bounds__((DecayShape<DT, DKT>::kThreads),
       }
     }
   }
-  power.fill(gd, 1.0f, false, len);
+  power.fill(gd, 1.0f, false, len < stride ? len : stride);
 
   const Elem<DT>* const qn = p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
@@ -917,9 +930,8 @@ __global__ __launch_bounds__((DecayShape<DT, DKT>::kThreads),
   const bool filled = p.dk == DKT * 16 && p.dv - col0 >= 64;
   KTile tk, tq;
   VTile tv, td;
-  auto fetch = [&](int32_t chunk) {
-    const int64_t t0 = int64_t(chunk) * CH;
-    const int32_t valid = len - t0 > CH ? CH : int32_t(len - t0);
+  auto fetch = [&](int64_t t0) {  // whole chunks: a smaller step's rows are left out on the way to LDS
+    const int32_t valid = hi - t0 > CH ? CH : int32_t(hi - t0);
     tk.template load<VEC>(kn + t0 * p.ks[1], p.ks[1], p.dk, valid, p.halves);
     tv.template load<VEC>(vn + t0 * p.vs[1], p.vs[1], p.dv - col0, valid, p.halves);
     if constexpr (!LOCAL) {
@@ -927,10 +939,10 @@ __global__ __launch_bounds__((DecayShape<DT, DKT>::kThreads),
       td.template load<VEC>(dn + t0 * pass.dys[1], pass.dys[1], p.dv - col0, valid, p.halves);
     }
   };
-  if (chunk_lo < chunk_hi) fetch(chunk_lo);
+  if (lo < hi) fetch(lo);
   double total = 0.0;
-  for (int32_t chunk = chunk_lo; chunk < chunk_hi; ++chunk) {
-    const int32_t valid = len - chunk * CH > CH ? CH : len - chunk * CH;
+  for (int32_t at = lo; at < hi; at += stride) {
+    const int32_t valid = hi - at > stride ? stride : hi - at;
     __syncthreads();  // the chunk before has been read
     const bool all = filled && valid == CH;
     tk.store(lds_k, all, p.dk, valid);
@@ -940,7 +952,7 @@ __global__ __launch_bounds__((DecayShape<DT, DKT>::kThreads),
       td.store(lds_d, all, p.dv - col0, valid);
     }
     __syncthreads();
-    if (chunk + 1 < chunk_hi) fetch(chunk + 1);
+    if (at + stride < hi) fetch(at + stride);
 
     if constexpr (!LOCAL) {
       float sum = 0.0f;

@@ -1,8 +1,10 @@
-"""Linear attention's states under decays that leave fp32's ordinary range: infinite states."""
+"""Linear attention's states under decays that leave fp32's ordinary range: infinite states, and growth (log_decay
+> 0) where the states themselves fit float32."""
 import numpy as np
 import pytest
 import torch
 
+import attention_reference as A
 import seq_reference as R
 
 pytestmark = pytest.mark.gpu
@@ -10,6 +12,8 @@ pytestmark = pytest.mark.gpu
 cn = pytest.importorskip("convolution_nhwc_conv2d_amd")
 
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+# as in test_gpu_linear_attention.py: one rounding of an operand
+OPERAND = {"f32": 0, "f16": 1 << 13, "bf16": 1 << 16}
 
 
 def _rows(seed, dt, n, l, h, dk, dv):
@@ -32,3 +36,67 @@ def test_an_infinite_state_stays_infinite(dt):
     assert cn.linear_attention_workspace_bytes(q, v) > 0  # more than one run
     _, last = cn.linear_attention(q, k, v, torch.tensor([-0.02, -0.05], device="cuda"), state=was, return_state=True)
     assert torch.equal(last[hit], was[hit]) and torch.isfinite(last[~hit]).all()
+
+
+def _growing(dt, n, l, h, growth, late, early, seed):
+    """The forward pass and the gradients that go through the state, with k and v only in the last
+    `late` positions, and the gradients that go through its derivative, with q and dy only in
+    the first `early` ones: every state is 0 or grows over that many positions."""
+    q, k, v, dy = _rows(seed, dt, n, l, h, 64, 48)
+    scale = 2.0 ** -int(growth * (late - 1) / np.log(2))  # y stays within f16
+    g = torch.full((h,), growth, device="cuda")
+    # 2 L + 512; each decay's exponent, g times positions, is rounded to 2^-24 of itself: at most
+    # g late units more a factor, twice where two factors meet
+    units = 2 * l + 512 + int(2 * growth * max(late, early))
+    kl, vl, dl = k.clone(), v.clone(), dy.clone()
+    kl[:, :l - late] = 0
+    vl[:, :l - late] = 0
+    dl[:, :l - late] = 0
+    check = lambda got, ref, mag, name: R.check(got, ref.cpu(), mag.cpu(), units + (
+        0 if got.dtype == torch.float32 else OPERAND[dt]) + (n * l if name == "dlog_decay" else 0), f"{name} {growth}")
+    # k alone, v alone, and both: what is 0 in one of them leaves no state either
+    for name, kk, vv in (("both", kl, vl), ("v everywhere", kl, v), ("k everywhere", k, vl)):
+        y, last = cn.linear_attention(q, kk, vv, g, scale=scale, return_state=True)
+        a = [A.wide(t) for t in (q, kk, vv, g)] + [scale, None, None]
+        mag = [t.abs() for t in a[:3]] + a[3:]
+        for t, ref, m, what in zip((y, last), A.attention(*a), A.attention(*mag), ("y", "state")):
+            check(t, ref, m, f"{name}: {what}")
+    r = cn.linear_attention_backward(dl, q, kl, v, g, scale=scale, decay_grad=True)
+    a = [A.wide(t) for t in (dl, q, kl, v, g)] + [scale, None, None, None]
+    mag = [t.abs() for t in a[:4]] + a[4:]
+    want, size = A.attention_backward(*a), A.attention_backward(*mag)
+    check(r.q, want["q"], size["q"], "dq")
+    check(r.log_decay, want["log_decay"], size["log_decay"], "dlog_decay")
+    qe, de, none = q.clone(), dy.clone(), torch.zeros_like(k)
+    qe[:, early:] = 0
+    de[:, early:] = 0
+    state = torch.zeros(n, h, 64, 48, device="cuda")
+    for name, qq, dd in (("both", qe, de), ("dy everywhere", qe, dy), ("q everywhere", q, de)):
+        for kk, vv in ((k, torch.zeros_like(v)), (none, v)):
+            r = cn.linear_attention_backward(dd, qq, kk, vv, g, scale=scale, state=state)
+            a = [A.wide(t) for t in (dd, qq, kk, vv, g)] + [scale, A.wide(state), None, None]
+            mag = [t.abs() for t in a[:4]] + a[4:]
+            want, size = A.attention_backward(*a), A.attention_backward(*mag)
+            for x in ("k", "v", "state"):
+                check(getattr(r, x), want[x], size[x], f"{name}: d{x}")
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("growth,l,late", [(1.4, 64, 20), (3.0, 30, 3), (5.0, 100, 3), (12.0, 70, 2), (44.0, 45, 1),
+                                           (80.0, 33, 1)])
+def test_growth_within_a_chunk(growth, l, late, dt):
+    """A chunk of 32 positions (of 64 for the decay's gradient) grows past float32."""
+    _growing(dt, 2, l, 3, growth, late, min(late, 5), [3, l, late])
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_growth_of_a_zero_state_over_a_whole_sequence(dt):
+    """e^90 over 30 positions is past float32; nothing enters the state before the last one."""
+    q, k, v, dy = _rows([4], dt, 1, 30, 1, 32, 32)
+    k[:, :29] = 0
+    g = torch.tensor([3.0], device="cuda")
+    y, last = cn.linear_attention(q, k, v, g, state=torch.zeros(1, 1, 32, 32, device="cuda"), return_state=True)
+    a = [A.wide(t) for t in (q, k, v, g)] + [1.0, None, None]
+    mag = [t.abs() for t in a[:3]] + a[3:]
+    for t, ref, m, units in zip((y, last), A.attention(*a), A.attention(*mag), (OPERAND[dt], 0)):
+        R.check(t, ref.cpu(), m.cpu(), 2 * 30 + 512 + units, "growth of 0")
