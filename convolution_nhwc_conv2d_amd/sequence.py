@@ -399,7 +399,8 @@ def linear_attention(q, k, v, log_decay, *, scale=1.0, state=None, lengths=None,
         y[n,t,h] = scale q[n,t,h] S[n,t,h]
 
     q, k [N,L,H,DK] and v, y [N,L,H,DV] in one dtype; log_decay [H] (at most 0; minus
-    infinity forgets at once) and the states [N,H,DK,DV] in float32; DK, DV <= 256.
+    infinity forgets at once; above 0, growth, where every state fits float32) and the
+    states [N,H,DK,DV] in float32; DK, DV <= 256.
     An absent state counts as 0.  Heads may be expanded (a stride of 0).  With
     return_state: (y, the state after the last valid position)."""
     return _seq.linear_attention(q, k, v, log_decay, scale, state, lengths, return_state, out, workspace)

@@ -246,7 +246,9 @@ cnhwc_status_t cnhwc_rotary(const cnhwc_rotary_desc_t* desc, const void* x, cons
 /* ------------------------------------------------------------ linear attention
  *   S[t] = exp(log_decay[h]) S[t-1] + k[t]^T v[t],   y[t] = scale q[t] S[t]
  * for each head; the state S is fp32 [N,H,DK,DV].  Decays are meant (log_decay <= 0,
- * minus infinity included); a state that grows past fp32 is not represented.  An
+ * minus infinity included).  Growth is taken where exp(log_decay) and every state fit
+ * fp32 (a state of 0 stays 0 however long), for values and products of q and k up to 1e19;
+ * it runs in smaller steps, slower, from exp(1.3) a position on, in f16 from exp(0.25).  An
  * infinity or NaN in v reaches, as NaN, the y of its channel from its position on.
  * Heads may be shared through strides of 0; gradients are those of each head.  N * H
  * above 2^20 and L above 2^30 are UNSUPPORTED.

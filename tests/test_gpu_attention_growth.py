@@ -82,8 +82,20 @@ def _growing(dt, n, l, h, growth, late, early, seed):
 
 
 @pytest.mark.parametrize("dt", list(DT))
+def test_growth_over_many_runs(dt):
+    """e^0.95 a position: a run of 96 positions or more grows by e^91, past float32; what grows
+    starts 60 positions from the end."""
+    n, l, h, growth = 1, 1200, 16, 0.95
+    q = torch.empty(n, l, h, 64, dtype=DT[dt], device="cuda")
+    runs = 1 + cn.linear_attention_workspace_bytes(q, q[..., :48]) // (n * h * 64 * 64 * 4)
+    run = -(-(l // 32) // runs) * 32
+    assert runs > 2 and growth * run > 89
+    _growing(dt, n, l, h, growth, 60, 60, [2])
+
+
+@pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("growth,l,late", [(1.4, 64, 20), (3.0, 30, 3), (5.0, 100, 3), (12.0, 70, 2), (44.0, 45, 1),
-                                           (80.0, 33, 1)])
+                                           (80.0, 33, 1), (1.5, 200, 9)])
 def test_growth_within_a_chunk(growth, l, late, dt):
     """A chunk of 32 positions (of 64 for the decay's gradient) grows past float32."""
     _growing(dt, 2, l, 3, growth, late, min(late, 5), [3, l, late])
