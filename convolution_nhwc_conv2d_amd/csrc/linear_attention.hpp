@@ -213,9 +213,9 @@ __device__ __forceinline__ typename Mma<CT>::Frag without_odd(const typename Mma
   }
 }
 
-// An operand of P floats as TERMS operands that add up to it.
+// An operand of P floats as TERMS operands that add up to it, each `next` times as large as that.
 template <int CT, int TERMS, int P>
-__device__ __forceinline__ void split(const float (&x)[P], typename Mma<CT>::Frag (&f)[TERMS]) {
+__device__ __forceinline__ void split(const float (&x)[P], typename Mma<CT>::Frag (&f)[TERMS], float next = 1.0f) {
   if constexpr (P == 4) {
     f[0] = make_float4(x[0], x[1], x[2], x[3]);
   } else {
@@ -229,7 +229,8 @@ __device__ __forceinline__ void split(const float (&x)[P], typename Mma<CT>::Fra
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         p[i] = M::pack(v[2 * i], v[2 * i + 1]);
-        if (t + 1 < TERMS) v[2 * i] -= M::low(p[i]), v[2 * i + 1] -= M::high(p[i]);
+        if (t + 1 < TERMS)
+          v[2 * i] = (v[2 * i] - M::low(p[i])) * next, v[2 * i + 1] = (v[2 * i + 1] - M::high(p[i])) * next;
       }
       f[t] = make_uint4(p[0], p[1], p[2], p[3]);
     }
@@ -249,8 +250,10 @@ __device__ __forceinline__ void unpack(const typename Mma<CT>::Frag& f, float (&
 }
 
 // Powers of two that bring fp32 values into f16's range and back: the largest of them to
-// [2^14, 2^15), so that what is 2^28 times smaller still has all its digits.  Infinities
-// and NaN are passed over: the values beside them keep theirs.
+// [2^14, 2^15), so that what is 2^28 times smaller still has all its 11 digits, and nothing
+// is off by more than 2^-39 of the largest.  Of a position's products of q and k; of a
+// wavefront's 16 columns of the state that enters y; of a column's decayed v in a chunk.
+// Infinities and NaN are passed over: the values beside them keep theirs.
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = __builtin_fabsf(x);
   return a <= FLT_MAX ? a : 0.0f;
@@ -463,11 +466,32 @@ struct Passes {
   Pass<DT> p[3];
 };
 
+// What a workgroup has: a part of the columns of a head's state, for a run.
+struct Work {
+  int32_t parts, part, run;  // run: in the order that the pass goes through them
+  uint32_t nh, n, hd;
+  __device__ __forceinline__ Work(int32_t columns, int32_t cols, int32_t runs, int32_t h) {
+    parts = (columns + cols - 1) / cols;
+    const uint32_t row = blockIdx.x / unsigned(parts);
+    part = int32_t(blockIdx.x - row * unsigned(parts));
+    nh = row / unsigned(runs);
+    run = int32_t(row - nh * unsigned(runs));
+    n = nh / unsigned(h), hd = nh - n * unsigned(h);
+  }
+};
+
 // What a workgroup does.  LOCAL: the state that a run of chunks leaves from a zero state
 // (the first run: from the initial one), for all runs but the last.  Otherwise y and
 // the final state.
-template <int DT, int DKT, int W, bool LOCAL, bool VEC, bool BACK>
-__device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, char* lds,
+//
+// STEEP, f16 only: in the product that goes to the state v's second term loses its digits to
+// f16's narrow range from 2^-17 of the column's largest on, and what is below 2^-39 of it
+// is 0.  Where a chunk's decay is faster than 2^-8 that term stands 2^11 higher, in an
+// accumulator of its own: digits down to 2^-27, 0 below 2^-50.  (For every head 8 x 2048 x 16 x
+// 128 x 128 takes 139 us for 132, its backward 277 for 269.)
+constexpr float kHigher = 0x1p11f;
+template <int DT, int DKT, int W, bool LOCAL, bool VEC, bool BACK, bool STEEP>
+__device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, const Work& w, char* lds,
                                           Powers<ChunkShape<DT, DKT, W>::kChunk>& power) {
   using Sh = ChunkShape<DT, DKT, W>;
   using M = typename Sh::M;
@@ -483,13 +507,8 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
 
   const int lane = threadIdx.x & 63, c = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t parts = (p.dv + Sh::kCols - 1) / Sh::kCols;  // workgroups along the state's columns
-  const int32_t part = int32_t(blockIdx.x % unsigned(parts));
-  const int64_t row = blockIdx.x / unsigned(parts);
-  const int32_t runs = LOCAL ? g.runs - 1 : g.runs;
-  const int64_t nh = row / runs;
-  const int32_t run = int32_t(row - nh * runs);  // in the order that the pass goes through them
-  const int64_t n = nh / g.h, hd = nh - n * g.h;
+  const int32_t parts = w.parts, part = w.part, run = w.run;
+  const int64_t nh = w.nh, n = w.n, hd = w.hd;
   const int32_t len = valid_len(g.lengths, n, g.l);
   const float gd = rate(g.log_decay[hd]);
 
@@ -521,7 +540,6 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
 
   power.fill(gd, p.scale_k, BACK, len < stride ? len : stride);
   const Decay full(gd * float(stride));
-
   const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
   const Elem<DT>* const vn = p.v + n * p.vs[0] + hd * p.vs[2] + col0;
@@ -765,13 +783,19 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, cha
         for (int e = 0; e < PE; ++e) x[e] *= of_v.in;
       }
       Frag vt[M::kTerms];
-      split<DT>(x, vt);
+      split<DT>(x, vt, STEEP ? kHigher : 1.0f);
 #pragma unroll
       for (int a = 0; a < DKT; ++a) {
         const Frag f = KTile::across(lds_k, a, kb);
         v4f acc = M::kScaled ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : s[a];
 #pragma unroll
-        for (int t = 0; t < M::kTerms; ++t) M::mul(f, vt[t], acc);
+        for (int t = 0; t < (STEEP ? 1 : M::kTerms); ++t) M::mul(f, vt[t], acc);
+        if constexpr (STEEP) {
+          v4f next = {0.0f, 0.0f, 0.0f, 0.0f};
+          M::mul(f, vt[M::kTerms - 1], next);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(next[r], 1.0f / kHigher, acc[r]);
+        }
         if constexpr (M::kScaled) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) s[a][r] = __builtin_fmaf(acc[r], of_v.out, s[a][r]);
@@ -807,8 +831,16 @@ __global__ __launch_bounds__(64 * W, (ChunkShape<DT, DKT, W>::kWaves)) void la_c
   __shared__ __attribute__((aligned(16))) char lds[LOCAL ? Sh::KTile::kBytes + Sh::VTile::kBytes : Sh::kLds];
   __shared__ Powers<Sh::kChunk> power;
   const Pass<DT>& p = passes.p[blockIdx.y];
-  if (p.back) la_chunks<DT, DKT, W, LOCAL, VEC, true>(p, g, lds, power);
-  else la_chunks<DT, DKT, W, LOCAL, VEC, false>(p, g, lds, power);
+  const Work w(p.dv, Sh::kCols, LOCAL ? g.runs - 1 : g.runs, g.h);
+  auto run = [&](auto steep) __attribute__((always_inline)) {
+    if (p.back) la_chunks<DT, DKT, W, LOCAL, VEC, true, decltype(steep)::value>(p, g, w, lds, power);
+    else la_chunks<DT, DKT, W, LOCAL, VEC, false, decltype(steep)::value>(p, g, w, lds, power);
+  };
+  if constexpr (Sh::M::kScaled) {
+    const bool steep = __builtin_fabsf(rate(g.log_decay[w.hd])) * float(Sh::kChunk) > 5.5f;
+    if (__builtin_amdgcn_readfirstlane(steep)) return run(std::true_type{});
+  }
+  run(std::false_type{});
 }
 
 // Along the runs, in place: what each leaves from a zero state -> the state that

@@ -257,7 +257,10 @@ cnhwc_status_t cnhwc_rotary(const cnhwc_rotary_desc_t* desc, const void* x, cons
  * operand of a matrix product is rounded to their type once (the products of q and
  * k under their decays, the state that 32 positions start from) on the way to y and the
  * gradients of q, k and v; on the way to a state and to log_decay's gradient it is taken
- * in as many terms as fp32 has digits. */
+ * in terms: three of bf16, fp32's digits; two of f16 on the way to a state.  f16 has a
+ * narrow range: what is rounded once is off by 2^-12 of itself or 2^-39 of the largest that it
+ * stands beside (a position's products, 16 columns of a state), what is in two terms by
+ * 2^-23 of itself or 2^-50 of the largest of its column in 32 positions. */
 #define CNHWC_LINEAR_ATTENTION_MAX_DIM 256
 
 typedef struct {

@@ -1,5 +1,5 @@
-"""Linear attention's states under decays that leave fp32's ordinary range: infinite states, and growth (log_decay
-> 0) where the states themselves fit float32."""
+"""Linear attention's states under decays that leave fp32's ordinary range: infinite states; growth (log_decay
+> 0) where the states themselves fit float32; and the digits that fast decays leave."""
 import numpy as np
 import pytest
 import torch
@@ -112,3 +112,27 @@ def test_growth_of_a_zero_state_over_a_whole_sequence(dt):
     mag = [t.abs() for t in a[:3]] + a[3:]
     for t, ref, m, units in zip((y, last), A.attention(*a), A.attention(*mag), (OPERAND[dt], 0)):
         R.check(t, ref.cpu(), m.cpu(), 2 * 30 + 512 + units, "growth of 0")
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_digits_of_what_a_fast_decay_leaves(dt):
+    """Keys of one channel each, so that a row of the state is one position's v under its decay,
+    down to e^-31 of the last one's.  In f16, whose products have a narrow range, to 2^-50
+    of the largest of a chunk's column, 2^-39 where the decay across a chunk is slower than 2^-8."""
+    l, h = 32, 5
+    _, _, v, dy = _rows([5], dt, 2, l, h, 32, 40)
+    eye = torch.eye(l, dtype=DT[dt], device="cuda")[None, :, None].expand(2, l, h, l)
+    g = -torch.tensor([0.2, 0.5, 0.7, 1.0, 0.17], device="cuda")
+    least = torch.tensor([2.0 ** -50] * 4 + [2.0 ** -39], device="cuda").double()[:, None, None]
+
+    def check(got, ref):
+        tol = (2 * l + 512) * R.EPS * ref.abs() + 2.0 ** -126
+        if dt == "f16":
+            tol = tol + least * ref.abs().amax(2, keepdim=True)
+        bad = (got.double() - ref).abs() > tol
+        assert not bad.any(), torch.nonzero(bad)[0].tolist()
+    _, last = cn.linear_attention(eye, eye, v, g, return_state=True)
+    a = [A.wide(t) for t in (eye, eye, v, g)] + [1.0]
+    check(last, A.attention(*a, None, None)[1])
+    r = cn.linear_attention_backward(dy, eye, eye, v, g, state=torch.zeros_like(last))  # the gradient: from the end
+    check(r.state, A.attention_backward(A.wide(dy), *a, A.wide(torch.zeros_like(last)), None, None)["state"])
