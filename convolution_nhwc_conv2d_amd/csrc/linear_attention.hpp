@@ -98,20 +98,11 @@ struct Decay {
 // small that they stay within it: past e^88 it is taken in three factors, enough for any
 // two fp32 values (e^-104 to e^88.7), so that 0 stays 0 and nothing is NaN.
 struct RunDecay {
-  bool vast;
-  Decay d;  // or its cube root
+  Decay d;     // or its cube root
+  float more;  // then that again, else 1
   __device__ __forceinline__ explicit RunDecay(float g)
-      : vast(g > 88.0f), d(vast ? (g < 264.0f ? g : 264.0f) * (1.0f / 3.0f) : g) {}
-  __device__ __forceinline__ v4f operator()(v4f x) const {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = d(x[r]);
-    if (__builtin_amdgcn_ballot_w64(vast) != 0) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (vast) x[r] = x[r] * d.m * d.m;
-    }
-    return x;
-  }
+      : d(g > 88.0f ? (g < 264.0f ? g : 264.0f) * (1.0f / 3.0f) : g), more(g > 88.0f ? d.m : 1.0f) {}
+  __device__ __forceinline__ float operator()(float x) const { return d(x) * more * more; }
 };
 
 // Positions that a chunk's products take at a time: all of them, fewer where the state grows
@@ -858,7 +849,7 @@ __global__ __launch_bounds__(256) void la_join_kernel(Passes<DT> passes, LaGeo g
     const float gd = rate(g.log_decay[hd]);
     float4* at = p.kept + nh * slots * per + (id - nh * per);
     constexpr int kAhead = 8;
-    v4f h = {0.0f, 0.0f, 0.0f, 0.0f};
+    float4 h = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int32_t k0 = 0; k0 < slots; k0 += kAhead) {
       float4 v[kAhead];
 #pragma unroll
@@ -871,8 +862,8 @@ __global__ __launch_bounds__(256) void la_join_kernel(Passes<DT> passes, LaGeo g
         const int32_t lo = run * g.run * chunk, hi = (run + 1 == g.runs ? g.chunks : (run + 1) * g.run) * chunk;
         const int32_t valid = (hi < len ? hi : len) - lo;
         const RunDecay d(gd * float(valid < 0 ? 0 : valid));
-        h = d(h) + __builtin_bit_cast(v4f, v[i]);
-        at[int64_t(k0 + i) * per] = __builtin_bit_cast(float4, h);
+        h.x = d(h.x) + v[i].x, h.y = d(h.y) + v[i].y, h.z = d(h.z) + v[i].z, h.w = d(h.w) + v[i].w;
+        at[int64_t(k0 + i) * per] = h;
       }
     }
   }
@@ -1148,10 +1139,12 @@ __global__ __launch_bounds__(256) void la_decay_join_kernel(DecayPass<DT> pass, 
       const int32_t valid = (hi < len ? hi : len) - lo;
       const float count = float(valid < 0 ? 0 : valid);
       const RunDecay d(gd * count);
+      const v4f s = __builtin_bit_cast(v4f, at[0]), grow = __builtin_bit_cast(v4f, at[64]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) t[r] = __builtin_fmaf(count, h[r], t[r]);
-      t = d(t) + __builtin_bit_cast(v4f, at[64]);
-      h = d(h) + __builtin_bit_cast(v4f, at[0]);
+      for (int r = 0; r < 4; ++r) {
+        t[r] = d(__builtin_fmaf(count, h[r], t[r])) + grow[r];
+        h[r] = d(h[r]) + s[r];
+      }
       at[0] = __builtin_bit_cast(float4, h);
       at[64] = __builtin_bit_cast(float4, t);
     }
