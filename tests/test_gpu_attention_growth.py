@@ -115,6 +115,48 @@ def test_growth_of_a_zero_state_over_a_whole_sequence(dt):
 
 
 @pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("place", [0, 4, 5])
+def test_growth_of_ragged_sequences(place, dt):
+    """Steps of a few positions, in both directions, with lengths that end inside and on them, states
+    from outside, rows behind the lengths, and rows off 16 bytes."""
+    n, l, h, dk, dv = 4, 70, 3, 48, 40
+    growth = torch.tensor([3.0, 0.7, -1.0], device="cuda")
+    lengths = torch.tensor([20, 7, 0, 16], dtype=torch.int32, device="cuda")
+    scale = 2.0 ** -86  # e^-60
+    q, k, v, dy = _rows([6], dt, n, l, h, dk, dv)[:3] + (_rows([7], dt, n, l, h, dk, dv)[3],)
+
+    def placed(t):
+        buf = torch.full((n, l, h * t.shape[-1] + 12), float("nan"), dtype=t.dtype, device="cuda")
+        x = buf[..., place:place + h * t.shape[-1]].unflatten(-1, (h, t.shape[-1]))
+        x.copy_(t)
+        for j, m in enumerate(lengths.tolist()):
+            x[j, m:] = float("nan")
+        return x
+    q, k, v, dy = (placed(t) for t in (q, k, v, dy))
+    g = np.random.default_rng(8)
+    state, dstate = R.rand(g, n, h, dk, dv).cuda(), R.rand(g, n, h, dk, dv).cuda() * scale
+    y, last = cn.linear_attention(q, k, v, growth, scale=scale, state=state, lengths=lengths, return_state=True)
+    r = cn.linear_attention_backward(dy, q, k, v, growth, scale=scale, state=state, lengths=lengths, dstate=dstate,
+                                     decay_grad=True)
+    q, k, v, dy = (torch.nan_to_num(t) for t in (q, k, v, dy))
+    a = [A.wide(t) for t in (q, k, v, growth)] + [scale, A.wide(state), lengths]
+    mag = A.absolute(*a)
+    mag[3] = a[3]
+    want, size = A.attention(*a), A.attention(*mag)
+    back = A.attention_backward(A.wide(dy), *a, A.wide(dstate))
+    bsize = A.attention_backward(A.wide(dy).abs(), *mag, A.wide(dstate).abs())
+    units = 2 * l + 512 + 2 * 3 * 20  # and the exponents' roundings, as in _growing
+    for name, got, ref, m in [("y", y, want[0], size[0]), ("last", last, want[1], size[1])] + [
+            (x, getattr(r, x), back[x], bsize[x]) for x in ("q", "k", "v", "log_decay", "state")]:
+        more = n * l if name == "log_decay" else 0 if name in ("last", "state") else OPERAND[dt]
+        R.check(got, ref.cpu(), m.cpu(), units + more, f"{name} {place}")
+        if name in ("y", "q", "k", "v"):
+            for j, x in enumerate(lengths.tolist()):
+                assert not got[j, x:].any()
+    assert torch.equal(last[2], state[2]) and torch.equal(r.state[2], dstate[2])
+
+
+@pytest.mark.parametrize("dt", list(DT))
 def test_digits_of_what_a_fast_decay_leaves(dt):
     """Keys of one channel each, so that a row of the state is one position's v under its decay,
     down to e^-31 of the last one's.  In f16, whose products have a narrow range, to 2^-50
