@@ -24,7 +24,9 @@ namespace {
 // four columns, 16 row groups of NI consecutive rows.  The state is the traffic, read
 // once and written once: VEC with whole vectors of it, and of q and k, whose elements
 // one by one are as many loads as the state's vectors (64 x 16 x 128 x 128 bf16: single elements of
-// all 51 us, whole vectors of the state 33, of q and k too 29, 4.7 TB/s: memory).
+// all 51 us, whole vectors of the state 33, of q and k too 29, 4.6 TB/s: memory).  That is for DK
+// of 32, 64, 128 and 256; any other goes by single elements: 80 x 80 25 us for 10.5 at 5 TB/s, 96 x 96 29
+// for 15, 192 x 192 133 for 60.
 template <int DT, int NI, bool VEC>
 __global__ __launch_bounds__(256) void la_step_kernel(Pass<DT> p, LaGeo g) {
   __shared__ float part[4][64];

@@ -18,13 +18,20 @@
 // cut into runs: one kernel takes the state that each leaves from a zero state, one joins
 // these, and one takes the outputs.
 //
-// Measured, bf16, 16 heads of 128 x 128.  1 x 16384: 120 us, of which the states of 32 runs
-// 41, the join 15, the outputs 69; k and v are read twice and the states between runs
-// written and read twice, 535 MB, at 4.5 TB/s.  8 x 2048 backward, three passes in one
-// launch of 384 workgroups: 208 us; the vector pipes are busy for 34% of it, the matrix pipes 22%,
-// the LDS 29%, and the rest is waiting: what a chunk does follows what the one before left
+// 16-bit types round two operands to themselves once, on the way to y (dq, dk, dv): the
+// products of q and k under their decays, and the state that enters.  With the rounding of y
+// itself that is 0.00235 of y's norm in bf16 and 0.00029 in f16, where y's alone is 0.00166 and
+// 0.00021.  Both in two terms would leave that alone, and take bf16 1 x 16384 from 121 us to
+// 136, 8 x 2048 114 to 124, its backward 202 to 243, f16 147 to 157, 131 to 139, 270 to 295 (16 heads of
+// 128 x 128): not worth it for what is stored in 16 bits.  The state and its sums keep fp32's.
+//
+// Measured, bf16, 16 heads of 128 x 128.  1 x 16384: 118 us; on a trace, whose clocks are lower,
+// the states of 32 runs 42, the join 15, the outputs 68; k and v are read twice and the states
+// between runs written and read twice, 535 MB, at 4.5 TB/s.  8 x 2048 backward, three passes in
+// one launch of 384 workgroups: 203 us; the vector pipes are busy for 35% of it, the matrix pipes
+// 22%, the LDS 29%, and the rest is waiting: what a chunk does follows what the one before left
 // (barriers, the state), two workgroups on half of the compute units and one on the others.
-// f16 148 and 270, fp32 (matrix instructions of 154 TFLOP/s) 300 and 676.
+// f16 138 and 271, fp32 (matrix instructions of 154 TFLOP/s) 298 and 637.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -881,11 +888,12 @@ __global__ __launch_bounds__(256) void la_join_kernel(Passes<DT> passes, LaGeo g
 // workgroup holds 64 columns of both states; S, T and the decayed v are taken in all
 // their terms, so nothing is rounded below fp32.
 //
-// 8 x 2048 x 16 heads x 128 x 128 bf16: 172 us, vector pipes 55% (the terms), matrix pipes
-// 29%, LDS 27%; one workgroup of eight wavefronts a compute unit, whose registers are the two
-// states.  Chunks of 32 with three of four: 10% more for the whole backward pass.  f16 in
-// fp32 takes 390 us: its two terms, brought into range by rows and columns, would need ranges
-// of S, T and both decayed v.
+// 8 x 2048 x 16 heads x 128 x 128 bf16: 178 us on a trace, 156 more for the call; vector pipes 56%
+// (the terms), matrix pipes 29%, LDS 26%; one workgroup of eight wavefronts a compute unit, whose
+// registers are the two states.  Chunks of 32 with three of four: 10% more for the whole backward
+// pass.  f16 goes in fp32, 412 us more: in two f16 terms S, T and both decayed v would each need
+// a range.  (An f16 value is two bf16 terms; with three of the states' that would be
+// five products of 16 cycles for the 256 of the fp32 instructions.  Not tried.)
 template <int DT>
 struct DecayPass {
   Pass<DT> a;               // q, k, v, the initial state; y, state_out unused

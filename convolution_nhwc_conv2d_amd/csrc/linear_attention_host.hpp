@@ -9,11 +9,12 @@ namespace seq {
 
 // The form of a pass: 16-row tiles of a state, wavefronts of a workgroup, 16 columns each.
 // Eight where there are columns for them, since each workgroup takes up all of k and q and
-// their products (bf16, 16 heads of 128 x 128: 1 x 16384 131 us, with four 165; 8 x 2048 126, 169; backward
-// 225, 287; f16 282, 320).  fp32, where the matrix instructions weigh more than what they are fed
-// from, has four (narrow) where half as many columns even out the workgroups, from 128 of eight
-// wavefronts on: 8 x 2048 293 us, with four 266, backward 752, 660; but with 16 of them 313, 349, with
-// 64 (4 x 4096 x 16 x 100 x 80) 296, 310, and with 256 rows 280, 349.
+// their products (16 heads of 128 x 128, bf16: 1 x 16384 122 us, with four 129; 8 x 2048 109, 121; backward
+// 202, 213; f16 138, 158; 128, 158; but backward 271, 259).  fp32, where the matrix instructions weigh
+// more than what they are fed from, has four (narrow) where half as many columns even out the
+// workgroups, from 128 of eight wavefronts on: 8 x 2048 293 us, with four 257, backward 757, 638; but
+// with 16 of them (1 x 16384) 298, 310, with 64 (4 x 4096 x 16 x 100 x 80) 298, 312, and with 256 rows 2 x 4096 x 8
+// 282, 355, 8 x 2048 x 16 695, 959.
 template <typename F>
 void with_shape(int32_t dk, int32_t dv, bool narrow, F&& f) {
   auto wide = [&](auto dkt) {
@@ -36,13 +37,13 @@ struct Cut {
 };
 // More than one run costs a kernel over k and v, about 0.6 of the other one, and the
 // states between them: worth it up to five workgroups for eight compute units.
-// Measured (128 x 128 bf16, 2048 positions): 256 workgroups in one run 142 us, in two 180; 192
-// 133 and 160; 128 in four 111, in two 120, fp32 in one 376, in two 290; 64 x 64, 4096
-// positions, 64 workgroups in eight 57, in four 76.  At least three chunks to a run, fewer only
-// while every run has a compute unit to itself (1 x 300 x 4 heads of 64 x 64 one chunk 15 us, three
-// 19; 3 x 591 x 96 x 100 fp32 25, 46, its decay's gradient 48 us less; 2 x 1000 x 8 heads of 64 x 128 two
-// 25, three 25, one 32, fp32 29, 35, 35; but 1 x 4096 x 8 x 128 x 128 two 48, three 38), and one run up
-// to `few` chunks, whose time the two other kernels would not save.
+// Measured (128 x 128 bf16, 2048 positions): 256 workgroups in one run 155 us, in two 181; 192
+// 151 and 155; 128 in four 109, in two 125, in one 150, fp32 in two 293, in one 382; 64 x 64, 4096
+// positions, 64 workgroups in eight 58, in four 81.  At least three chunks to a run, fewer only
+// while every run has a compute unit to itself (1 x 300 x 4 heads of 64 x 64 one chunk 16 us, three
+// 18; 3 x 591 x 96 x 100 fp32 26, 39, backward with the decay's gradient 65, 109; 2 x 1000 x 8 heads of
+// 64 x 128 two 26, three 25, one 33, fp32 30, 32, 36; but 1 x 4096 x 8 x 128 x 128 two 49, three 44, four
+// 39), and one run up to `few` chunks, whose time the two other kernels would not save.
 inline void cut_runs(Cut& c, int64_t l, int64_t all, int64_t room, int64_t few) {
   c.chunks = int32_t((l + c.chunk - 1) / c.chunk);
   int64_t runs = all > 160 ? 1 : room / all;
@@ -63,8 +64,8 @@ Cut cut_of(const cnhwc_linear_attention_desc_t& d, int32_t dk, int32_t dv, int64
     c.chunk = Sh::kChunk;
     c.parts = (dv + Sh::kCols - 1) / Sh::kCols;
     c.per = c.parts * W * DKT * 64;
-    // a chunk in fp32 takes longer: 1 x 128 x 4 heads of 128 x 128 in four runs 20 us, in one 28, 64 x 64 15
-    // and 14, 32 x 32 14 and 11; 2 x 130 x 8 of 64 x 96 in five 18, in one 23
+    // a chunk in fp32 takes longer: 1 x 128 x 4 heads of 128 x 128 in four runs 21 us, in one 29, 64 x 64 15
+    // and 14, 32 x 32 14 and 11; 2 x 130 x 8 of 64 x 96 in five 19, in one 23
     const int few = DT == CNHWC_F32 && DKT * W > 16 ? 3 : 5;
     cut_runs(c, d.l, d.n * d.h * c.parts * passes, 256 * Sh::kGroups, few);
   });

@@ -19,8 +19,9 @@
 // the largest tile are read again from the cache.
 //
 // Bound by memory: 4 x 4096 x 4096 bf16 with the residual 99 us (5.4 TB/s), the same in 8
-// bits by groups of 128 93 us (5.1 TB/s), 8 x 2048 x 2048 backward 54 us (5.0 TB/s); a
-// token's row by its launch (kernel 2.3 us).
+// bits by groups of 128 93 us (5.1 TB/s), 8 x 2048 x 2048 backward 56 us (4.8 TB/s); a
+// token's row by its launch (kernel 2.1 us).  Rows off 16 bytes by their single elements:
+// 16384 x 613 bf16 with the residual 36 us (2.2 TB/s), in 8 bits 43, backward 29.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -496,7 +497,7 @@ hipError_t rms_fwd_t(const RmsGeo& g, const RmsFwd<DT>& io, hipStream_t st) {
 // 512, 768 and 1024: one vector to a thread, 16384 x 2048 bf16 54, 55, 58 us (256: 86), 65536 x 512
 // 49, 53, 54, 16384 x 1024 f32 50, 52, 54; two, 16384 x 4096 bf16 111, 109, 114, 8192 x 2424 f16 50, 43,
 // 42; four, 8192 x 8192 bf16 117, 139, 132; elements, 16384 x 613 40, 32, 28; a workgroup of more than
-// 256 threads, 2048 x 16384 80 each, 64 with 256.
+// 256 threads, 2048 x 16384 80 each, 64 with 256 (one sweep).
 int64_t bwd_groups(const cnhwc_rms_norm_desc_t& d, bool vec) {
   const int64_t rows = d.n * d.l;
   const int64_t ve = vec ? 16 / int64_t(dtype_size(d.dtype)) : 1;
