@@ -478,6 +478,8 @@ struct Work {
   }
 };
 
+constexpr float kHigher = 0x1p11f;  // of STEEP's second term
+
 // What a workgroup does.  LOCAL: the state that a run of chunks leaves from a zero state
 // (the first run: from the initial one), for all runs but the last.  Otherwise y and
 // the final state.
@@ -487,7 +489,6 @@ struct Work {
 // is 0.  Where a chunk's decay is faster than 2^-8 that term stands 2^11 higher, in an
 // accumulator of its own: digits down to 2^-27, 0 below 2^-50.  (For every head 8 x 2048 x 16 x
 // 128 x 128 takes 139 us for 132, its backward 277 for 269.)
-constexpr float kHigher = 0x1p11f;
 template <int DT, int DKT, int W, bool LOCAL, bool VEC, bool BACK, bool STEEP>
 __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, const Work& w, char* lds,
                                           Powers<ChunkShape<DT, DKT, W>::kChunk>& power) {
@@ -538,6 +539,7 @@ __device__ __forceinline__ void la_chunks(const Pass<DT>& p, const LaGeo& g, con
 
   power.fill(gd, p.scale_k, BACK, len < stride ? len : stride);
   const Decay full(gd * float(stride));
+
   const Elem<DT>* const qn = LOCAL ? nullptr : p.q + n * p.qs[0] + hd * p.qs[2];
   const Elem<DT>* const kn = p.k + n * p.ks[0] + hd * p.ks[2];
   const Elem<DT>* const vn = p.v + n * p.vs[0] + hd * p.vs[2] + col0;

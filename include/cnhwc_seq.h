@@ -248,7 +248,8 @@ cnhwc_status_t cnhwc_rotary(const cnhwc_rotary_desc_t* desc, const void* x, cons
  * for each head; the state S is fp32 [N,H,DK,DV].  Decays are meant (log_decay <= 0,
  * minus infinity included).  Growth is taken where exp(log_decay) and every state fit
  * fp32 (a state of 0 stays 0 however long), for values and products of q and k up to 1e19;
- * it runs in smaller steps, slower, from exp(1.3) a position on, in f16 from exp(0.25).  An
+ * it runs in smaller steps, slower, from exp(1.3) a position on (exp(0.6) in log_decay's
+ * gradient), in f16 from exp(0.25).  An
  * infinity or NaN in v reaches, as NaN, the y of its channel from its position on.
  * Heads may be shared through strides of 0; gradients are those of each head.  N * H
  * above 2^20 and L above 2^30 are UNSUPPORTED.
@@ -258,9 +259,10 @@ cnhwc_status_t cnhwc_rotary(const cnhwc_rotary_desc_t* desc, const void* x, cons
  * k under their decays, the state that 32 positions start from) on the way to y and the
  * gradients of q, k and v; on the way to a state and to log_decay's gradient it is taken
  * in terms: three of bf16, fp32's digits; two of f16 on the way to a state.  f16 has a
- * narrow range: what is rounded once is off by 2^-12 of itself or 2^-39 of the largest that it
- * stands beside (a position's products, 16 columns of a state), what is in two terms by
- * 2^-23 of itself or 2^-50 of the largest of its column in 32 positions. */
+ * narrow range: what is rounded once is off by 2^-11 of itself or 2^-39 of the largest that it
+ * stands beside (a position's products, 16 columns of a state), what is in two terms by 2^-22
+ * of itself or 2^-39 of the largest of its column in 32 positions (2^-50 where log_decay * 32
+ * is beyond 5.5 either way). */
 #define CNHWC_LINEAR_ATTENTION_MAX_DIM 256
 
 typedef struct {
